@@ -52,7 +52,7 @@ def listed():
         _shared("shared-f16-7b", "f16", 16, 32, 128, 1536, 8192, 65, 512, weights=True),
         # bf16, an odd prefix, answers about as long as half of it
         _shared("shared-bf16-odd", "bf16", 24, 32, 128, 1536, 2001, 0, 1000),
-        # a quantised cache: 32 requests over a prompt of 4096 tokens
+        # a bf16 layer with a quantised cache: 32 requests over a prompt of 4096 tokens
         _shared("shared-int8", "i8", 32, 32, 128, 768, 4096, 1, 256),
         # the largest batch over the longest prompt
         _shared("shared-f16-large", "f16", 64, 32, 128, 1536, 16384, 128, 1024),
@@ -60,7 +60,7 @@ def listed():
         _weights("weights-bf16-short", "bf16", 3, 8, 64, 256, 0, 700, add=True),
         # the 7B layer at full batch and length
         _weights("weights-f16-7b", "f16", 16, 32, 128, 1536, 8192, 8192),
-        # the quantised layer, long and ragged
+        # the same layer alone, long and ragged
         _weights("weights-int8-long", "i8", 32, 32, 128, 768, 4000, 16384),
         # rotary keys, ragged
         _weights("weights-bf16-rope", "bf16", 4, 32, 128, 1536, 1000, 4096, rope=True),
@@ -113,6 +113,11 @@ def _max_len(case):
     return case["hi"] + 8   # room for the next tokens
 
 
+def _weight(case):
+    """The weights' and outputs' type: the cache's, bf16 beside a quantised one."""
+    return "bf16" if case["cache"] == "i8" else case["cache"]
+
+
 def _rows(g, n, r, cache, spectrum):
     """n latent rows with falling channel magnitudes, as the cache holds them: (rows or int8 codes, group scales)."""
     x = torch.randn(n, r, generator=g, device=DEV) * spectrum
@@ -148,7 +153,7 @@ def prepare(case, seed):
     else:
         H, d_h = case["H"], case["d_h"]
         E = H * d_h
-        wt = F16["f16" if case["cache"] == "i8" else case["cache"]]
+        wt = F16[_weight(case)]
         # queries and keys of unit variance per channel; queries twice that, so that scores spread over some units
         up = lambda scale: (torch.randn(r, E, generator=g, device=DEV) * (scale / math.sqrt(r))).to(wt)  # noqa: E731
         s["wuq"], s["wuk"], s["wuv"] = up(2.0), up(1.0), up(1.0)
@@ -170,7 +175,7 @@ def _prepare_own(s):
         s["dims"] = q.make_dims(64, 1, 64, c["r"], c["B"], _max_len(c), cache=c["cache"])
         s["workspace"] = torch.empty(q.evict_workspace_bytes(s["dims"], c["budget"]), dtype=torch.uint8, device=DEV)
         return
-    wt = "f16" if c["cache"] == "i8" else c["cache"]
+    wt = _weight(c)
     d = s["dims"] = q.make_dims(c["H"] * c["d_h"], c["H"], c["d_h"], c["r"], c["B"], _max_len(c), cache=c["cache"],
                                 weight=wt, out=wt, rope=c.get("rope", False))
     wd = torch.zeros(d.E, d.r, dtype=s["wuq"].dtype, device=DEV)   # not used by a decode step

@@ -472,6 +472,68 @@ qsvd_status qsvd_decode_attn_per_head(const qsvd_dims* dims, const void* bk, con
 qsvd_status qsvd_prepare_per_head_fold(const qsvd_dims* dims, const void* bv, const void* wo, void* f,
                                        void* stream);
 
+/*
+ * qsvd_decode_attn_weights -- qsvd_decode_attn that also gives each cache
+ * row's attention weight, summed over the heads:
+ *   weights[b][t] = (accumulate ? weights[b][t] : 0) + sum_h p_{b,h,t},  t < len_b
+ * with p the step's softmax probabilities; entries t >= len_b are left as
+ * they were.  Summed over steps (accumulate != 0) it is what decides which
+ * rows qsvd_evict_rows keeps.  The output is that of qsvd_decode_attn.
+ * Serving decode; the pages have no counterpart.
+ *   weights    device, B x max_len float32, 4-byte aligned.
+ *   workspace  as in qsvd_decode_attn, with room for the step's scores
+ *              (B x H x max_len float32 more in absorbed mode); query its size
+ *              with this call.
+ * Every other argument, limit, status bit and error as in qsvd_decode_attn
+ * (all phases).  The weights are sums of float32 terms in head order: the
+ * same inputs and num_splits give the same bits.
+ */
+qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, const float* qin,
+                                     int qin_is_latent, const void* cache, const void* scales,
+                                     const int32_t* lengths, int num_splits, void* workspace,
+                                     size_t* workspace_bytes, void* out, float* weights,
+                                     int accumulate, void* stream);
+
+/*
+ * qsvd_evict_rows -- cut each sequence's cache to at most `budget` rows by
+ * accumulated attention weight (see qsvd_decode_attn_weights).  A sequence
+ * with n = lengths[b] > budget keeps its first `sink` rows, its last `recent`
+ * rows and the budget - sink - recent heaviest of those between: equal
+ * weights, the lower row first; -0 equals 0; a NaN weighs less than any
+ * number.  Other sequences keep every row.  The kept rows stay in order and
+ * become rows 0 .. m - 1 (m = min(n, budget)) of the destination; with rotary
+ * embedding a decode then places each at its new row.
+ * Serving decode; the pages have no counterpart.
+ *   weights      device, B x max_len float32 (rows t < lengths[b] are read).
+ *   lengths      device, B int32, clamped to [0, max_len] and flagged
+ *                (QSVD_STATUS_LEN_CLAMPED).
+ *   budget       1 .. max_len; sink, recent >= 0, sink + recent <= budget.
+ *   cache, scales  as in qsvd_append_latent.
+ *   dst_max_len  rows per sequence of the destination, >= budget.
+ *   dst_cache    device, B x dst_max_len rows: rows 0 .. m - 1 are written,
+ *                the others left as they were.  Either `cache` itself (in
+ *                place; dst_max_len == max_len) or memory that shares no byte
+ *                with it; so, each with its own source, for dst_scales,
+ *                dst_weights and dst_lengths.
+ *   dst_scales   the rows' scales (I8/I4 caches only; else NULL).
+ *   dst_weights  device, B x dst_max_len float32, or NULL: the kept rows'
+ *                weights, then zeros up to dst_max_len.
+ *   dst_lengths  device, B int32: m.
+ *   kept         device, B x budget int32, or NULL: the source row of each
+ *                kept row, then -1.
+ *   status       device int32 word or NULL; bits QSVD_STATUS_* are OR-ed in.
+ *   workspace    device scratch, 16-byte aligned, or NULL to query its size
+ *                (of dims and budget) into *workspace_bytes (in: capacity).
+ * Of dims it uses r, batch, max_len, group and cache_dtype.  Stream-ordered;
+ * nothing is allocated.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+qsvd_status qsvd_evict_rows(const qsvd_dims* dims, const float* weights, const int32_t* lengths,
+                            int budget, int sink, int recent, const void* cache,
+                            const void* scales, int dst_max_len, void* dst_cache,
+                            void* dst_scales, float* dst_weights, int32_t* dst_lengths,
+                            int32_t* kept, int32_t* status, void* workspace,
+                            size_t* workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* qsvd_status_string(qsvd_status s);
 

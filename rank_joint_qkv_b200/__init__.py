@@ -69,6 +69,10 @@ _sigs = {
     "qsvd_prefill_attention": [_D, _P, _P, _P, _P, _SZ, _P, _P, _P],
     "qsvd_prepare_per_head_fold": [_D, _P, _P, _P, _P],
     "qsvd_beta_exponents": [_P, ctypes.c_int, ctypes.c_double, _P, _P, _P],
+    "qsvd_decode_attn_weights": [_D, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P, _SZ, _P, _P,
+                                 ctypes.c_int, _P],
+    "qsvd_evict_rows": [_D, _P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P,
+                        _P, _P, _P, _P, _SZ, _P],
     "qsvd_sq_diff_sum": [_P, _P, ctypes.c_int64, _P, _P],
 }
 for _name, _args in _sigs.items():
@@ -306,6 +310,64 @@ def qsvd_combine_splits(dims: qsvd_dims, packed, workspace, num_splits, lengths,
     _check(_lib.qsvd_combine_splits(ctypes.byref(dims), _ptr(packed), _ptr(workspace),
                                     int(num_splits), _ptr(lengths), _ptr(out), _stream(stream)),
            "qsvd_combine_splits")
+
+
+def decode_weights_workspace_bytes(dims: qsvd_dims, num_splits: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.qsvd_decode_attn_weights(ctypes.byref(dims), None, None, 1, None, None, None, int(num_splits), None,
+                                         ctypes.byref(n), None, None, 0, None),
+           "qsvd_decode_attn_weights(size)")
+    return n.value
+
+
+def qsvd_decode_attn_weights(dims: qsvd_dims, packed, qin, qin_is_latent, cache, scales, lengths, out, weights,
+                             accumulate=True, num_splits=0, workspace=None, stream=None):
+    """qsvd_decode_attn that also gives each cache row's attention weight,
+    summed over the heads, in ``weights`` (B x max_len float32; added to what
+    is there with ``accumulate``).  Returns the workspace."""
+    if workspace is None:
+        workspace = _empty_bytes(decode_weights_workspace_bytes(dims, num_splits), cache.device)
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    _check(_lib.qsvd_decode_attn_weights(ctypes.byref(dims), _ptr(packed), _ptr(qin), int(bool(qin_is_latent)),
+                                         _ptr(cache), _ptr(scales), _ptr(lengths), int(num_splits), _ptr(workspace),
+                                         ctypes.byref(n), _ptr(out), _ptr(weights), int(bool(accumulate)),
+                                         _stream(stream)),
+           "qsvd_decode_attn_weights")
+    return workspace
+
+
+def evict_workspace_bytes(dims: qsvd_dims, budget: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.qsvd_evict_rows(ctypes.byref(dims), None, None, int(budget), 0, 0, None, None, 0, None, None, None,
+                                None, None, None, None, ctypes.byref(n), None),
+           "qsvd_evict_rows(size)")
+    return n.value
+
+
+def qsvd_evict_rows(dims: qsvd_dims, weights, lengths, budget, cache, scales=None, *, sink=0, recent=0,
+                    dst_max_len=None, dst_cache=None, dst_scales=None, dst_weights=None, dst_lengths=None, kept=None,
+                    status=None, workspace=None, stream=None):
+    """Cut each sequence's cache to at most ``budget`` rows: the first
+    ``sink``, the last ``recent`` and the heaviest of the others by
+    ``weights`` (B x max_len float32), in order.  Without ``dst_cache`` the
+    cut is in place: cache, scales, weights and lengths are all updated.
+    With it (B x dst_max_len rows; dst_scales beside int caches) the sources
+    are left alone; dst_weights (B x dst_max_len) is optional, dst_lengths
+    is not.  ``kept``: optional B x budget int32, the kept rows' sources.
+    Returns the workspace."""
+    if dst_cache is None:
+        dst_cache, dst_scales, dst_max_len = cache, scales, dims.max_len
+        dst_weights = weights if dst_weights is None else dst_weights
+        dst_lengths = lengths if dst_lengths is None else dst_lengths
+    if workspace is None:
+        workspace = _empty_bytes(evict_workspace_bytes(dims, budget), cache.device)
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    _check(_lib.qsvd_evict_rows(ctypes.byref(dims), _ptr(weights), _ptr(lengths), int(budget), int(sink), int(recent),
+                                _ptr(cache), _ptr(scales), int(dims.max_len if dst_max_len is None else dst_max_len),
+                                _ptr(dst_cache), _ptr(dst_scales), _ptr(dst_weights), _ptr(dst_lengths), _ptr(kept),
+                                _ptr(status), _ptr(workspace), ctypes.byref(n), _stream(stream)),
+           "qsvd_evict_rows")
+    return workspace
 
 
 def status_word(workspace: torch.Tensor) -> int:

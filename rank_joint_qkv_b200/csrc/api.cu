@@ -346,11 +346,18 @@ static float* quant_query_scales(const qsvd_dims& d, void* qt16) {
   return reinterpret_cast<float*>(static_cast<uint8_t*>(qt16) + size_t(3) * d.batch * d.H * d.r);
 }
 
+// What a decode step yields beside its output.
+struct DecodeExtra {
+  bool keep_scores = false;    // the workspace has room for the scores
+  float* weights = nullptr;    // B x max_len: the rows' attention weights ...
+  int add = 0;                 // ... added to what is there
+};
+
 static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const float* qin,
                                int qin_is_latent, const void* cache, const void* scales,
                                const int32_t* lengths, int num_splits, void* workspace,
                                size_t* workspace_bytes, void* out, unsigned phases,
-                               cudaStream_t s) {
+                               cudaStream_t s, const DecodeExtra& x = DecodeExtra()) {
   if (phases == 0) phases = QSVD_PHASE_ALL;
   constexpr unsigned kSub = QSVD_PHASE_SPLIT_SCORES | QSVD_PHASE_SPLIT_ACCUM;
   if (phases & ~(QSVD_PHASE_ALL | kSub)) return fail(QSVD_ERR_INVALID_ARG, "unknown phase bits");
@@ -377,7 +384,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   int G = 0;
   qsvd_status st = resolve_splits(d, num_splits, kernel, &G);
   if (st != QSVD_OK) return st;
-  const WsLayout W = ws_layout(d, G);
+  const WsLayout W = ws_layout(d, G, x.keep_scores);
   if (!workspace) { *workspace_bytes = W.total; return QSVD_OK; }
   if (*workspace_bytes < W.total)
     return fail(QSVD_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", *workspace_bytes, W.total);
@@ -407,6 +414,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   float* opart = reinterpret_cast<float*>(Wb + W.opart);
   const float* rope_tab = reinterpret_cast<const float*>(P + L.rope);
   const float sl2 = score_scale_log2(d);
+  float* scores = reinterpret_cast<float*>(Wb + W.scores);
+  float* keep = x.weights ? scores : nullptr;
   cudaError_t e;
 
   if (phases & QSVD_PHASE_PROLOGUE) {
@@ -440,7 +449,6 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   }
   if (split_any) {
     if (d.rope && kernel == QSVD_KERNEL_TCGEN05_CTA) {
-      float* scores = reinterpret_cast<float*>(Wb + W.scores);
       const int sms = device_sms();
       e = cudaSuccess;
       if (phases & QSVD_PHASE_SPLIT_SCORES)
@@ -451,16 +459,19 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
                 ? launch_split_tc_scores(d, scores, cache, sched, G, pm, pl, pz, &hdr->status, s)
                 : launch_split_simt_scores(d, scores, cache, scales, sched, G, pm, pl, pz, s);
     } else if (d.rope) {
-      e = launch_split_simt_rope(d, qt32, P + L.wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
+      e = launch_split_simt_rope(d, qt32, P + L.wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s,
+                                 keep);
     }
     else if (kernel == QSVD_KERNEL_TCGEN05_CLUSTER)
-      e = launch_split_cl(d, cache, qt16, sched, G, pm, pl, pz, &hdr->status, s);
+      e = launch_split_cl(d, cache, qt16, sched, G, pm, pl, pz, &hdr->status, s, keep);
     else if (kernel == QSVD_KERNEL_TCGEN05_CTA)
       e = launch_split_tc(d, cache, scales, qt16, sched, G, pm, pl, pz, &hdr->status, s,
-                          quant_query_scales(d, qt16));
+                          quant_query_scales(d, qt16), keep);
     else
-      e = launch_split_simt_absorbed(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
+      e = launch_split_simt_absorbed(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
     if (e != cudaSuccess) return cuda_fail(e, "split phase");
+    if (x.weights && (e = launch_row_weights(d, hdr, sched, pm, pl, nullptr, scores, x.weights, x.add, s)) != cudaSuccess)
+      return cuda_fail(e, "attention weights");
   }
   if (phases & QSVD_PHASE_COMBINE) {
     if (combine_uses_gemv(d)) {
@@ -488,6 +499,78 @@ qsvd_status qsvd_decode_attn(const qsvd_dims* dims, const void* packed, const fl
   if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
   return decode_impl(*dims, packed, qin, qin_is_latent, cache, scales, lengths, num_splits,
                      workspace, workspace_bytes, out, phases, static_cast<cudaStream_t>(stream));
+}
+
+qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, const float* qin,
+                                     int qin_is_latent, const void* cache, const void* scales,
+                                     const int32_t* lengths, int num_splits, void* workspace,
+                                     size_t* workspace_bytes, void* out, float* weights, int accumulate,
+                                     void* stream) {
+  qsvd_status st = validate(dims);
+  if (st != QSVD_OK) return st;
+  if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
+  if (workspace && (!weights || !aligned4(weights)))
+    return fail(QSVD_ERR_INVALID_ARG, "weights must be given, 4-byte aligned");
+  DecodeExtra x;
+  x.keep_scores = true;
+  x.weights = weights;
+  x.add = accumulate != 0;
+  return decode_impl(*dims, packed, qin, qin_is_latent, cache, scales, lengths, num_splits, workspace,
+                     workspace_bytes, out, QSVD_PHASE_ALL, static_cast<cudaStream_t>(stream), x);
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+qsvd_status qsvd_evict_rows(const qsvd_dims* dims, const float* weights, const int32_t* lengths, int budget, int sink,
+                            int recent, const void* cache, const void* scales, int dst_max_len, void* dst_cache,
+                            void* dst_scales, float* dst_weights, int32_t* dst_lengths, int32_t* kept,
+                            int32_t* status, void* workspace, size_t* workspace_bytes, void* stream) {
+  qsvd_status st = validate(dims);
+  if (st != QSVD_OK) return st;
+  const qsvd_dims& d = *dims;
+  if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
+  if (budget < 1 || budget > d.max_len)
+    return fail(QSVD_ERR_INVALID_ARG, "budget (%d) must be in [1, max_len = %d]", budget, d.max_len);
+  const size_t B = size_t(d.batch), src_bytes = align256(B * budget * 4), need = src_bytes + align256(B * 4);
+  if (!workspace) { *workspace_bytes = need; return QSVD_OK; }
+  if (sink < 0 || recent < 0 || (long long)sink + recent > budget)
+    return fail(QSVD_ERR_INVALID_ARG, "sink (%d) and recent (%d) must be >= 0 and within the budget (%d)", sink, recent,
+                budget);
+  if (dst_max_len < budget || (long long)d.batch * dst_max_len > 0x7FFFFFFFLL)
+    return fail(QSVD_ERR_INVALID_ARG, "dst_max_len (%d) must be at least the budget (%d), batch x dst_max_len below 2^31",
+                dst_max_len, budget);
+  if (*workspace_bytes < need)
+    return fail(QSVD_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", *workspace_bytes, need);
+  if (!weights || !lengths || !cache || !dst_cache || !dst_lengths)
+    return fail(QSVD_ERR_INVALID_ARG, "a required pointer is NULL");
+  const bool q = cache_is_int(d);
+  if (q && (!scales || !dst_scales)) return fail(QSVD_ERR_INVALID_ARG, "int caches need scales and dst_scales");
+  if (!aligned16(workspace) || !aligned16(cache) || !aligned16(dst_cache))
+    return fail(QSVD_ERR_INVALID_ARG, "workspace, cache and dst_cache must be 16-byte aligned");
+  if ((q && (!aligned2(scales) || !aligned2(dst_scales))) || !aligned4(weights) || !aligned4(lengths) ||
+      !aligned4(dst_lengths) || (dst_weights && !aligned4(dst_weights)) || (kept && !aligned4(kept)))
+    return fail(QSVD_ERR_INVALID_ARG, "scales must be 2-byte, weights, lengths and kept 4-byte aligned");
+  // a destination is its source (in place) or shares no byte with it
+  const size_t rows = B * d.max_len, drows = B * dst_max_len, rb = cache_row_bytes(d), sb = q ? size_t(d.r / d.group) * 2 : 0;
+  const bool same = dst_max_len == d.max_len;
+  auto clash = [&](const void* a, void* b, size_t unit) {
+    return b && (a == b ? !same : overlap(a, rows * unit, b, drows * unit));
+  };
+  if (clash(cache, dst_cache, rb) || (q && clash(scales, dst_scales, sb)) || clash(weights, dst_weights, 4) ||
+      (lengths != dst_lengths && overlap(lengths, B * 4, dst_lengths, B * 4)))
+    return fail(QSVD_ERR_INVALID_ARG,
+                "a destination must be its source (with dst_max_len == max_len) or not overlap it");
+  int32_t* src = static_cast<int32_t*>(workspace);
+  int32_t* new_len = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + src_bytes);
+  cudaError_t e = launch_evict(d, weights, lengths, budget, sink, recent, cache, scales, dst_max_len, dst_cache,
+                               dst_scales, dst_weights, dst_lengths, kept, src, new_len, status,
+                               static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "evict_rows");
+  return QSVD_OK;
 }
 
 qsvd_status qsvd_decode_attn_per_head(const qsvd_dims* dims, const void* bk, const void* bv,

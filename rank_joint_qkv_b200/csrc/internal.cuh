@@ -121,7 +121,8 @@ inline int combine_jsplit(const qsvd_dims& d) { return (d.r + 127) / 128; }
 int prologue_tickets(const qsvd_dims& d);  // ticket counters of that GEMV
 int gemv_tickets_vup(const qsvd_dims& d);  // ticket counters of the combine's V-up GEMV
 
-inline WsLayout ws_layout(const qsvd_dims& d, int G) {
+// keep_scores: room for the scores in absorbed mode too (attention weights).
+inline WsLayout ws_layout(const qsvd_dims& d, int G, bool keep_scores = false) {
   WsLayout w{};
   w.G = G;
   w.P = G + d.batch;
@@ -145,7 +146,7 @@ inline WsLayout ws_layout(const qsvd_dims& d, int G) {
   w.pz = o;    o = align256(o + size_t(w.P) * H * r * 4);
   w.opart = o; o = align256(o + size_t(w.JS) * B * E * 4);   // also the V-up GEMV's partials
   w.zm = o;    o = align256(o + B * H * r * 4);                 // merged latents [B][H][r]
-  w.scores = o; if (d.rope) o = align256(o + B * H * size_t(d.max_len) * 4);   // rotary: [B][H][max_len]
+  w.scores = o; if (d.rope || keep_scores) o = align256(o + B * H * size_t(d.max_len) * 4);   // [B][H][max_len]
   w.ow = o;    if (d.out_proj == QSVD_OUT_PROJ_CHAIN) o = align256(o + B * E * 4);   // o before W_O
   w.ypart = o; o = align256(o + size_t(w.KSY) * B * E * 4);    // output-projection partials
   w.total = o;
@@ -213,11 +214,13 @@ cudaError_t launch_rope_query(const qsvd_dims& d, const float* q, const int32_t*
                               const float* rope_tab, float scale_log2, float* qrot,
                               cudaStream_t s);
 
-// Split phase.
+// Split phase.  keep (absorbed mode and the CUDA-core rotary kernel): the
+// scores are also written there, [B][H][max_len] in the log2 domain, when it
+// is not null (the rotary scores kernel writes them in any case).
 cudaError_t launch_split_simt_absorbed(const qsvd_dims& d, const float* qt32,
                                        const void* cache, const void* scales,
                                        const int32_t* sched, int G, float* pm,
-                                       float* pl, float* pz, cudaStream_t s);
+                                       float* pl, float* pz, cudaStream_t s, float* keep = nullptr);
 // Rotary mode on the tensor cores: keys rebuilt from the latent, rotated,
 // scored against the rotary query into `scores` ([B][H][max_len]); then a
 // split kernel runs the softmax and the latent accumulation on them (the
@@ -238,7 +241,7 @@ cudaError_t launch_split_simt_rope(const qsvd_dims& d, const float* qrot,
                                    const void* wuk, const float* rope_tab,
                                    const void* cache, const void* scales,
                                    const int32_t* sched, int G, float* pm,
-                                   float* pl, float* pz, cudaStream_t s);
+                                   float* pl, float* pz, cudaStream_t s, float* keep = nullptr);
 int split_simt_grid_heads(const qsvd_dims& d);   // head blocks per split
 bool split_tc_supported(const qsvd_dims& d);
 // Absorbed mode, the tile's channels spread over a thread-block cluster;
@@ -246,13 +249,14 @@ bool split_tc_supported(const qsvd_dims& d);
 bool split_cl_supported(const qsvd_dims& d);
 int split_cl_clusters(const qsvd_dims& d);
 cudaError_t launch_split_cl(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
-                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s);
+                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
+                            float* keep = nullptr);
 // Absorbed mode, one CTA per split (tcgen05).  qt16: the query as 16-bit
 // hi/lo parts, or for an int8/int4 latent its int8 parts (launch_quant_query)
 // with qsh their per-(sequence, head) scales.
 cudaError_t launch_split_tc(const qsvd_dims& d, const void* cache, const void* scales, const void* qt16,
                             const int32_t* sched, int G, float* pm, float* pl, float* pz,
-                            int32_t* status, cudaStream_t s, const float* qsh = nullptr);
+                            int32_t* status, cudaStream_t s, const float* qsh = nullptr, float* keep = nullptr);
 
 // Prefill of the latent cache (tcgen05 GEMM x W^d with the append path's
 // rounding / quantisation fused): 16-bit weights, r % 256 == 0, E % 64 == 0,
@@ -301,6 +305,20 @@ cudaError_t launch_combine(const qsvd_dims& d, const WsHeader* hdr, const int32_
                            const float* pm, const float* pl, const float* pz,
                            const void* wuv, float* opart, int JS, int P, void* out,
                            cudaStream_t s);
+
+// Attention weight of each cache row from the kept scores (row_weights.cu):
+// w[b][t] = (add ? w[b][t] : 0) + sum_h 2^(s - M_h) / L_h for t < len_b.  ml:
+// {M, 1 / L} [B][H], or null to merge them from the splits' pm and pl.
+cudaError_t launch_row_weights(const qsvd_dims& d, const WsHeader* hdr, const int32_t* sched, const float* pm,
+                               const float* pl, const float2* ml, const float* scores, float* w, int add,
+                               cudaStream_t s);
+
+// Cutting caches to a budget of rows (evict.cu).  src [B][budget] and new_len
+// [B] are scratch.
+cudaError_t launch_evict(const qsvd_dims& d, const float* weights, const int32_t* lengths, int budget, int sink,
+                         int recent, const void* cache, const void* scales, int dst_max_len, void* dst_cache,
+                         void* dst_scales, float* dst_weights, int32_t* dst_lengths, int32_t* kept, int32_t* src,
+                         int32_t* new_len, int32_t* status, cudaStream_t s);
 
 // Append.
 int append_ksplit(const qsvd_dims& d);

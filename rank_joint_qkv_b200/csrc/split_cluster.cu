@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreadsCl, 1)
 k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q,
            const uint8_t* __restrict__ cache, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
-           int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int nt) {
+           int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int nt,
+           float* __restrict__ keep) {
   constexpr int QS = 2, PS = BF16 ? 2 : 1;
   constexpr int SW = QS * NP;                 // S accumulator columns per buffer
   constexpr int ZC0 = 2 * SW;                 // first Z column
@@ -463,6 +464,12 @@ k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUt
 
       // online softmax, m and l per head in shared memory (thread t < NP owns head t)
       const bool valid = t < nv;
+      if (keep && valid) {   // scores wanted ([B][H][max_len]): the cluster's CTAs share the heads
+        float* kp = keep + size_t(it.b) * H * max_len + it.t0() + t;
+#pragma unroll
+        for (int h = 0; h < NP; ++h)
+          if (h < H && h % CS == int(rank)) kp[size_t(h) * max_len] = sv[h];
+      }
       int need = first;
 #pragma unroll
       for (int h = 0; h < NP; ++h) {
@@ -656,7 +663,8 @@ struct ClPlan {
     return n;
   }
   static cudaError_t launch(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
-                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s) {
+                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
+                            float* keep) {
     TensorMapEncode enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
     constexpr int QS = 2;
@@ -695,7 +703,7 @@ struct ClPlan {
     cudaError_t e = config(CS, G, s, &cfg, &attr, &nt);
     if (e != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, k_split_cl<NP, BF16, RC>, tc, tq, static_cast<const uint8_t*>(cache),
-                           sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, nt);
+                           sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, nt, keep);
     if (e != cudaSuccess) return e;
     note_launch();
     return check_launch();
@@ -720,8 +728,9 @@ struct ClClusters {
 template <int NP, bool BF16, int RC>
 struct ClLaunch {
   static cudaError_t run(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
-                         int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s) {
-    return ClPlan<NP, BF16, RC>::launch(d, cache, qt16, sched, G, pm, pl, pz, status, s);
+                         int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
+                            float* keep) {
+    return ClPlan<NP, BF16, RC>::launch(d, cache, qt16, sched, G, pm, pl, pz, status, s, keep);
   }
 };
 
@@ -739,9 +748,10 @@ int split_cl_clusters(const qsvd_dims& d) {
 }
 
 cudaError_t launch_split_cl(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
-                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s) {
+                            int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
+                            float* keep) {
   if (!split_cl_supported(d)) return cudaErrorInvalidConfiguration;
-  return cl_dispatch<ClLaunch>(d, cache, qt16, sched, G, pm, pl, pz, status, s);
+  return cl_dispatch<ClLaunch>(d, cache, qt16, sched, G, pm, pl, pz, status, s, keep);
 }
 
 }  // namespace qsvd

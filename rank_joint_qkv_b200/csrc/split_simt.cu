@@ -89,13 +89,15 @@ __device__ __forceinline__ void stage_rows(float* dst, int ld, int TS, const uin
 // smem: qs[HB][r], cs[TS][r], zs[HB][r] (float), sc[TS*HB], red[8][64].
 // ---------------------------------------------------------------------------
 // SG: the scores come precomputed (rotary mode: [B][H][max_len], log2 domain,
-// scaled) instead of from the absorbed query.
+// scaled) instead of from the absorbed query.  keep: the scores are also
+// written there ([B][H][max_len]) when it is not null.
 template <qsvd_dtype CT, int HB, bool SG = false>
 __global__ void __launch_bounds__(kThreads)
 k_split_abs(const float* __restrict__ qt32, const uint8_t* __restrict__ cache,
             const __half* __restrict__ scales, const int32_t* __restrict__ sched,
             float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
-            int B, int H, int r, int max_len, int group, int G, const float* __restrict__ sgiven = nullptr) {
+            int B, int H, int r, int max_len, int group, int G, const float* __restrict__ sgiven,
+            float* __restrict__ keep) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   constexpr int TS = 8;             // tokens per sub-tile
@@ -182,6 +184,8 @@ k_split_abs(const float* __restrict__ qt32, const uint8_t* __restrict__ cache,
 #pragma unroll
         for (int w = 0; w < 8; ++w) s += red[w][threadIdx.x];
         sc[threadIdx.x] = s;
+        const int tt = threadIdx.x / HB, hh = threadIdx.x % HB;
+        if (keep && tt < nv) keep[(size_t(b) * H + h0 + hh) * max_len + s0 + tt] = s;
       }
       }
       __syncthreads();
@@ -243,7 +247,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
              const float* __restrict__ tab, const uint8_t* __restrict__ cache,
              const __half* __restrict__ scales, const int32_t* __restrict__ sched,
              float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
-             int B, int H, int d_h, int r, int E, int max_len, int group, int G) {
+             int B, int H, int d_h, int r, int E, int max_len, int group, int G, float* __restrict__ keep) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   constexpr int TS = 16;
@@ -348,6 +352,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
       __syncthreads();
       if (warp == 0) {
         const float s = lane < nv ? sc[lane & (TS - 1)] : -INFINITY;
+        if (keep && lane < nv) keep[(size_t(b) * H + h) * max_len + s0 + lane] = s;
         const float mx = dev::warp_max(lane < TS ? s : -INFINITY);
         const float m_old = m_s;
         const float m_new = fmaxf(m_old, mx);
@@ -392,7 +397,7 @@ int head_block(const qsvd_dims& d) {
 template <qsvd_dtype CT, int HB, bool SG = false>
 cudaError_t abs_t(const qsvd_dims& d, const float* qt32, const void* cache, const void* scales,
                   const int32_t* sched, int G, float* pm, float* pl, float* pz, cudaStream_t s,
-                  const float* sgiven = nullptr) {
+                  const float* sgiven, float* keep) {
   const size_t smem = size_t(2 * HB + 8) * d.r * 4;
   auto kern = k_split_abs<CT, HB, SG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -400,7 +405,7 @@ cudaError_t abs_t(const qsvd_dims& d, const float* qt32, const void* cache, cons
   dim3 grid(G, d.H / HB);
   {
     const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s,
-                                     qt32, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.r, d.max_len, d.group, G, sgiven);
+                                     qt32, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.r, d.max_len, d.group, G, sgiven, keep);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -411,22 +416,22 @@ template <qsvd_dtype CT>
 cudaError_t scores_ct(const qsvd_dims& d, const float* sgiven, const void* cache, const void* scales,
                       const int32_t* sched, int G, float* pm, float* pl, float* pz, cudaStream_t s) {
   switch (head_block(d)) {
-    case 8: return abs_t<CT, 8, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven);
-    case 4: return abs_t<CT, 4, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven);
-    case 2: return abs_t<CT, 2, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven);
-    case 1: return abs_t<CT, 1, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven);
+    case 8: return abs_t<CT, 8, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven, nullptr);
+    case 4: return abs_t<CT, 4, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven, nullptr);
+    case 2: return abs_t<CT, 2, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven, nullptr);
+    case 1: return abs_t<CT, 1, true>(d, nullptr, cache, scales, sched, G, pm, pl, pz, s, sgiven, nullptr);
     default: return cudaErrorInvalidConfiguration;
   }
 }
 
 template <qsvd_dtype CT>
 cudaError_t abs_ct(const qsvd_dims& d, const float* qt32, const void* cache, const void* scales,
-                   const int32_t* sched, int G, float* pm, float* pl, float* pz, cudaStream_t s) {
+                   const int32_t* sched, int G, float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
   switch (head_block(d)) {
-    case 8: return abs_t<CT, 8>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case 4: return abs_t<CT, 4>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case 2: return abs_t<CT, 2>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case 1: return abs_t<CT, 1>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
+    case 8: return abs_t<CT, 8>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, nullptr, keep);
+    case 4: return abs_t<CT, 4>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, nullptr, keep);
+    case 2: return abs_t<CT, 2>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, nullptr, keep);
+    case 1: return abs_t<CT, 1>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, nullptr, keep);
     default: return cudaErrorInvalidConfiguration;
   }
 }
@@ -434,7 +439,7 @@ cudaError_t abs_ct(const qsvd_dims& d, const float* qt32, const void* cache, con
 template <qsvd_dtype CT, typename WT>
 cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                    const void* cache, const void* scales, const int32_t* sched, int G,
-                   float* pm, float* pl, float* pz, cudaStream_t s) {
+                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
   const size_t smem = (size_t(16) * (d.r + 1) + size_t(32) * d.d_h + d.r) * 4;
   auto kern = k_split_rope<CT, WT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -442,7 +447,7 @@ cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const
   dim3 grid(G, d.H);
   {
     const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s,
-                                     qrot, static_cast<const WT*>(wuk), tab, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.d_h, d.r, d.E, d.max_len, d.group, G);
+                                     qrot, static_cast<const WT*>(wuk), tab, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.d_h, d.r, d.E, d.max_len, d.group, G, keep);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -452,11 +457,11 @@ cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const
 template <qsvd_dtype CT>
 cudaError_t rope_ct(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                     const void* cache, const void* scales, const int32_t* sched, int G,
-                    float* pm, float* pl, float* pz, cudaStream_t s) {
+                    float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
   switch (d.weight_dtype) {
-    case QSVD_F32: return rope_t<CT, float>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_F16: return rope_t<CT, __half>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_BF16: return rope_t<CT, __nv_bfloat16>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s);
+    case QSVD_F32: return rope_t<CT, float>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_F16: return rope_t<CT, __half>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_BF16: return rope_t<CT, __nv_bfloat16>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -471,13 +476,13 @@ int split_simt_grid_heads(const qsvd_dims& d) {
 
 cudaError_t launch_split_simt_absorbed(const qsvd_dims& d, const float* qt32, const void* cache,
                                        const void* scales, const int32_t* sched, int G,
-                                       float* pm, float* pl, float* pz, cudaStream_t s) {
+                                       float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
   switch (d.cache_dtype) {
-    case QSVD_F32: return abs_ct<QSVD_F32>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_F16: return abs_ct<QSVD_F16>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_BF16: return abs_ct<QSVD_BF16>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_I8: return abs_ct<QSVD_I8>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_I4: return abs_ct<QSVD_I4>(d, qt32, cache, scales, sched, G, pm, pl, pz, s);
+    case QSVD_F32: return abs_ct<QSVD_F32>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_F16: return abs_ct<QSVD_F16>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_BF16: return abs_ct<QSVD_BF16>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_I8: return abs_ct<QSVD_I8>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_I4: return abs_ct<QSVD_I4>(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
   }
   return cudaErrorInvalidValue;
 }
@@ -495,13 +500,13 @@ cudaError_t launch_split_simt_scores(const qsvd_dims& d, const float* scores, co
 cudaError_t launch_split_simt_rope(const qsvd_dims& d, const float* qrot, const void* wuk,
                                    const float* rope_tab, const void* cache, const void* scales,
                                    const int32_t* sched, int G, float* pm, float* pl, float* pz,
-                                   cudaStream_t s) {
+                                   cudaStream_t s, float* keep) {
   switch (d.cache_dtype) {
-    case QSVD_F32: return rope_ct<QSVD_F32>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_F16: return rope_ct<QSVD_F16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_BF16: return rope_ct<QSVD_BF16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_I8: return rope_ct<QSVD_I8>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
-    case QSVD_I4: return rope_ct<QSVD_I4>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s);
+    case QSVD_F32: return rope_ct<QSVD_F32>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_F16: return rope_ct<QSVD_F16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_BF16: return rope_ct<QSVD_BF16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_I8: return rope_ct<QSVD_I8>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_I4: return rope_ct<QSVD_I4>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
   }
   return cudaErrorInvalidValue;
 }

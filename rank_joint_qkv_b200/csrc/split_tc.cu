@@ -694,18 +694,24 @@ __device__ void drain_ring(uint64_t* full, long long k, int nslots) {
 // of all chunks does not fit TMEM, `ch` CTAs share one tile range (split g =
 // blockIdx.x / ch), each owning every ch-th chunk; all of them run the same
 // softmax on the same scores and part 0 writes m and l.
-template <int NP, bool BF16, int QS, int PS, int QB, bool SG>
+// KEEP: the scores of the attended tokens are also written to `scores`
+// ([B][H][max_len] fp32, log2 domain), from which the rows' attention weights
+// are formed once the splits' m and l are merged.  A warp's store is 32
+// consecutive floats of one head; 4 H bytes per token beside the 2 r or more
+// of its latent row, most of it still in L2 when it is read back.
+template <int NP, bool BF16, int QS, int PS, int QB, bool SG, bool KEEP>
 __global__ void __launch_bounds__(split_threads<NP, QB>(), 1)
 k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CUtensorMap tm_cz,
            const __grid_constant__ CUtensorMap tm_q,
            const uint8_t* __restrict__ cache, const __half* __restrict__ scales,
-           const float* __restrict__ scores, const int32_t* __restrict__ sched,
+           float* __restrict__ scores, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
            int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int ns, int nz,
            int nsg, int nraw, int ch, const float* __restrict__ qsh) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   static_assert(!(SG && QB), "scores given: 16-bit latent only");
+  static_assert(!(SG && KEEP), "scores given: they are kept already");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -1057,6 +1063,16 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
         tmem_wait_ld();
       }
       const bool valid = t < nv;
+      if constexpr (KEEP) {
+        if (valid) {
+          float* kp = scores + (size_t(it.b) * H + hb) * max_len + it.t0() + t;
+#pragma unroll
+          for (int h = 0; h < HW; ++h) {
+            if (hb + h < H) *kp = sv[h];
+            kp += max_len;
+          }
+        }
+      }
       int need = first;   // a segment starts: m and l are set below
 #pragma unroll
       for (int h = 0; h < HW; ++h) {
@@ -1436,9 +1452,9 @@ void ring_slots(int* ns, int* nz) {
   *nz = z;
 }
 
-template <int NP, bool BF16, int QB, bool SG = false>
+template <int NP, bool BF16, int QB, bool SG = false, bool KEEP = false>
 cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, const void* qt16,
-                     const float* scores, const int32_t* sched, int G, float* pm, float* pl,
+                     float* scores, const int32_t* sched, int G, float* pm, float* pl,
                      float* pz, int32_t* status, cudaStream_t s, int ch = 1, const float* qsh = nullptr) {
   TensorMapEncode enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
@@ -1554,7 +1570,7 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   const size_t smem = 1024 + size_t(ns) * a_slot_bytes<NP, QS, SG, QB>() + size_t(nz) * kZSlotBytes +
                       2 * PS * pbuf_bytes<NP>() +
                       (QB ? size_t(nraw) * raw_s_bytes(QB) + kScaleBufs * scale_buf_bytes(d.r) : 0) + kMiscBytes;
-  auto kern = k_split_tc<NP, BF16, QS, PS, QB, SG>;
+  auto kern = k_split_tc<NP, BF16, QS, PS, QB, SG, KEEP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   {
@@ -1631,23 +1647,26 @@ bool split_tc_supported(const qsvd_dims& d) {
 
 cudaError_t launch_split_tc(const qsvd_dims& d, const void* cache, const void* scales, const void* qt16,
                             const int32_t* sched, int G, float* pm, float* pl, float* pz,
-                            int32_t* status, cudaStream_t s, const float* qsh) {
-  const int np = split_tc_heads_padded(d);
-  const float* ns = nullptr;
-  switch (d.cache_dtype) {
-    case QSVD_BF16:
-      return np == 16 ? launch_t<16, true, 0>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s)
-                      : launch_t<32, true, 0>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s);
-    case QSVD_I4:
-      return np == 16 ? launch_t<16, false, 4>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s, 1, qsh)
-                      : launch_t<32, false, 4>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s, 1, qsh);
-    case QSVD_I8:
-      return np == 16 ? launch_t<16, false, 8>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s, 1, qsh)
-                      : launch_t<32, false, 8>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s, 1, qsh);
-    default:
-      return np == 16 ? launch_t<16, false, 0>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s)
-                      : launch_t<32, false, 0>(d, cache, scales, qt16, ns, sched, G, pm, pl, pz, status, s);
+                            int32_t* status, cudaStream_t s, const float* qsh, float* keep) {
+  const bool n16 = split_tc_heads_padded(d) == 16;
+#define QSVD_TC(BF, QB, KP)                                                                                   \
+  return n16 ? launch_t<16, BF, QB, false, KP>(d, cache, scales, qt16, keep, sched, G, pm, pl, pz, status, s, 1, qsh) \
+             : launch_t<32, BF, QB, false, KP>(d, cache, scales, qt16, keep, sched, G, pm, pl, pz, status, s, 1, qsh)
+  if (keep) {
+    switch (d.cache_dtype) {
+      case QSVD_BF16: QSVD_TC(true, 0, true);
+      case QSVD_I4: QSVD_TC(false, 4, true);
+      case QSVD_I8: QSVD_TC(false, 8, true);
+      default: QSVD_TC(false, 0, true);
+    }
   }
+  switch (d.cache_dtype) {
+    case QSVD_BF16: QSVD_TC(true, 0, false);
+    case QSVD_I4: QSVD_TC(false, 4, false);
+    case QSVD_I8: QSVD_TC(false, 8, false);
+    default: QSVD_TC(false, 0, false);
+  }
+#undef QSVD_TC
 }
 
 // Scores given: heads padded to 16, 32 or 48 (softmax registers), and the
@@ -1677,7 +1696,7 @@ cudaError_t launch_split_tc_scores(const qsvd_dims& d, const float* scores, cons
   const int np = sg_heads_padded(d), ch = split_tc_scores_parts(d);
   if (ch == 0) return cudaErrorInvalidConfiguration;
 #define QSVD_SG(NP, BF)                                                                         \
-  launch_t<NP, BF, 0, true>(d, cache, nullptr, nullptr, scores, sched, G, pm, pl, pz, status, s, ch)
+  launch_t<NP, BF, 0, true>(d, cache, nullptr, nullptr, const_cast<float*>(scores), sched, G, pm, pl, pz, status, s, ch)
   if (d.cache_dtype == QSVD_BF16)
     return np == 16 ? QSVD_SG(16, true) : np == 32 ? QSVD_SG(32, true) : QSVD_SG(48, true);
   return np == 16 ? QSVD_SG(16, false) : np == 32 ? QSVD_SG(32, false) : QSVD_SG(48, false);

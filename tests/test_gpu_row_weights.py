@@ -1,0 +1,115 @@
+"""qsvd_decode_attn_weights: a decode step that also gives each row's attention
+weight.  The output is the plain decode's bit for bit (the same kernels); the
+weights are compared with the definition in 64 bits, within a bound on the
+scores' error that is computed from the inputs."""
+import pytest
+import torch
+
+import rank_joint_qkv_b200 as q
+from tests.serving_util import DEV, Layer, close_weights
+
+pytestmark = pytest.mark.gpu
+
+A, S, T, C = (q.QSVD_KERNEL_AUTO, q.QSVD_KERNEL_SIMT, q.QSVD_KERNEL_TCGEN05_CTA, q.QSVD_KERNEL_TCGEN05_CLUSTER)
+CASES = {
+    # every split kernel; head padding (H 4 of 16, 20 of 32), lengths 0, 1, either side of a tile
+    "f32-simt": dict(cache="f32", weight="f32", H=4, d_h=64, r=96, lens=(5, 0, 1, 130)),
+    "f16-simt": dict(cache="f16", H=6, d_h=64, r=160, lens=(127, 128, 129), kernel=S),
+    "f16-tc": dict(cache="f16", H=4, d_h=64, r=256, lens=(0, 1, 127, 128, 129, 700), kernel=T),
+    "f16-tc-20-heads": dict(cache="f16", H=20, d_h=64, r=384, lens=(300, 64), kernel=T),
+    "bf16-tc": dict(cache="bf16", weight="bf16", out="bf16", H=32, d_h=128, r=512, lens=(1000, 3), kernel=T),
+    "f16-cluster": dict(cache="f16", H=8, d_h=64, r=512, lens=(0, 257, 40), kernel=C),
+    "i8-tc": dict(cache="i8", H=4, d_h=64, r=256, lens=(0, 1, 129, 500), kernel=T),
+    "i8-tc-32-heads": dict(cache="i8", weight="bf16", out="bf16", H=32, d_h=64, r=256, lens=(200, 77), kernel=T),
+    "i4-tc": dict(cache="i4", H=8, d_h=64, r=384, lens=(1, 400), kernel=T),
+    "i4-simt-group": dict(cache="i4", H=4, d_h=64, r=96, group=32, lens=(33, 9), kernel=S),
+    "f16-rope-tc": dict(cache="f16", H=4, d_h=128, r=256, lens=(0, 1, 129, 333), rope=True),
+    "bf16-rope-tc": dict(cache="bf16", weight="bf16", out="bf16", H=8, d_h=128, r=128, lens=(130, 64), rope=True),
+    "f32-rope-simt": dict(cache="f32", weight="f32", H=2, d_h=64, r=64, lens=(40, 0, 17), rope=True),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_weights_against_the_definition(cuda_ok, name):
+    m = Layer(**CASES[name])
+    plain = m.empty_out()
+    q.qsvd_decode_attn(m.dims, m.packed, m.qin, True, m.cache, m.scales, m.lengths, plain)
+    _, want, bound = m.exact()
+    w = torch.full((m.B, m.max_len), 7.0, device=DEV)   # written, not added to
+    out = m.empty_out()
+    ws = q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, m.scales, m.lengths, out, w,
+                                    accumulate=False)
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain)
+    assert q.status_word(ws) == 0
+    close_weights(w, want, bound, m.lens)
+    for b, n in enumerate(m.lens):
+        assert bool((w[b, n:] == 7.0).all())            # entries behind the length stay
+    # added to what is there: one float32 addition of the same sum
+    before = torch.rand(m.B, m.max_len, device=DEV)
+    acc = before.clone()
+    q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, m.scales, m.lengths, out, acc, workspace=ws)
+    torch.cuda.synchronize()
+    for b, n in enumerate(m.lens):
+        assert torch.equal(acc[b, :n], before[b, :n] + w[b, :n])
+        assert torch.equal(acc[b, n:], before[b, n:])
+
+
+@pytest.mark.parametrize("kernel", [S, T])
+def test_rows_behind_the_length_have_no_bearing(cuda_ok, kernel):
+    """NaN and infinity behind each length; the weights of a sequence sum to H."""
+    clean = Layer(H=4, r=256, lens=(100, 1, 260), kernel=kernel, seed=3)
+    for past in (float("nan"), float("inf")):
+        m = Layer(H=4, r=256, lens=(100, 1, 260), kernel=kernel, seed=3, past=past)
+        got = []
+        for layer in (clean, m):
+            w, out = torch.zeros(3, layer.max_len, device=DEV), layer.empty_out()
+            q.qsvd_decode_attn_weights(layer.dims, layer.packed, layer.qin, True, layer.cache, None, layer.lengths, out, w)
+            got.append((out, w))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        # H probabilities' sums, each 1 up to the rounding of n float32 terms
+        assert bool(((got[1][1].double().sum(1) - 4).abs() <= 4 * 300 * 2.0 ** -23).all())
+
+
+def test_split_counts_give_the_same_weights(cuda_ok):
+    m = Layer(H=4, r=256, lens=(700, 129), kernel=T)
+    _, want, bound = m.exact()
+    for splits in (1, 3, 1000):
+        w, out = torch.zeros(2, m.max_len, device=DEV), m.empty_out()
+        q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, m.lengths, out, w, num_splits=splits)
+        close_weights(w, want, bound, m.lens)
+
+
+def test_graph_replay_and_side_stream(cuda_ok):
+    """Captured on a side stream and replayed: each replay adds the same weights; two graphs with workspaces of their own."""
+    m = Layer(H=8, r=256, lens=(300, 40), kernel=T)
+    once, out = torch.zeros(2, m.max_len, device=DEV), m.empty_out()
+    q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, m.lengths, out, once)
+    accs, graphs = [], []
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        acc, o = torch.zeros(2, m.max_len, device=DEV), m.empty_out()
+        ws = torch.empty(q.decode_weights_workspace_bytes(m.dims), dtype=torch.uint8, device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, m.lengths, o, acc, workspace=ws)
+        accs.append((acc, o, ws))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    want = (once + once) + once
+    for acc, o, _ in accs:
+        assert torch.equal(acc, want) and torch.equal(o, out)
+
+
+def test_clamped_length_is_flagged(cuda_ok):
+    m = Layer(H=4, r=256, lens=(50, 60), kernel=T)
+    lengths = torch.tensor([-3, m.max_len + 9], dtype=torch.int32, device=DEV)
+    w, out = torch.zeros(2, m.max_len, device=DEV), m.empty_out()
+    ws = q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, lengths, out, w)
+    assert q.status_word(ws) == q.QSVD_STATUS_LEN_CLAMPED
+    assert bool((out[0] == 0).all()) and bool((w[0] == 0).all()) and bool((w[1] > 0).all())

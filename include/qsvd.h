@@ -478,7 +478,9 @@ qsvd_status qsvd_prepare_per_head_fold(const qsvd_dims* dims, const void* bv, co
  *   weights[b][t] = (accumulate ? weights[b][t] : 0) + sum_h p_{b,h,t},  t < len_b
  * with p the step's softmax probabilities; entries t >= len_b are left as
  * they were.  Summed over steps (accumulate != 0) it is what decides which
- * rows qsvd_evict_rows keeps.  The output is that of qsvd_decode_attn.
+ * rows qsvd_evict_rows keeps.  The output is that of qsvd_decode_attn, up to
+ * a few 1e-6 of the scores (the query is scaled up by what the tensor cores'
+ * truncating accumulation takes off them).
  * Serving decode; the pages have no counterpart.
  *   weights    device, B x max_len float32, 4-byte aligned.
  *   workspace  as in qsvd_decode_attn, with room for the step's scores

@@ -154,6 +154,21 @@ static float score_scale_log2(const qsvd_dims& d) {
   return float(tau * 1.4426950408889634);
 }
 
+// The tensor cores add into their float32 accumulator by truncation: each of
+// a score's `steps` accumulations loses half a unit in the last place on
+// average, 0.5 x 2^-23 of a mantissa that averages 1 / 0.72, while the partial
+// sum is on average 0.7 to 0.8 of the final one -- about 2^-25 of the score a
+// step.  Scores come out short by that factor (measured: 2.7e-6 at r 1536,
+// where 96 x 2^-25 = 2.9e-6), a slightly higher softmax temperature that 16-bit
+// outputs do not show but float32 attention weights do (1e-5 of a weight);
+// the query is scaled up by it where weights are asked for.
+static float score_scale_for_weights(const qsvd_dims& d, int kernel) {
+  double steps = 0;
+  if (kernel != QSVD_KERNEL_SIMT && !cache_is_int(d))   // quantised: integer sums, exact
+    steps = kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) / 16.0 : d.r / 16.0;
+  return float(score_scale_log2(d) * (1.0 + steps / 33554432.0));
+}
+
 }  // namespace qsvd
 
 using namespace qsvd;
@@ -413,7 +428,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   float* pz = reinterpret_cast<float*>(Wb + W.pz);
   float* opart = reinterpret_cast<float*>(Wb + W.opart);
   const float* rope_tab = reinterpret_cast<const float*>(P + L.rope);
-  const float sl2 = score_scale_log2(d);
+  const float sl2 = x.weights ? score_scale_for_weights(d, kernel) : score_scale_log2(d);
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
   cudaError_t e;

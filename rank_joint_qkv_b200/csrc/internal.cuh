@@ -248,6 +248,7 @@ bool split_tc_supported(const qsvd_dims& d);
 // G = the number of clusters (split_cl_clusters: as many as fit at once).
 bool split_cl_supported(const qsvd_dims& d);
 int split_cl_clusters(const qsvd_dims& d);
+int split_cl_channels(const qsvd_dims& d);   // channels per CTA of a cluster
 cudaError_t launch_split_cl(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
                             int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
                             float* keep = nullptr);

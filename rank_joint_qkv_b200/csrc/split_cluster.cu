@@ -742,6 +742,8 @@ bool split_cl_supported(const qsvd_dims& d) {
   return cl_slice(d.r) != 0 && cl_heads_padded(d.H) != 0;
 }
 
+int split_cl_channels(const qsvd_dims& d) { return cl_slice(d.r); }
+
 int split_cl_clusters(const qsvd_dims& d) {
   if (!split_cl_supported(d)) return 0;
   return cl_dispatch<ClClusters>(d);

@@ -497,6 +497,46 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
                                      int accumulate, void* stream);
 
 /*
+ * qsvd_decode_attn_shared -- one decode step of a batch whose sequences share
+ * a prefix: sequence b attends the prefix's `prefix_len` latent rows, stored
+ * once, and then its own rows 0 .. len_b - 1,
+ *   p_{b,h} = softmax over prefix and own rows of tau q_{b,h} . k_u,
+ *   o_{b,h} = (sum_u p_u c_u) W^u_{v,h},
+ * as qsvd_decode_attn would with the prefix's rows at the start of every
+ * sequence's cache -- but the prefix is read once for the batch, as one pair
+ * of tensor-core products over all B H query rows.  Serving decode; the pages
+ * have no counterpart.
+ *   dims           as in qsvd_decode_attn; max_len is the capacity of the own
+ *                  caches.  Absorbed mode only (dims->rope: UNSUPPORTED).
+ *   prefix, prefix_scales  device, prefix_len rows (and group scales) as in
+ *                  qsvd_append_latent's cache, 16-byte (2-byte) aligned; not
+ *                  read when prefix_len is 0.
+ *   prefix_len     >= 0, batch x prefix_len < 2^31.
+ *   cache, scales, lengths, num_splits  the own rows, as in qsvd_decode_attn;
+ *                  a sequence with len 0 attends the prefix alone, with
+ *                  prefix_len 0 too its output row is zero.
+ *   weights        device, B x max_len float32, or NULL: the own rows' weights
+ *                  as in qsvd_decode_attn_weights (the prefix's share of the
+ *                  softmax is not reported).
+ *   workspace      device scratch, or NULL to query the size of dims,
+ *                  prefix_len and num_splits (on the current device) into
+ *                  *workspace_bytes; its first int32 is the status word.
+ *   out            device, B x E, out_dtype (B x E projected with
+ *                  dims->out_proj).
+ * The prefix runs on the tensor cores for F16, BF16, I8 and I4 caches with
+ * r % 64 == 0, H <= 128 and dims->kernel other than SIMT, and on the CUDA cores
+ * otherwise.  A quantised prefix is expanded to fp16 parts in the workspace,
+ * so code x scale and the absorbed query must lie within fp16's range.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, const float* qin,
+                                    int qin_is_latent, const void* prefix,
+                                    const void* prefix_scales, int prefix_len, const void* cache,
+                                    const void* scales, const int32_t* lengths, int num_splits,
+                                    void* workspace, size_t* workspace_bytes, void* out,
+                                    float* weights, int accumulate, void* stream);
+
+/*
  * qsvd_evict_rows -- cut each sequence's cache to at most `budget` rows by
  * accumulated attention weight (see qsvd_decode_attn_weights).  A sequence
  * with n = lengths[b] > budget keeps its first `sink` rows, its last `recent`

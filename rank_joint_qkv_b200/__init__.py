@@ -71,6 +71,8 @@ _sigs = {
     "qsvd_beta_exponents": [_P, ctypes.c_int, ctypes.c_double, _P, _P, _P],
     "qsvd_decode_attn_weights": [_D, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P, _SZ, _P, _P,
                                  ctypes.c_int, _P],
+    "qsvd_decode_attn_shared": [_D, _P, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P, _SZ, _P,
+                                _P, ctypes.c_int, _P],
     "qsvd_evict_rows": [_D, _P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P,
                         _P, _P, _P, _P, _SZ, _P],
     "qsvd_sq_diff_sum": [_P, _P, ctypes.c_int64, _P, _P],
@@ -333,6 +335,32 @@ def qsvd_decode_attn_weights(dims: qsvd_dims, packed, qin, qin_is_latent, cache,
                                          ctypes.byref(n), _ptr(out), _ptr(weights), int(bool(accumulate)),
                                          _stream(stream)),
            "qsvd_decode_attn_weights")
+    return workspace
+
+
+def decode_shared_workspace_bytes(dims: qsvd_dims, prefix_len: int, num_splits: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.qsvd_decode_attn_shared(ctypes.byref(dims), None, None, 1, None, None, int(prefix_len), None, None,
+                                        None, int(num_splits), None, ctypes.byref(n), None, None, 0, None),
+           "qsvd_decode_attn_shared(size)")
+    return n.value
+
+
+def qsvd_decode_attn_shared(dims: qsvd_dims, packed, qin, qin_is_latent, prefix, prefix_scales, prefix_len, cache,
+                            scales, lengths, out, weights=None, accumulate=True, num_splits=0, workspace=None,
+                            stream=None):
+    """Decode step of a batch over ``prefix_len`` shared latent rows
+    (``prefix``, ``prefix_scales``) and each sequence's own rows.  ``weights``:
+    optional B x max_len float32, the own rows' attention weights as in
+    qsvd_decode_attn_weights.  Returns the workspace."""
+    if workspace is None:
+        workspace = _empty_bytes(decode_shared_workspace_bytes(dims, prefix_len, num_splits), cache.device)
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    _check(_lib.qsvd_decode_attn_shared(ctypes.byref(dims), _ptr(packed), _ptr(qin), int(bool(qin_is_latent)),
+                                        _ptr(prefix), _ptr(prefix_scales), int(prefix_len), _ptr(cache), _ptr(scales),
+                                        _ptr(lengths), int(num_splits), _ptr(workspace), ctypes.byref(n), _ptr(out),
+                                        _ptr(weights), int(bool(accumulate)), _stream(stream)),
+           "qsvd_decode_attn_shared")
     return workspace
 
 

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "internal.cuh"
+#include "prefix.cuh"
 #include "wsvd.cuh"
 
 namespace qsvd {
@@ -162,11 +163,10 @@ static float score_scale_log2(const qsvd_dims& d) {
 // where 96 x 2^-25 = 2.9e-6), a slightly higher softmax temperature that 16-bit
 // outputs do not show but float32 attention weights do (1e-5 of a weight);
 // the query is scaled up by it where weights are asked for.
-static float score_scale_for_weights(const qsvd_dims& d, int kernel) {
-  double steps = 0;
-  if (kernel != QSVD_KERNEL_SIMT && !cache_is_int(d))   // quantised: integer sums, exact
-    steps = kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) / 16.0 : d.r / 16.0;
-  return float(score_scale_log2(d) * (1.0 + steps / 33554432.0));
+static double score_gain(double steps) { return 1.0 + steps / 33554432.0; }
+static double split_score_gain(const qsvd_dims& d, int kernel) {
+  if (kernel == QSVD_KERNEL_SIMT || cache_is_int(d)) return 1.0;   // quantised: integer sums, exact
+  return score_gain(kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) / 16.0 : d.r / 16.0);
 }
 
 }  // namespace qsvd
@@ -366,6 +366,10 @@ struct DecodeExtra {
   bool keep_scores = false;    // the workspace has room for the scores
   float* weights = nullptr;    // B x max_len: the rows' attention weights ...
   int add = 0;                 // ... added to what is there
+  bool shared = false;         // a prefix that the sequences share
+  const void* prefix = nullptr;
+  const void* prefix_scales = nullptr;
+  int prefix_len = 0;
 };
 
 static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const float* qin,
@@ -400,9 +404,12 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   qsvd_status st = resolve_splits(d, num_splits, kernel, &G);
   if (st != QSVD_OK) return st;
   const WsLayout W = ws_layout(d, G, x.keep_scores);
-  if (!workspace) { *workspace_bytes = W.total; return QSVD_OK; }
-  if (*workspace_bytes < W.total)
-    return fail(QSVD_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", *workspace_bytes, W.total);
+  const int sms = device_sms() > 0 ? device_sms() : 1;
+  const PrefixLayout X = x.shared ? prefix_layout(d, x.prefix_len, sms, W.total) : PrefixLayout{};
+  const size_t total = x.shared ? X.total : W.total;
+  if (!workspace) { *workspace_bytes = total; return QSVD_OK; }
+  if (*workspace_bytes < total)
+    return fail(QSVD_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", *workspace_bytes, total);
   if (!packed || !lengths) return fail(QSVD_ERR_INVALID_ARG, "packed/lengths is NULL");
   if ((phases & QSVD_PHASE_PROLOGUE) && !qin) return fail(QSVD_ERR_INVALID_ARG, "qin is NULL");
   if (split_any && !cache) return fail(QSVD_ERR_INVALID_ARG, "cache is NULL");
@@ -428,15 +435,21 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   float* pz = reinterpret_cast<float*>(Wb + W.pz);
   float* opart = reinterpret_cast<float*>(Wb + W.opart);
   const float* rope_tab = reinterpret_cast<const float*>(P + L.rope);
-  const float sl2 = x.weights ? score_scale_for_weights(d, kernel) : score_scale_log2(d);
+  const bool px = x.shared && x.prefix_len > 0;   // prefix rows: on the tensor cores (X.fast) or the CUDA cores
+  const double gain = x.weights || x.shared ? split_score_gain(d, kernel) : 1.0;
+  const float sl2 = float(double(score_scale_log2(d)) * gain);
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
+  void* px16 = cache_is_int(d) ? static_cast<void*>(Wb + X.qt16) : qt16;   // the prefix's 16-bit query parts
   cudaError_t e;
 
   if (phases & QSVD_PHASE_PROLOGUE) {
     int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets);
     if ((e = launch_schedule(d, lengths, G, sched, hdr, kernel, tickets, W.NT, s)) != cudaSuccess)
       return cuda_fail(e, "schedule");
+    if (x.shared && (!X.fast || !combine_uses_gemv(d)) &&
+        (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
+      return cuda_fail(e, "prefix schedule");
     // q = c_new W^u_q (reduced into the workspace), or the query as given
     const float* qsrc = qin;
     if (qin_is_latent) {
@@ -448,26 +461,25 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     if (d.rope)
       e = launch_rope_query(d, qsrc, sched, rope_tab, sl2, qt32, s);
     else
-      // only the copy the split kernel reads: fp32 for CUDA cores, 16-bit hi/lo
+      // only the copies the split kernels read: fp32 for CUDA cores, 16-bit hi/lo
       // for tensor cores; a quantised latent on the tensor cores takes the
       // absorbed query as three int8 parts and one scale per (sequence, head),
       // both written into the 16-bit parts' section from the fp32 copy
-      if (kernel != QSVD_KERNEL_SIMT && cache_is_int(d)) {
-        e = launch_absorb(d, qsrc, P + L.wuk, sl2, qt32, nullptr, &hdr->status, s);
-        if (e == cudaSuccess)
-          e = launch_quant_query(d, qt32, static_cast<int8_t*>(qt16), quant_query_scales(d, qt16), s);
-      } else {
-        e = launch_absorb(d, qsrc, P + L.wuk, sl2, kernel == QSVD_KERNEL_SIMT ? qt32 : nullptr,
-                          kernel == QSVD_KERNEL_SIMT ? nullptr : qt16, &hdr->status, s);
-      }
+    {
+      const bool codes = kernel != QSVD_KERNEL_SIMT && cache_is_int(d);
+      const bool need32 = kernel == QSVD_KERNEL_SIMT || codes || (px && !X.fast);
+      void* parts = (kernel != QSVD_KERNEL_SIMT && !codes) || (px && X.fast) ? (px && cache_is_int(d) ? px16 : qt16) : nullptr;
+      e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s);
+      if (e == cudaSuccess && codes)
+        e = launch_quant_query(d, qt32, static_cast<int8_t*>(qt16), quant_query_scales(d, qt16), s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "query prologue");
   }
   if (split_any) {
     if (d.rope && kernel == QSVD_KERNEL_TCGEN05_CTA) {
-      const int sms = device_sms();
       e = cudaSuccess;
       if (phases & QSVD_PHASE_SPLIT_SCORES)
-        e = launch_rope_scores(d, cache, P + L.wukT, qt32, rope_tab, sched, sms > 0 ? sms : 1,
+        e = launch_rope_scores(d, cache, P + L.wukT, qt32, rope_tab, sched, sms,
                                scores, &hdr->status, s);
       if (e == cudaSuccess && (phases & QSVD_PHASE_SPLIT_ACCUM))
         e = split_tc_scores_supported(d)
@@ -485,10 +497,36 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     else
       e = launch_split_simt_absorbed(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
     if (e != cudaSuccess) return cuda_fail(e, "split phase");
-    if (x.weights && (e = launch_row_weights(d, hdr, sched, pm, pl, nullptr, scores, x.weights, x.add, s)) != cudaSuccess)
+    if (px) {
+      e = launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qt32,
+                        float(score_gain(prefix_score_steps(d)) / gain), sms, &hdr->status, s);
+      if (e != cudaSuccess) return cuda_fail(e, "prefix");
+    }
+    if (x.weights && !x.shared && (e = launch_row_weights(d, hdr, sched, pm, pl, nullptr, scores, x.weights, x.add, s)) != cudaSuccess)
       return cuda_fail(e, "attention weights");
   }
-  if (phases & QSVD_PHASE_COMBINE) {
+  if (x.shared) {
+    const bool gemv = combine_uses_gemv(d);
+    float* zm = reinterpret_cast<float*>(Wb + W.zm);
+    const bool fold = d.out_proj == QSVD_OUT_PROJ_FOLD;
+    const size_t wb = dtype_bytes(d.weight_dtype);
+    e = launch_merge_shared(d, X, Wb, hdr, sched, pm, pl, pz, zm, !gemv, fold ? P + L.wo : P + L.wuv,
+                            !gemv ? 0 : (fold ? out_proj_rows(d) : size_t(d.r)) * d.E * wb, s);
+    if (e != cudaSuccess) return cuda_fail(e, "merge");
+    if (gemv) {
+      int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NTQ;
+      const OutProj op{P + L.wo, reinterpret_cast<float*>(Wb + W.ow), reinterpret_cast<float*>(Wb + W.ypart),
+                       tickets + W.NTV};
+      e = launch_vup_gemv(d, P + L.wuv, zm, opart, tickets, &hdr->status, out, op, s);
+    } else {
+      e = launch_combine(d, reinterpret_cast<const WsHeader*>(Wb + X.hdr), reinterpret_cast<const int32_t*>(Wb + X.csched),
+                         reinterpret_cast<const float*>(Wb + X.cm), reinterpret_cast<const float*>(Wb + X.cl),
+                         reinterpret_cast<const float*>(Wb + X.cz), P + L.wuv, opart, W.JS, 2 * d.batch, out, s);
+    }
+    if (e == cudaSuccess && x.weights)
+      e = launch_row_weights(d, hdr, sched, pm, pl, reinterpret_cast<const float2*>(Wb + X.ml), scores, x.weights, x.add, s);
+    if (e != cudaSuccess) return cuda_fail(e, "combine phase");
+  } else if (phases & QSVD_PHASE_COMBINE) {
     if (combine_uses_gemv(d)) {
       float* zm = reinterpret_cast<float*>(Wb + W.zm);
       int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NTQ;
@@ -532,6 +570,38 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
   x.add = accumulate != 0;
   return decode_impl(*dims, packed, qin, qin_is_latent, cache, scales, lengths, num_splits, workspace,
                      workspace_bytes, out, QSVD_PHASE_ALL, static_cast<cudaStream_t>(stream), x);
+}
+
+qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, const float* qin, int qin_is_latent,
+                                    const void* prefix, const void* prefix_scales, int prefix_len, const void* cache,
+                                    const void* scales, const int32_t* lengths, int num_splits, void* workspace,
+                                    size_t* workspace_bytes, void* out, float* weights, int accumulate, void* stream) {
+  qsvd_status st = validate(dims);
+  if (st != QSVD_OK) return st;
+  const qsvd_dims& d = *dims;
+  if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
+  if (d.rope)
+    return fail(QSVD_ERR_UNSUPPORTED, "a shared prefix needs absorbed mode (no rotary embedding)");
+  if (prefix_len < 0 || (long long)d.batch * prefix_len > 0x7FFFFFFFLL)
+    return fail(QSVD_ERR_INVALID_ARG, "prefix_len (%d) must be >= 0 and batch x prefix_len below 2^31", prefix_len);
+  if (workspace && prefix_len > 0) {
+    if (!prefix || !aligned16(prefix)) return fail(QSVD_ERR_INVALID_ARG, "prefix must be given, 16-byte aligned");
+    if (cache_is_int(d) && (!prefix_scales || !aligned2(prefix_scales)))
+      return fail(QSVD_ERR_INVALID_ARG, "int caches need prefix_scales, 2-byte aligned");
+  }
+  if (weights && !aligned4(weights)) return fail(QSVD_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (split_simt_grid_heads(d) == 0 && (d.cache_dtype == QSVD_F32 || d.r % 64 || d.H > 128))
+    return fail(QSVD_ERR_UNSUPPORTED, "rank too large for the CUDA-core split kernel");
+  DecodeExtra x;
+  x.keep_scores = true;
+  x.weights = weights;
+  x.add = accumulate != 0;
+  x.shared = true;
+  x.prefix = prefix;
+  x.prefix_scales = prefix_scales;
+  x.prefix_len = prefix_len;
+  return decode_impl(d, packed, qin, qin_is_latent, cache, scales, lengths, num_splits, workspace, workspace_bytes, out,
+                     QSVD_PHASE_ALL, static_cast<cudaStream_t>(stream), x);
 }
 
 // Whether [a, a + na) and [b, b + nb) share a byte.

@@ -316,6 +316,36 @@ cudaError_t out_t(const qsvd_dims& d, const float* opart, int JS, void* out, cud
   return check_launch();
 }
 
+// V-up (and output projection) of the merged latents zm.
+template <typename WT, typename OT>
+cudaError_t vup_gemv_t(const qsvd_dims& d, const void* wuv, float* zm, float* vpart, int32_t* tickets,
+                       int32_t* status, void* out, const OutProj& op, cudaStream_t s) {
+  const WT* wo = static_cast<const WT*>(op.wo);
+  if (d.out_proj == QSVD_OUT_PROJ_FOLD) {
+    // out[b][n] = sum_{h, j} zm[b][h][j] F[h r + j][n]: the merged latents of
+    // all heads are one activation row of H r elements
+    const int K = d.H * d.r;
+    return launch_gemv<float, WT, OT>(zm, wo, op.ypart, d.batch, K, d.E, gemv_ksplit(K, d.weight_dtype),
+                                      static_cast<OT*>(out), op.ytickets, status, s);
+  }
+  // o[b][h d_h + n] = zm[b][h] . W^u_v[:, h d_h + n]: activation row of
+  // column group h (d_h columns) is zm + b H r + h r
+  const XGroups xg{(long long)d.H * d.r, d.d_h, d.r};
+  if (d.out_proj == QSVD_OUT_PROJ_CHAIN) {
+    const cudaError_t e =
+        launch_gemv<float, WT, float>(zm, static_cast<const WT*>(wuv), vpart, d.batch, d.r, d.E,
+                                      gemv_ksplit(d.r, d.weight_dtype), op.ow, tickets, status, s, xg);
+    if (e != cudaSuccess) return e;
+    // y = o W_O with o kept in fp32 (the GEMV splits it into two 16-bit parts)
+    return launch_gemv<float, WT, OT>(op.ow, wo, op.ypart, d.batch, d.E, d.E,
+                                      gemv_ksplit(d.E, d.weight_dtype), static_cast<OT*>(out), op.ytickets,
+                                      status, s);
+  }
+  return launch_gemv<float, WT, OT>(zm, static_cast<const WT*>(wuv), vpart, d.batch, d.r, d.E,
+                                    gemv_ksplit(d.r, d.weight_dtype), static_cast<OT*>(out), tickets,
+                                    status, s, xg);
+}
+
 template <typename WT, typename OT>
 cudaError_t merge_vup_t(const qsvd_dims& d, const WsHeader* hdr, const int32_t* sched,
                         const float* pm, const float* pl, const float* pz, const void* wuv,
@@ -333,31 +363,9 @@ cudaError_t merge_vup_t(const qsvd_dims& d, const WsHeader* hdr, const int32_t* 
     if (le != cudaSuccess) return le;
   }
   note_launch();
-  cudaError_t e = check_launch();
+  const cudaError_t e = check_launch();
   if (e != cudaSuccess) return e;
-  const WT* wo = static_cast<const WT*>(op.wo);
-  if (d.out_proj == QSVD_OUT_PROJ_FOLD) {
-    // out[b][n] = sum_{h, j} zm[b][h][j] F[h r + j][n]: the merged latents of
-    // all heads are one activation row of H r elements
-    const int K = d.H * d.r;
-    return launch_gemv<float, WT, OT>(zm, wo, op.ypart, d.batch, K, d.E, gemv_ksplit(K, d.weight_dtype),
-                                      static_cast<OT*>(out), op.ytickets, status, s);
-  }
-  // o[b][h d_h + n] = zm[b][h] . W^u_v[:, h d_h + n]: activation row of
-  // column group h (d_h columns) is zm + b H r + h r
-  const XGroups xg{(long long)d.H * d.r, d.d_h, d.r};
-  if (d.out_proj == QSVD_OUT_PROJ_CHAIN) {
-    e = launch_gemv<float, WT, float>(zm, static_cast<const WT*>(wuv), vpart, d.batch, d.r, d.E,
-                                      gemv_ksplit(d.r, d.weight_dtype), op.ow, tickets, status, s, xg);
-    if (e != cudaSuccess) return e;
-    // y = o W_O with o kept in fp32 (the GEMV splits it into two 16-bit parts)
-    return launch_gemv<float, WT, OT>(op.ow, wo, op.ypart, d.batch, d.E, d.E,
-                                      gemv_ksplit(d.E, d.weight_dtype), static_cast<OT*>(out), op.ytickets,
-                                      status, s);
-  }
-  return launch_gemv<float, WT, OT>(zm, static_cast<const WT*>(wuv), vpart, d.batch, d.r, d.E,
-                                    gemv_ksplit(d.r, d.weight_dtype), static_cast<OT*>(out), tickets,
-                                    status, s, xg);
+  return vup_gemv_t<WT, OT>(d, wuv, zm, vpart, tickets, status, out, op, s);
 }
 
 }  // namespace
@@ -387,6 +395,21 @@ cudaError_t launch_combine_gemv(const qsvd_dims& d, const WsHeader* hdr, const i
   if (d.weight_dtype == QSVD_BF16) { QSVD_MV(__nv_bfloat16) }
   if (d.weight_dtype == QSVD_F16) { QSVD_MV(__half) }
 #undef QSVD_MV
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_vup_gemv(const qsvd_dims& d, const void* wuv, float* zm, float* vpart, int32_t* tickets,
+                            int32_t* status, void* out, const OutProj& op, cudaStream_t s) {
+#define QSVD_VU(WT)                                                                                      \
+  switch (d.out_dtype) {                                                                                 \
+    case QSVD_F32: return vup_gemv_t<WT, float>(d, wuv, zm, vpart, tickets, status, out, op, s);         \
+    case QSVD_F16: return vup_gemv_t<WT, __half>(d, wuv, zm, vpart, tickets, status, out, op, s);        \
+    case QSVD_BF16: return vup_gemv_t<WT, __nv_bfloat16>(d, wuv, zm, vpart, tickets, status, out, op, s); \
+    default: return cudaErrorInvalidValue;                                                               \
+  }
+  if (d.weight_dtype == QSVD_BF16) { QSVD_VU(__nv_bfloat16) }
+  if (d.weight_dtype == QSVD_F16) { QSVD_VU(__half) }
+#undef QSVD_VU
   return cudaErrorInvalidValue;
 }
 

@@ -302,6 +302,8 @@ cudaError_t launch_combine_gemv(const qsvd_dims& d, const WsHeader* hdr, const i
                                 const float* pm, const float* pl, const float* pz, const void* wuv,
                                 float* zm, float* vpart, int32_t* tickets, int32_t* status, void* out,
                                 const OutProj& op, cudaStream_t s);
+cudaError_t launch_vup_gemv(const qsvd_dims& d, const void* wuv, float* zm, float* vpart, int32_t* tickets,
+                            int32_t* status, void* out, const OutProj& op, cudaStream_t s);   // after another merge
 cudaError_t launch_combine(const qsvd_dims& d, const WsHeader* hdr, const int32_t* sched,
                            const float* pm, const float* pl, const float* pz,
                            const void* wuv, float* opart, int JS, int P, void* out,

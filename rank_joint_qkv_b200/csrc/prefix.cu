@@ -1,0 +1,722 @@
+// Decode attention of a whole batch over a prefix that its sequences share
+// (absorbed query): the latent rows c_0 .. c_{P-1} are stored once, and all B
+// sequences' H heads read them in one pass as B H query rows,
+//
+//   S = Qt C^T  (B H x P, K = r)     P = 2^(S - m)     Z = P C  (B H x r, K = P)
+//
+// 4 B H r P flops for P r values read: with tens of sequences both products
+// are bound by the tensor cores, not by HBM as the per-sequence decode is.
+// The accumulator of Z alone is r columns per 128 query rows, three times
+// TMEM at r 1536, so the two products are two kernels with P between them
+// (16-bit, 2 B H P bytes: 8 MB at B 16, H 32, P 8192, within L2) rather than
+// one that keeps a tile's scores on chip:
+//
+//   k_prefix_gemm<scores>   128 query rows x 256 tokens per unit; the epilogue
+//                           (thread = query row) takes the tile's maximum,
+//                           writes 2^(s - ref) and keeps ref and the sum
+//   k_prefix_norm           per row and token split: the reference of the
+//                           split's tiles made one, m and l of the split
+//   k_prefix_gemm<values>   128 query rows x 256 channels per unit over a
+//                           split's tokens; float32 partials for the merge
+//
+// A tile's reference is its maximum rounded down to a multiple of 8 (log2
+// units): P <= 2^8 as in the split kernels, and neighbouring tiles mostly
+// share it, so k_prefix_norm rewrites few of them; where it does, the factor
+// is a power of two and the only loss is a fp16 subnormal's.
+//
+// Precision as in the split kernels: the query as two 16-bit parts (both
+// products accumulate in float32), P as two for bf16; a quantised prefix is
+// expanded to the fp16 hi and lo parts of code x scale (18 bits: exact), each
+// a pass of both products, so that the scores are as good as the integer ones
+// of the sequences' own rows.
+//
+// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM and the MMA thread,
+// warps 2-5 epilogue; two TMEM accumulators of 256 columns, so the epilogue
+// of a unit runs under the next one's products.  Every wait is bounded.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "internal.cuh"
+#include "prefix.cuh"
+#include "tc_common.cuh"
+
+namespace qsvd {
+namespace {
+
+constexpr int kPxThreads = 192;
+constexpr int kPxA = 128 * 128;            // A box: 128 rows x 64 K x 2 bytes
+constexpr int kPxB = 256 * 128;            // B: 256 N x 64 K x 2 bytes
+constexpr int kPxMaxSlots = 4;
+constexpr int kPxSmem = 232448;            // opt-in dynamic shared memory per block on sm_100
+
+template <int AP>
+__host__ __device__ constexpr int px_slot() { return AP * kPxA + kPxB; }
+template <int AP>
+__host__ __device__ constexpr int px_slots() { return AP == 2 ? 3 : 4; }
+
+struct PxArgs {
+  int B, H, r, plen, nb, MB, tiles, ppad, SP;
+  void* p;        // [AP parts][MB 128][ppad] P (scores: written)
+  float* mt;      // [tiles][MB 128] reference of a tile
+  float* lt;      // [tiles][MB 128] sum of its P
+  float* pz;      // [SP B][H][r] (values: written)
+  float gain;     // on the scores (see launch_prefix)
+  int32_t* status;
+};
+
+// Tiles [t0, t1) of token split sp.
+__device__ __forceinline__ int split_tile(int sp, int tiles, int SP) { return int((long long)sp * tiles / SP); }
+
+// AP: 16-bit parts of A in pass 0 (a second pass, for the lo part of an
+// expanded prefix, takes A's first part only).  CP: passes (parts of C).
+// PS: parts of P that the scores' epilogue writes.
+template <bool BF16, int AP, int CP, int PS, bool VALUES>
+__global__ void __launch_bounds__(kPxThreads, 1)
+k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
+              const __grid_constant__ CUtensorMap tm_b1, const PxArgs g) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  constexpr int kSlot = px_slot<AP>(), ns = px_slots<AP>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + size_t(ns) * kSlot);
+  uint64_t* full = bars;                    // [kPxMaxSlots]
+  uint64_t* empty = bars + kPxMaxSlots;     // [kPxMaxSlots]
+  uint64_t* afull = bars + 2 * kPxMaxSlots; // [2] accumulator complete
+  uint64_t* aempty = afull + 2;             // [2] accumulator read by the epilogue
+  uint64_t* drain = aempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NB = VALUES ? (g.r + 255) / 256 : g.tiles;       // column blocks of the product
+  const int units = g.MB * NB * (VALUES ? g.SP : 1);
+  const int mine = units > int(blockIdx.x) ? (units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
+  if (mine == 0) return;   // uniform across the CTA
+  // unit u: row block u % MB, so that the blocks in flight share their B tiles in L2
+  auto unit = [&](int j, int* mb, int* n, int* sp, int* k0, int* k1) {
+    const int u = int(blockIdx.x) + j * int(gridDim.x);
+    *mb = u % g.MB;
+    *n = (u / g.MB) % NB;
+    *sp = (u / g.MB) / NB;
+    if (VALUES) {   // 64-token blocks of the split's tiles
+      *k0 = 4 * split_tile(*sp, g.tiles, g.SP);
+      *k1 = min(4 * split_tile(*sp + 1, g.tiles, g.SP), (g.plen + 63) / 64);
+    } else {
+      *k0 = 0;
+      *k1 = g.r / 64;
+    }
+  };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ns; ++i) {
+      mbar_init(saddr(&full[i]), 1);
+      mbar_init(saddr(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(saddr(&afull[i]), 1);
+      mbar_init(saddr(&aempty[i]), 1);
+    }
+    mbar_init(saddr(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     saddr(tmem_holder))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t ring0 = saddr(base);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    Ring rg(ns);
+    long long k = 0;
+    bool ok = true;
+    for (int j = 0; j < mine && ok; ++j) {
+      int mb, n, sp, k0, k1;
+      unit(j, &mb, &n, &sp, &k0, &k1);
+      for (int pass = 0; pass < CP && ok; ++pass) {
+        const int parts = pass == 0 ? AP : 1;
+        const uint32_t abytes = uint32_t(VALUES ? kPxA : g.nb * g.H * 128);
+        for (int ki = k0; ki < k1; ++ki) {
+          if (!__all_sync(0xffffffffu, mbar_wait(saddr(&empty[rg.slot]), rg.phase ^ 1u))) { ok = false; break; }
+          const uint32_t dst = ring0 + uint32_t(rg.slot) * kSlot;
+          const uint32_t fb = saddr(&full[rg.slot]);
+          if (lane == 0) mbar_expect_tx(fb, parts * abytes + uint32_t(kPxB));
+          __syncwarp();
+          const int ln = int(k % 10) * 3;   // rotating issuing lanes, one per operation
+          if (lane >= ln && lane < ln + parts) {
+            const int part = lane - ln;
+            if (VALUES) tma_load_3d(dst + part * kPxA, &tm_a, 64 * ki, mb * 128, part, fb);
+            else tma_load_4d(dst + part * kPxA, &tm_a, 64 * ki, 0, part, mb * g.nb, fb);
+          }
+          if (lane == ln + 2) {
+            const CUtensorMap* tb = pass == 0 ? &tm_b0 : &tm_b1;
+            if (VALUES) tma_load_3d(dst + AP * kPxA, tb, 0, 64 * ki, 4 * n, fb);
+            else tma_load_2d(dst + AP * kPxA, tb, 64 * ki, kPxTile * n, fb);
+          }
+          __syncwarp();
+          rg.advance();
+          ++k;
+        }
+      }
+      if (__any_sync(0xffffffffu, *abort_flag)) ok = false;
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(g.status, QSVD_STATUS_TIMEOUT);
+      for (long long kk = (k > ns ? k - ns : 0); kk < k; ++kk)
+        mbar_wait(saddr(&full[int(kk % ns)]), uint32_t(kk / ns) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f16(128, 256, BF16, false, VALUES);   // values: C is the MN-major operand
+      const uint64_t da0 = sdesc(ring0, 16, 1024);                          // K-major
+      const uint64_t db0 = sdesc(ring0 + AP * kPxA, VALUES ? 64 * 128 : 16, 1024);
+      constexpr int kBStep = VALUES ? 16 * 128 : 32;                        // 16 tokens, or 16 channels
+      Ring rg(ns);
+      bool ok = true;
+      for (int j = 0; j < mine && ok; ++j) {
+        int mb, n, sp, k0, k1;
+        unit(j, &mb, &n, &sp, &k0, &k1);
+        const int ab = j & 1;
+        if (j >= 2 && !mbar_wait(saddr(&aempty[ab]), uint32_t((j - 2) >> 1) & 1u)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(ab * 256);
+        uint32_t acc = 0;
+        for (int pass = 0; pass < CP && ok; ++pass) {
+          const int parts = pass == 0 ? AP : 1;
+          for (int ki = k0; ki < k1; ++ki) {
+            if (!mbar_wait(saddr(&full[rg.slot]), rg.phase)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t off = uint64_t((rg.slot * kSlot) >> 4);
+            for (int part = 0; part < parts; ++part) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {   // K = 16 per MMA
+                tc_mma(d, da0 + off + uint64_t((part * kPxA + kk * 32) >> 4), db0 + off + uint64_t((kk * kBStep) >> 4), id,
+                       acc);
+                acc = 1;
+              }
+            }
+            tc_commit(saddr(&empty[rg.slot]));
+            rg.advance();
+          }
+        }
+        if (!ok) break;
+        tc_commit(saddr(&afull[ab]));
+        if (*abort_flag) ok = false;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(g.status, QSVD_STATUS_TIMEOUT);
+      }
+      tc_commit(saddr(drain));
+      mbar_wait(saddr(drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    const int q = warp & 3;
+    const int t = 32 * q + lane;   // query row of the block == TMEM lane
+    const uint32_t lane_off = uint32_t(32 * q) << 16;
+    const int seq = t / g.H, head = t - seq * g.H;
+    const size_t rows = size_t(g.MB) * 128;
+    for (int j = 0; j < mine; ++j) {
+      int mb, n, sp, k0, k1;
+      unit(j, &mb, &n, &sp, &k0, &k1);
+      const int ab = j & 1;
+      const int fail = group_or(!mbar_wait(saddr(&afull[ab]), uint32_t(j >> 1) & 1u));
+      if (fail) {
+        if (t == 0) { *abort_flag = 1; atomicOr(g.status, QSVD_STATUS_TIMEOUT); }
+        break;
+      }
+      tc_fence_after();
+      const int b = mb * g.nb + seq;
+      const bool live = seq < g.nb && b < g.B;
+      const uint32_t ta = tmem + lane_off + uint32_t(ab * 256);
+      if (VALUES) {
+        float* z = g.pz + ((size_t(sp) * g.B + b) * g.H + head) * g.r + size_t(n) * 256;
+        const int nc = min(256, g.r - n * 256);   // a multiple of 64
+#pragma unroll 1
+        for (int c = 0; c < nc; c += 32) {
+          float v[32];
+          tmem_ld16(ta + uint32_t(c), v);
+          tmem_ld16(ta + uint32_t(c + 16), v + 16);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(z + c)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        }
+      } else {
+        const int nv = min(kPxTile, g.plen - n * kPxTile);   // tokens of the tile, >= 1
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kPxTile; c += 32) {
+          float v[32];
+          tmem_ld16(ta + uint32_t(c), v);
+          tmem_ld16(ta + uint32_t(c + 16), v + 16);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = c + e < nv ? fmaxf(mx, v[e]) : mx;
+        }
+        const float ref = 8.f * floorf(mx * g.gain * 0.125f);
+        float sum = 0.f;
+        T16* prow = static_cast<T16*>(g.p) + (size_t(mb) * 128 + t) * g.ppad + size_t(n) * kPxTile;
+#pragma unroll 1
+        for (int c = 0; c < kPxTile; c += 32) {
+          float v[32];
+          tmem_ld16(ta + uint32_t(c), v);
+          tmem_ld16(ta + uint32_t(c + 16), v + 16);
+          tmem_wait_ld();
+          uint4 hi[4], lo[4];
+          T16* hv = reinterpret_cast<T16*>(hi);
+          T16* lv = reinterpret_cast<T16*>(lo);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p = c + e < nv ? exp2f(fmaf(v[e], g.gain, -ref)) : 0.f;
+            sum += p;
+            hv[e] = dev::from_f<T16>(p);
+            if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(prow + c)[e] = hi[e];
+            if (PS == 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(prow + rows * g.ppad + c)[e] = lo[e];
+            }
+          }
+        }
+        if (live) {
+          g.mt[size_t(n) * rows + size_t(mb) * 128 + t] = ref;
+          g.lt[size_t(n) * rows + size_t(mb) * 128 + t] = sum;
+        }
+      }
+      tc_fence_before();
+      group_sync();
+      if (t == 0) mbar_arrive(saddr(&aempty[ab]));
+      if (group_or(*abort_flag)) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// One warp per (query row, token split): m = the largest reference of the
+// split's tiles, l = their sums brought to it, and P of the tiles with a lower
+// one scaled to it.  grid (B H / 8 rounded up, SP), block 256.
+template <typename T16, int PS>
+__global__ void __launch_bounds__(256)
+k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __restrict__ lt, float* __restrict__ pm,
+              float* __restrict__ pl, int B, int H, int nb, int MB, int tiles, int ppad, int SP) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long bh = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (bh >= (long long)B * H) return;
+  const int b = int(bh / H), h = int(bh % H), sp = blockIdx.y;
+  const size_t rows = size_t(MB) * 128, row = size_t(b / nb) * 128 + size_t(b % nb) * H + h;
+  const int t0 = split_tile(sp, tiles, SP), t1 = split_tile(sp + 1, tiles, SP);
+  float m = -INFINITY;
+  for (int t = t0 + lane; t < t1; t += 32) m = fmaxf(m, __ldcg(mt + size_t(t) * rows + row));
+  m = dev::warp_max(m);
+  float l = 0.f;
+  for (int tb = t0; tb < t1; tb += 32) {
+    const int t = tb + lane;
+    const float f = t < t1 ? exp2f(__ldcg(mt + size_t(t) * rows + row) - m) : 1.f;   // a power of two
+    if (t < t1) l += f * __ldcg(lt + size_t(t) * rows + row);
+    unsigned lower = __ballot_sync(0xffffffffu, f != 1.f);
+    while (lower) {
+      const int i = __ffs(lower) - 1;
+      lower &= lower - 1;
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+      for (int part = 0; part < PS; ++part) {
+        uint4* v = reinterpret_cast<uint4*>(p + (part * rows + row) * ppad + size_t(tb + i) * kPxTile) + lane;
+        uint4 x = __ldcg(v);
+        T16* e = reinterpret_cast<T16*>(&x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = dev::from_f<T16>(dev::to_f(e[k]) * fi);
+        *v = x;
+      }
+    }
+  }
+  l = dev::warp_sum(l);
+  if (lane == 0) {
+    pm[(size_t(sp) * B + b) * H + h] = m;
+    pl[(size_t(sp) * B + b) * H + h] = l;
+  }
+}
+
+// Quantised prefix -> fp16 hi and lo parts of code x scale, [2][P][r].
+// Thread = one 16-byte vector of codes.
+template <qsvd_dtype CT>
+__global__ void __launch_bounds__(256)
+k_prefix_expand(const uint8_t* __restrict__ codes, const __half* __restrict__ scales, __half* __restrict__ out,
+                int plen, int r, int group) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  constexpr int N = dev::CacheVec<CT>::N;
+  const int vpr = r / N;
+  const size_t total = size_t(plen) * vpr, part = size_t(plen) * r;
+  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += size_t(gridDim.x) * 256) {
+    const size_t t = i / vpr;
+    const int j0 = int(i % vpr) * N;
+    const float s = __half2float(scales[t * (r / group) + j0 / group]);
+    float v[N];
+    dev::CacheVec<CT>::load(codes + t * (size_t(r) * (CT == QSVD_I4 ? 1 : 2) / 2), j0, s, v);
+    __half* o = out + t * r + j0;
+#pragma unroll
+    for (int e0 = 0; e0 < N; e0 += 8) {
+      uint4 hi, lo;
+      __half* hv = reinterpret_cast<__half*>(&hi);
+      __half* lv = reinterpret_cast<__half*>(&lo);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        hv[e] = __float2half_rn(v[e0 + e]);
+        lv[e] = __float2half_rn(v[e0 + e] - __half2float(hv[e]));
+      }
+      *reinterpret_cast<uint4*>(o + e0) = hi;
+      *reinterpret_cast<uint4*>(o + part + e0) = lo;
+    }
+  }
+}
+
+// Schedules that need no lengths: the prefix as B sequences of plen rows
+// (CUDA cores), and one tile per sequence for the combine of merged slots.
+__global__ void __launch_bounds__(256)
+k_prefix_schedule(int32_t* __restrict__ sched, int32_t* __restrict__ csched, WsHeader* __restrict__ hdr, int B,
+                  int plen) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  const int nt = (plen + kTile - 1) / kTile;
+  for (int i = threadIdx.x; i <= B; i += 256) {
+    sched[i] = i * nt;
+    csched[i] = i;
+    if (i < B) {
+      sched[B + 1 + i] = plen;
+      csched[B + 1 + i] = 1;
+    }
+  }
+  if (threadIdx.x == 0) {
+    hdr->status = 0;
+    hdr->G = B;
+    hdr->tile = kTile;
+    hdr->kernel = 0;
+  }
+}
+
+// The merge of combine.cu with the prefix's partials beside the own splits'.
+// grid (ceil(r / 512), H, B), block 128.
+struct MergeIn {
+  const float *pm, *pl, *pz;   // own: slot c + b of split c
+  const int32_t* sched;
+  const float *xm, *xl, *xz;   // prefix: slot sp B + b (n = SP), or slot c + b of schedule xsched, G xg
+  const int32_t* xsched;
+  int n, xg;
+};
+
+__global__ void __launch_bounds__(128)
+k_merge_shared(const WsHeader* __restrict__ hdr, const MergeIn in, float* __restrict__ zout, float* __restrict__ cm,
+               float* __restrict__ cl, float2* __restrict__ ml, int B, int H, int r, const uint8_t* __restrict__ pf,
+               unsigned long long pf_bytes) {
+  // the following GEMV's weights towards L2 (constant; a hint)
+  if (pf_bytes && threadIdx.x == 32) dev::l2_prefetch_share(pf, pf_bytes);
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  __shared__ float wt[2][kMaxSplits];
+  __shared__ int range[2][2];
+  const int ch = blockIdx.x * 512 + 4 * threadIdx.x;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    const long long G = hdr->G, T = in.sched[B];
+    int c0[2] = {0, 0}, c1[2] = {-1, -1};
+    if (in.sched[b + 1] > in.sched[b]) {
+      c0[0] = int(dev::split_of_tile(in.sched[b], G, T));
+      c1[0] = int(dev::split_of_tile(in.sched[b + 1] - 1, G, T));
+    }
+    const long long XG = in.xg, XT = in.xsched ? in.xsched[B] : 0;
+    if (in.xsched) {
+      c0[1] = int(dev::split_of_tile(in.xsched[b], XG, XT));
+      c1[1] = int(dev::split_of_tile(in.xsched[b + 1] - 1, XG, XT));
+    } else {
+      c1[1] = in.n - 1;
+    }
+    // split c of source k: its place in the partials, or -1 when it is empty
+    auto place = [&](int k, int c) -> long long {
+      if (k == 0) return dev::split_begin(c, G, T) == dev::split_begin(c + 1, G, T) ? -1 : ((long long)c + b) * H + h;
+      if (!in.xsched) return ((long long)c * B + b) * H + h;
+      return dev::split_begin(c, XG, XT) == dev::split_begin(c + 1, XG, XT) ? -1 : ((long long)c + b) * H + h;
+    };
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      for (int c = c0[k] + lane; c <= c1[k]; c += 32) {
+        const long long at = place(k, c);
+        if (at >= 0) M = fmaxf(M, __ldcg((k ? in.xm : in.pm) + at));
+      }
+    M = dev::warp_max(M);
+    float L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      for (int c = c0[k] + lane; c <= c1[k]; c += 32) {
+        const long long at = place(k, c);
+        float w = 0.f;
+        if (at >= 0) {
+          w = exp2f(__ldcg((k ? in.xm : in.pm) + at) - M);
+          L += w * __ldcg((k ? in.xl : in.pl) + at);
+        }
+        wt[k][c - c0[k]] = w;
+      }
+    L = dev::warp_sum(L);
+    const float invL = L > 0.f ? 1.f / L : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      for (int c = c0[k] + lane; c <= c1[k]; c += 32) wt[k][c - c0[k]] *= invL;
+      if (lane == 0) { range[k][0] = c0[k]; range[k][1] = c1[k]; }
+    }
+    if (lane == 0 && blockIdx.x == 0) {
+      ml[size_t(b) * H + h] = make_float2(M, invL);
+      if (cm) {   // one slot per sequence (2 b), merged already
+        cm[size_t(2 * b) * H + h] = 0.f;
+        cl[size_t(2 * b) * H + h] = 1.f;
+      }
+    }
+  }
+  __syncthreads();
+  if (ch >= r) return;
+  float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int c0 = range[k][0], c1 = range[k][1];
+    const bool rowwise = k == 1 && !in.xsched;
+    const float* base = (k ? in.xz : in.pz) + size_t(h) * r + ch;
+    for (int cb = c0; cb <= c1; cb += 8) {   // eight splits' loads in flight, added in split order
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const size_t slot = rowwise ? size_t(cb + i) * B + b : size_t(cb + i) + b;
+        v[i] = cb + i <= c1 && wt[k][cb + i - c0] != 0.f
+                   ? __ldcg(reinterpret_cast<const float4*>(base + slot * H * r))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = cb + i <= c1 ? wt[k][cb + i - c0] : 0.f;
+        z.x = fmaf(w, v[i].x, z.x); z.y = fmaf(w, v[i].y, z.y);
+        z.z = fmaf(w, v[i].z, z.z); z.w = fmaf(w, v[i].w, z.w);
+      }
+    }
+  }
+  *reinterpret_cast<float4*>(zout + (size_t(cm ? 2 * b : b) * H + h) * r + ch) = z;
+}
+
+// ------------------------------------------------------------------ host
+
+bool encode(CUtensorMap* tm, bool bf16, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  TensorMapEncode enc = tensor_map_encoder();
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  memset(tm, 0, sizeof(*tm));
+  return enc && enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, cuuint32_t(rank),
+                    const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int AP, int CP, int PS, bool VALUES>
+cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, int sms,
+                   cudaStream_t s) {
+  const long long units = (long long)g.MB * (VALUES ? (long long)((g.r + 255) / 256) * g.SP : g.tiles);
+  if (units > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  const int grid = units < sms ? int(units) : sms;
+  const size_t smem = 1024 + size_t(px_slots<AP>()) * px_slot<AP>() + (2 * kPxMaxSlots + 5) * 8 + 16;
+  static_assert(1024 + px_slots<AP>() * px_slot<AP>() + (2 * kPxMaxSlots + 5) * 8 + 16 <= kPxSmem, "ring fits");
+  auto kern = k_prefix_gemm<BF16, AP, CP, PS, VALUES>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kPxThreads), smem, s, ta, tb0, tb1, g);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return check_launch();
+}
+
+// C parts: CP copies of [plen][r] 16-bit rows at `c`, one after another.
+template <bool BF16, int CP>
+cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* c, const void* qt16, float gain,
+                   int sms, int32_t* status, cudaStream_t s) {
+  constexpr int PS = BF16 ? 2 : 1;
+  using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  const cuuint64_t r = cuuint64_t(d.r), P = cuuint64_t(L.plen), rows = cuuint64_t(L.MB) * 128, ppad = cuuint64_t(L.ppad);
+  CUtensorMap tq, tp, tbs[2], tbv[2];
+  {
+    // query parts [B][2][H][r] as {channel, head, part, sequence}: one box is a block's rows of one part
+    const cuuint64_t dims[4] = {r, cuuint64_t(d.H), 2, cuuint64_t(d.batch)};
+    const cuuint64_t strides[3] = {r * 2, cuuint64_t(d.H) * r * 2, 2 * cuuint64_t(d.H) * r * 2};
+    const cuuint32_t box[4] = {64, cuuint32_t(d.H), 1, cuuint32_t(L.nb)};
+    if (!encode(&tq, BF16, 4, qt16, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    // P [PS][MB 128][ppad] as {token, row, part}
+    const cuuint64_t dims[3] = {ppad, rows, cuuint64_t(PS)};
+    const cuuint64_t strides[2] = {ppad * 2, rows * ppad * 2};
+    const cuuint32_t box[3] = {64, 128, 1};
+    if (!encode(&tp, BF16, 3, ws + L.p, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  for (int part = 0; part < 2; ++part) {
+    const uint8_t* cp = static_cast<const uint8_t*>(c) + (part < CP ? size_t(part) * L.plen * d.r * 2 : 0);
+    const cuuint64_t sd[2] = {r, P}, ss[1] = {r * 2};   // scores: 256 tokens x 64 channels, K-major; rows past P zeros
+    const cuuint32_t sb[2] = {64, kPxTile};
+    const cuuint64_t vd[3] = {64, P, r / 64}, vs[2] = {r * 2, 128};   // values: 64 tokens x 256 channels, MN-major
+    const cuuint32_t vb[3] = {64, 64, 4};
+    if (!encode(&tbs[part], BF16, 2, cp, sd, ss, sb) || !encode(&tbv[part], BF16, 3, cp, vd, vs, vb))
+      return cudaErrorInvalidValue;
+  }
+  PxArgs g{d.batch, d.H, d.r, L.plen, L.nb, L.MB, L.tiles, L.ppad, L.SP, ws + L.p,
+           reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pz),
+           gain, status};
+  cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, sms, s);
+  if (e != cudaSuccess) return e;
+  const long long bh = (long long)d.batch * d.H;
+  e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned((bh + 7) / 8), unsigned(L.SP)), dim3(256), 0, s,
+                 reinterpret_cast<T16*>(ws + L.p), g.mt, g.lt, reinterpret_cast<float*>(ws + L.pm),
+                 reinterpret_cast<float*>(ws + L.pl), d.batch, d.H, L.nb, L.MB, L.tiles, L.ppad, L.SP);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  if ((e = check_launch()) != cudaSuccess) return e;
+  return gemm_t<BF16, PS, CP, PS, true>(tp, tbv[0], tbv[1], g, sms, s);
+}
+
+}  // namespace
+
+PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
+  PrefixLayout L{};
+  const bool q = cache_is_int(d);
+  L.plen = plen;
+  L.fast = d.kernel != QSVD_KERNEL_SIMT && d.cache_dtype != QSVD_F32 && d.r % 64 == 0 && d.H <= 128;
+  const size_t B = size_t(d.batch), H = size_t(d.H), r = size_t(d.r), P = size_t(plen);
+  size_t o = base;
+  L.ml = o; o = align256(o + B * H * 8);
+  L.sched = o; o = align256(o + (2 * B + 1) * 4);
+  L.csched = o; o = align256(o + (2 * B + 1) * 4);
+  L.hdr = o; o = align256(o + sizeof(WsHeader));
+  if (!combine_uses_gemv(d)) {   // merged slots for the CUDA-core combine
+    L.cm = o; o = align256(o + 2 * B * H * 4);
+    L.cl = o; o = align256(o + 2 * B * H * 4);
+    L.cz = o; o = align256(o + 2 * B * H * r * 4);
+  }
+  if (plen == 0) { L.total = o; return L; }
+  if (L.fast) {
+    L.tiles = (plen + kPxTile - 1) / kPxTile;
+    L.nb = 128 / d.H;
+    if (L.nb > d.batch) L.nb = d.batch;
+    L.MB = (d.batch + L.nb - 1) / L.nb;
+    L.ppad = L.tiles * kPxTile;
+    // token splits of the value product: the fewest that come within 3% of
+    // the best fill of the GPU's waves (a split costs B H r float32 partials,
+    // written and merged)
+    const long long units = (long long)L.MB * ((d.r + 255) / 256);
+    double best = 1e30;
+    for (int pass = 0; pass < 2; ++pass)
+      for (int sp = 1; sp <= 16 && sp <= L.tiles; ++sp) {
+        const double cost = double((units * sp + sms - 1) / sms) / sp;
+        if (pass == 0 && cost < best) best = cost;
+        if (pass == 1 && cost <= best * 1.03) { L.SP = sp; break; }
+      }
+    L.slots = L.SP * d.batch;
+    if (q) { L.qt16 = o; o = align256(o + 2 * B * H * r * 2); }   // beside the int8 parts
+    if (q) { L.cparts = o; o = align256(o + 2 * P * r * 2); }
+    const size_t rows = size_t(L.MB) * 128;
+    L.p = o; o = align256(o + (d.cache_dtype == QSVD_BF16 ? 2 : 1) * rows * L.ppad * 2);
+    L.mt = o; o = align256(o + size_t(L.tiles) * rows * 4);
+    L.lt = o; o = align256(o + size_t(L.tiles) * rows * 4);
+  } else {
+    const long long t = (long long)d.batch * ((plen + kTile - 1) / kTile);
+    const int hb = split_simt_grid_heads(d);
+    long long G = hb > 0 ? (2LL * sms + hb - 1) / hb : sms;
+    if (G > t) G = t;
+    if (G > kMaxSplits) G = kMaxSplits;
+    L.G = int(G < 1 ? 1 : G);
+    L.slots = L.G + d.batch;
+  }
+  L.pm = o; o = align256(o + size_t(L.slots) * H * 4);
+  L.pl = o; o = align256(o + size_t(L.slots) * H * 4);
+  L.pz = o; o = align256(o + size_t(L.slots) * H * r * 4);
+  L.total = o;
+  return L;
+}
+
+cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                          const void* scales, const void* qt16, const float* qt32, float gain, int sms, int32_t* status,
+                          cudaStream_t s) {
+  if (!L.fast) {
+    // the CUDA-core split kernel with the same rows for every sequence: no
+    // stride between sequences
+    qsvd_dims v = d;
+    v.max_len = 0;
+    return launch_split_simt_absorbed(v, qt32, prefix, scales, reinterpret_cast<const int32_t*>(ws + L.sched), L.G,
+                                      reinterpret_cast<float*>(ws + L.pm), reinterpret_cast<float*>(ws + L.pl),
+                                      reinterpret_cast<float*>(ws + L.pz), s);
+  }
+  if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
+  if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
+  const size_t vecs = size_t(L.plen) * cache_row_bytes(d) / 16;
+  const unsigned grid = unsigned(vecs / 256 + 1 < size_t(sms) * 8 ? vecs / 256 + 1 : size_t(sms) * 8);
+  cudaError_t e = launch_pdl(d.cache_dtype == QSVD_I8 ? k_prefix_expand<QSVD_I8> : k_prefix_expand<QSVD_I4>, dim3(grid),
+                             dim3(256), 0, s, static_cast<const uint8_t*>(prefix), static_cast<const __half*>(scales),
+                             reinterpret_cast<__half*>(ws + L.cparts), L.plen, d.r, d.group);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  if ((e = check_launch()) != cudaSuccess) return e;
+  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, status, s);
+}
+
+int prefix_score_steps(const qsvd_dims& d) { return d.r / 16 * (cache_is_int(d) ? 3 : 2); }
+
+cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s) {
+  cudaError_t e = launch_pdl(k_prefix_schedule, dim3(1), dim3(256), 0, s, reinterpret_cast<int32_t*>(ws + L.sched),
+                             reinterpret_cast<int32_t*>(ws + L.csched), reinterpret_cast<WsHeader*>(ws + L.hdr), d.batch,
+                             L.plen);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return check_launch();
+}
+
+cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr,
+                                const int32_t* sched, const float* pm, const float* pl, const float* pz, float* zm,
+                                bool slots, const void* next_weights, size_t next_bytes, cudaStream_t s) {
+  const float* xm = reinterpret_cast<const float*>(ws + L.pm);
+  const bool listed = L.plen > 0 && !L.fast;
+  const MergeIn in{pm, pl, pz, sched, xm, reinterpret_cast<const float*>(ws + L.pl),
+                   reinterpret_cast<const float*>(ws + L.pz),
+                   listed ? reinterpret_cast<const int32_t*>(ws + L.sched) : nullptr, L.plen > 0 ? L.SP : 0, L.G};
+  cudaError_t e = launch_pdl(k_merge_shared, dim3(unsigned((d.r + 511) / 512), unsigned(d.H), unsigned(d.batch)),
+                             dim3(128), 0, s, hdr, in, slots ? reinterpret_cast<float*>(ws + L.cz) : zm,
+                             slots ? reinterpret_cast<float*>(ws + L.cm) : nullptr,
+                             slots ? reinterpret_cast<float*>(ws + L.cl) : nullptr, reinterpret_cast<float2*>(ws + L.ml),
+                             d.batch, d.H, d.r, static_cast<const uint8_t*>(next_weights),
+                             (unsigned long long)next_bytes);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return check_launch();
+}
+
+}  // namespace qsvd

@@ -1,0 +1,39 @@
+// Workspace and launchers of the shared-prefix decode (prefix.cu), used by
+// the C-ABI layer.
+#pragma once
+
+#include "internal.cuh"
+
+namespace qsvd {
+
+constexpr int kPxTile = 256;   // tokens per score tile
+
+// Sections behind the decode's own workspace.
+struct PrefixLayout {
+  bool fast;        // tensor cores; else the CUDA-core split kernel on B views of the prefix
+  int plen, tiles;  // prefix rows, score tiles
+  int nb, MB;       // sequences per block of 128 query rows, blocks
+  int ppad;         // tokens per row of P (tiles x 256)
+  int SP;           // token splits of the value product
+  int G;            // CUDA cores: split CTAs
+  int slots;        // partials (fast: SP x B; CUDA cores: G + B)
+  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, total;
+};
+PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
+
+// The prefix's partials (m, l, z per slot) from the absorbed query: qt16 its
+// 16-bit parts [B][2][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
+// the tensor cores' scores, for what their accumulation truncates.
+cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                          const void* scales, const void* qt16, const float* qt32, float gain, int sms, int32_t* status,
+                          cudaStream_t s);
+cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
+// Accumulations that a score of the tensor-core path takes.
+int prefix_score_steps(const qsvd_dims& d);
+// Merge of the own splits' and the prefix's partials: zm [B][H][r], or (slots
+// != 0) one slot per sequence for launch_combine; ml {M, 1 / L} [B][H].
+cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr,
+                                const int32_t* sched, const float* pm, const float* pl, const float* pz, float* zm,
+                                bool slots, const void* next_weights, size_t next_bytes, cudaStream_t s);
+
+}  // namespace qsvd

@@ -77,6 +77,7 @@ class Layer:
         wq, wk, wv = (w.to(f64) for w in (self.wuq, self.wuk, self.wuv))
         H, d_h, tau = self.H, self.d_h, self.d_h ** -0.5
         out = torch.zeros(self.B, self.E, dtype=f64, device=DEV)
+        self.spread = torch.zeros_like(out)   # sum_t p_t |v_t|, for the rounding of p
         w = torch.zeros(self.B, self.max_len, dtype=f64, device=DEV)
         u = max(PARTS[self.weight], PARTS["bf16"] if self.cache.dtype == torch.bfloat16 else 0.0) + \
             (self.r + self.d_h) * 2.0 ** -24
@@ -99,6 +100,7 @@ class Layer:
                 qb, k = turn(qb, cos[n - 1], sin[n - 1]), turn(k, cos, sin)
             p = torch.softmax(torch.einsum("thd,hd->th", k, qb) * tau, 0)
             out[b] = torch.einsum("th,thd->hd", p, v).reshape(-1)
+            self.spread[b] = torch.einsum("th,thd->hd", p, v.abs()).reshape(-1)
             w[b, :n] = p[P:].sum(1)
         if wo is not None:
             out = out @ wo.to(f64)

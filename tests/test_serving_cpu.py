@@ -111,3 +111,32 @@ def test_weight_keys_keep_the_order():
     assert key([np.nan, -np.nan]).tolist() == [0, 0] and key([-0.0]) == key([0.0])
     src = open(q.LIB_PATH.replace("libqsvd.so", "csrc/evict.cu")).read()
     assert "return (u & 0x80000000u) ? ~u : (u | 0x80000000u);" in src and "if (isnan(w)) return 0u;" in src
+
+
+def shared_call(d, plen=100, splits=4, prefix=OK, prefix_scales=None, workspace=OK, ws_bytes=1 << 40, weights=None, cache=OK,
+                scales=None, out=OK, qin=OK, packed=OK, lengths=OK):
+    n = ctypes.c_size_t(ws_bytes)
+    p = lambda v: None if v is None else ctypes.c_void_p(v)  # noqa: E731
+    return lambda: q._lib.qsvd_decode_attn_shared(ctypes.byref(d), p(packed), p(qin), 1, p(prefix), p(prefix_scales), plen,
+                                                  p(cache), p(scales), p(lengths), splits, p(workspace), ctypes.byref(n),
+                                                  p(out), p(weights), 1, None)
+
+
+def test_shared_refusals():
+    d = dims()
+    bad = q.QSVD_ERR_INVALID_ARG
+    refused(shared_call(dims(rope=True)), q.QSVD_ERR_UNSUPPORTED, "absorbed mode")
+    refused(shared_call(d, plen=-1), bad, "prefix_len")
+    refused(shared_call(d, plen=1 << 30), bad, "below 2^31")
+    refused(shared_call(d, prefix=None), bad, "prefix must be given")
+    refused(shared_call(d, prefix=OK + 8), bad, "16-byte aligned")
+    refused(shared_call(dims(cache="i8"), scales=OK), bad, "prefix_scales")
+    refused(shared_call(dims(cache="i8"), scales=OK, prefix_scales=OK + 1), bad, "2-byte")
+    refused(shared_call(dims(cache="i8"), prefix_scales=OK), bad, "int caches need scales")
+    refused(shared_call(d, weights=OK + 1), bad, "4-byte aligned")
+    refused(shared_call(d, ws_bytes=q.decode_shared_workspace_bytes(d, 100, 4) - 1), q.QSVD_ERR_WORKSPACE, "workspace holds")
+    for k in ("cache", "lengths", "packed", "qin", "out"):
+        refused(shared_call(d, **{k: None}), bad, "NULL")
+    refused(shared_call(d, splits=-1), bad, "num_splits")
+    refused(shared_call(dims(d_h=24, H=8, E=192, r=128, out_proj="chain")), q.QSVD_ERR_UNSUPPORTED, "output projection")
+    assert q.decode_shared_workspace_bytes(d, 0, 4) < q.decode_shared_workspace_bytes(d, 1, 4)

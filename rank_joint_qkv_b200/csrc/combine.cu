@@ -236,7 +236,9 @@ k_combine_vup(const WsHeader* __restrict__ hdr, const int32_t* __restrict__ sche
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[a][c] = 0.f;
-    const int kend = ksp < KSP ? (ksp + 1) * kper : 0;   // spare threads when 256 % d_h != 0
+    // the last split takes the rows that kJ / KSP leaves over (d_h 24, 40, 48, 72, 80);
+    // spare threads when 256 % d_h != 0 take none
+    const int kend = ksp >= KSP ? 0 : ksp == KSP - 1 ? kJ : (ksp + 1) * kper;
     for (int k = ksp * kper; k < kend; ++k) {
       float w4[4];
       {

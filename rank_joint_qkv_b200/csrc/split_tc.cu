@@ -29,13 +29,14 @@
 // one 4D operation.
 //
 // Roles (256 threads):
-//   warp 0     S producer: latent chunk + query chunk per slot (ragged last
-//              tile of a sequence: latent rows past its length are written as
-//              zeros by the warp, so a NaN or Inf stored there cannot leak
-//              through P = 0)
+//   warp 0     S producer: latent chunk + query chunk per slot
 //   warp 1     TMEM allocation; one thread issues the S MMAs
-//   warp 2     Z producer: latent chunk re-read per slot (same ragged rule)
-//   warp 3     one thread issues the Z MMAs
+//   warp 2     Z producer: latent chunk re-read per slot
+//   warp 3     one thread issues the Z MMAs (ragged last tile of a sequence:
+//              not those of 16 tokens past its length, and rows past it in
+//              the last group become zeros first, so a NaN or Inf stored there
+//              cannot leak through P = 0; one warp zero-filling the tile from
+//              plain loads instead took 160 us a tile at r 1536)
 //   warps 4-7  softmax over the S accumulator (one TMEM lane = one token),
 //              conditional rescale of Z, P written to shared memory, and the
 //              per-segment epilogue (partials m, l, z to global memory)
@@ -209,22 +210,17 @@ __device__ __forceinline__ void set_abort(const Smem& s, int32_t* status) {
 }
 
 
-// Zero-filled copy of latent rows into a slot by one warp, in the
-// 128-byte-swizzled layout TMA would have produced: `nbox` 64-channel boxes
-// of `rows` rows starting at tile row `row_lo`; tile rows >= nv become zeros.
-// `src` is the tile's first row at the first box's channel offset.
-__device__ __forceinline__ void ragged_rows(uint8_t* d, const uint8_t* src, size_t row_bytes,
-                                            int rows, int nbox, int row_lo, int nv, int lane) {
-  const int per_box = rows * 8;   // 16-byte vectors per box
-  for (int idx = lane; idx < nbox * per_box; idx += 32) {
-    const int box = idx / per_box, tt = (idx >> 3) % rows, c = idx & 7;
-    const int t = row_lo + tt;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t < nv) v = *reinterpret_cast<const uint4*>(src + size_t(t) * row_bytes + box * 128 + c * 16);
-    *reinterpret_cast<uint4*>(d + box * rows * 128 + tt * 128 + ((c ^ (tt & 7)) << 4)) = v;
+__device__ __forceinline__ void sts128z(uint32_t a) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+}
+// Zeros in rows [r0, r1) of a Z slot (two 64-channel boxes of 64 rows; whole
+// rows, so the swizzle has no bearing), by one thread.
+__device__ __forceinline__ void zero_z_rows(uint32_t d, int r0, int r1) {
+  for (int i = r0 * 8; i < r1 * 8; ++i) {
+    sts128z(d + uint32_t(i) * 16);
+    sts128z(d + uint32_t(kZBoxBytes) + uint32_t(i) * 16);
   }
   fence_proxy_async();   // generic-proxy stores -> visible to the tensor core
-  __syncwarp();
 }
 
 // ------------------------------------------------- quantised latent rows
@@ -608,11 +604,10 @@ __device__ void drain_q(int wsub, int nsub, const Smem& s, int nslots, int nraw,
 // or an abort.
 template <int NP, int QS, bool SG>
 __device__ bool produce(int kind, const Smem& s, const CUtensorMap* tm_cs, const CUtensorMap* tm_cz,
-                        const CUtensorMap* tm_q, const uint8_t* cache, const int32_t* sched, int B,
+                        const CUtensorMap* tm_q, const int32_t* sched, int B,
                         int r, int max_len, long long tb, long long te, int n, int nslots, int lane,
                         long long* issued, int ch, int cpart) {
   const int NI = r / 64;
-  const size_t row_bytes = size_t(r) * 2;
   const bool zk = SG || kind == 1;   // this ring carries Z items
   uint8_t* ring = kind == 0 ? s.sring : s.zring;
   const uint32_t slot_bytes = zk ? uint32_t(kZSlotBytes) : uint32_t(s_slot_bytes<NP, QS>());
@@ -627,7 +622,6 @@ __device__ bool produce(int kind, const Smem& s, const CUtensorMap* tm_cs, const
   for (int i = 0; i < n; ++i) {
     const int nv = it.nvalid(), b = it.b, t0 = it.t0();
     const int row = b * max_len + t0;
-    const uint8_t* tile = cache + size_t(row) * row_bytes;
     for (int u = 0; u < NI; ++u) {
       if (SG && !sg_owns(u >> 1, ch, cpart, kind)) continue;   // another ring's (or CTA's) chunk
       if (!__all_sync(0xffffffffu, mbar_wait(saddr(&empty[rg.slot]), rg.phase ^ 1u))) {   // warp-uniform
@@ -637,8 +631,9 @@ __device__ bool produce(int kind, const Smem& s, const CUtensorMap* tm_cs, const
       const uint32_t dst = ring0 + uint32_t(rg.slot) * slot_bytes;
       const uint32_t fb = saddr(&full[rg.slot]);
       const int lo = zk ? 64 * (u & 1) : 0;               // first tile row of the item
-      const int hi = zk ? lo + 64 : kTile;
-      if (nv >= hi) {
+      if (nv > lo) {
+        // (rows of a ragged last tile past its length arrive as stored: the
+        // softmax masks their scores, the Z MMAs see to their own)
         if (lane == 0) mbar_expect_tx(fb, slot_bytes);
         __syncwarp();
         // TMA operations of one thread are processed one after another, so the
@@ -651,19 +646,8 @@ __device__ bool produce(int kind, const Smem& s, const CUtensorMap* tm_cs, const
         } else if (lane == ln) {
           tma_load_3d_hint(dst, tm_cz, 0, row + lo, 2 * (u >> 1), fb, policy);
         }
-      } else {
-        // last tile of a sequence: rows past its length are written as zeros
-        uint8_t* d = ring + size_t(rg.slot) * slot_bytes;
-        if (!zk) ragged_rows(d, tile + 128 * u, row_bytes, kTile, 1, 0, nv, lane);
-        else ragged_rows(d, tile + 256 * (u >> 1), row_bytes, 64, 2, lo, nv, lane);
-        if (lane == 0) {
-          if (!zk) {
-            mbar_expect_tx(fb, uint32_t(QS * NP * 128));
-            tma_load_4d(dst + kBoxBytes, tm_q, 0, 0, QS * b, u, fb);
-          } else {
-            mbar_arrive(fb);
-          }
-        }
+      } else if (lane == 0) {
+        mbar_arrive(fb);   // no attended token in this half: nothing to load, no MMA reads the slot
       }
       __syncwarp();
       rg.advance();
@@ -703,8 +687,7 @@ template <int NP, bool BF16, int QS, int PS, int QB, bool SG, bool KEEP>
 __global__ void __launch_bounds__(split_threads<NP, QB>(), 1)
 k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CUtensorMap tm_cz,
            const __grid_constant__ CUtensorMap tm_q,
-           const uint8_t* __restrict__ cache, const __half* __restrict__ scales,
-           float* __restrict__ scores, const int32_t* __restrict__ sched,
+           const __half* __restrict__ scales, float* __restrict__ scores, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
            int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int ns, int nz,
            int nsg, int nraw, int ch, const float* __restrict__ qsh) {
@@ -811,7 +794,7 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
     } else {
       const int kind = warp == 0 ? 0 : 1;
       const int nslots = kind == 0 ? ns : nz;
-      ok = produce<NP, QS, SG>(kind, s, &tm_cs, &tm_cz, &tm_q, cache, sched, B, r, max_len, tb, te,
+      ok = produce<NP, QS, SG>(kind, s, &tm_cs, &tm_cz, &tm_q, sched, B, r, max_len, tb, te,
                                n, nslots, lane, &issued, ch, cpart);
       if (!ok && lane == 0) {
         set_abort(s, status);
@@ -915,6 +898,7 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         const bool first = it.first(tb);
+        const int nv = it.nvalid();
         if (!mbar_wait(saddr(&s.p_full[i & 1]), uint32_t(i >> 1) & 1u)) { ok = false; break; }
         const uint64_t pb = pb0 + uint64_t(((i & 1) * PS * pbuf_bytes<NP>()) >> 4);
         for (int u = 0; u < NI; ++u) {
@@ -924,8 +908,16 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
           tc_fence_after();
           const uint32_t d = tmem + uint32_t(ZC0 + (SG ? j / ch : j) * NP);
           const uint64_t za = za0 + uint64_t((rg.slot * kZSlotBytes) >> 4);
+          // a ragged last tile: groups of 16 tokens without an attended one are
+          // left out, and the rest of the last group becomes zeros (a NaN or
+          // Inf stored past the length would leak through P = 0).  The
+          // quantised path's rows are dequantised to zeros already.
+          const int nk = QB ? 4 : min(4, max(0, (nv - 64 * h + 15) >> 4));
+          if (!QB && nk > 0 && nv - 64 * h < 16 * nk)
+            zero_z_rows(saddr(ra ? s.sring : s.zring) + uint32_t(rg.slot * kZSlotBytes), nv - 64 * h, 16 * nk);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {   // K = 16 tokens per MMA
+            if (!QB && kk >= nk) break;
             const uint64_t a = za + uint64_t((kk * 16 * 128) >> 4);
 #pragma unroll
             for (int part = 0; part < PS; ++part) {   // P = P_hi (+ P_lo for bf16)
@@ -1575,7 +1567,7 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   if (e != cudaSuccess) return e;
   {
     const cudaError_t le = launch_pdl(kern, dim3(G * ch), dim3(split_threads<NP, QB>()), smem, s,
-                                     tcs, tcz, tq, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
+                                     tcs, tcz, tq, static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
     if (le != cudaSuccess) return le;
   }
   note_launch();

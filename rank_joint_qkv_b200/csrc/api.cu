@@ -361,13 +361,12 @@ static float* quant_query_scales(const qsvd_dims& d, void* qt16) {
   return reinterpret_cast<float*>(static_cast<uint8_t*>(qt16) + size_t(3) * d.batch * d.H * d.r);
 }
 
-// What a decode step yields beside its output.
+// What a decode step does beside the plain one.
 struct DecodeExtra {
-  bool keep_scores = false;    // the workspace has room for the scores
+  bool on = false;             // room in the workspace for scores, merged statistics and a prefix
   float* weights = nullptr;    // B x max_len: the rows' attention weights ...
   int add = 0;                 // ... added to what is there
-  bool shared = false;         // a prefix that the sequences share
-  const void* prefix = nullptr;
+  const void* prefix = nullptr;   // rows that every sequence attends before its own
   const void* prefix_scales = nullptr;
   int prefix_len = 0;
 };
@@ -403,10 +402,10 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   int G = 0;
   qsvd_status st = resolve_splits(d, num_splits, kernel, &G);
   if (st != QSVD_OK) return st;
-  const WsLayout W = ws_layout(d, G, x.keep_scores);
+  const WsLayout W = ws_layout(d, G, x.on);
   const int sms = device_sms() > 0 ? device_sms() : 1;
-  const PrefixLayout X = x.shared ? prefix_layout(d, x.prefix_len, sms, W.total) : PrefixLayout{};
-  const size_t total = x.shared ? X.total : W.total;
+  const PrefixLayout X = x.on ? prefix_layout(d, x.prefix_len, sms, W.total) : PrefixLayout{};
+  const size_t total = x.on ? X.total : W.total;
   if (!workspace) { *workspace_bytes = total; return QSVD_OK; }
   if (*workspace_bytes < total)
     return fail(QSVD_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", *workspace_bytes, total);
@@ -435,8 +434,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   float* pz = reinterpret_cast<float*>(Wb + W.pz);
   float* opart = reinterpret_cast<float*>(Wb + W.opart);
   const float* rope_tab = reinterpret_cast<const float*>(P + L.rope);
-  const bool px = x.shared && x.prefix_len > 0;   // prefix rows: on the tensor cores (X.fast) or the CUDA cores
-  const double gain = x.weights || x.shared ? split_score_gain(d, kernel) : 1.0;
+  const bool px = x.on && x.prefix_len > 0;   // prefix rows: on the tensor cores (X.fast) or the CUDA cores
+  const double gain = x.on ? split_score_gain(d, kernel) : 1.0;
   const float sl2 = float(double(score_scale_log2(d)) * gain);
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
@@ -447,7 +446,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets);
     if ((e = launch_schedule(d, lengths, G, sched, hdr, kernel, tickets, W.NT, s)) != cudaSuccess)
       return cuda_fail(e, "schedule");
-    if (x.shared && (!X.fast || !combine_uses_gemv(d)) &&
+    if (x.on && ((px && !X.fast) || !combine_uses_gemv(d)) &&
         (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
       return cuda_fail(e, "prefix schedule");
     // q = c_new W^u_q (reduced into the workspace), or the query as given
@@ -502,10 +501,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
                         float(score_gain(prefix_score_steps(d)) / gain), sms, &hdr->status, s);
       if (e != cudaSuccess) return cuda_fail(e, "prefix");
     }
-    if (x.weights && !x.shared && (e = launch_row_weights(d, hdr, sched, pm, pl, nullptr, scores, x.weights, x.add, s)) != cudaSuccess)
-      return cuda_fail(e, "attention weights");
   }
-  if (x.shared) {
+  if (x.on) {
     const bool gemv = combine_uses_gemv(d);
     float* zm = reinterpret_cast<float*>(Wb + W.zm);
     const bool fold = d.out_proj == QSVD_OUT_PROJ_FOLD;
@@ -524,7 +521,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
                          reinterpret_cast<const float*>(Wb + X.cz), P + L.wuv, opart, W.JS, 2 * d.batch, out, s);
     }
     if (e == cudaSuccess && x.weights)
-      e = launch_row_weights(d, hdr, sched, pm, pl, reinterpret_cast<const float2*>(Wb + X.ml), scores, x.weights, x.add, s);
+      e = launch_row_weights(d, sched, reinterpret_cast<const float2*>(Wb + X.ml), scores, x.weights, x.add, s);
     if (e != cudaSuccess) return cuda_fail(e, "combine phase");
   } else if (phases & QSVD_PHASE_COMBINE) {
     if (combine_uses_gemv(d)) {
@@ -565,7 +562,7 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
   if (workspace && (!weights || !aligned4(weights)))
     return fail(QSVD_ERR_INVALID_ARG, "weights must be given, 4-byte aligned");
   DecodeExtra x;
-  x.keep_scores = true;
+  x.on = true;
   x.weights = weights;
   x.add = accumulate != 0;
   return decode_impl(*dims, packed, qin, qin_is_latent, cache, scales, lengths, num_splits, workspace,
@@ -593,10 +590,9 @@ qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, c
   if (split_simt_grid_heads(d) == 0 && (d.cache_dtype == QSVD_F32 || d.r % 64 || d.H > 128))
     return fail(QSVD_ERR_UNSUPPORTED, "rank too large for the CUDA-core split kernel");
   DecodeExtra x;
-  x.keep_scores = true;
+  x.on = true;
   x.weights = weights;
   x.add = accumulate != 0;
-  x.shared = true;
   x.prefix = prefix;
   x.prefix_scales = prefix_scales;
   x.prefix_len = prefix_len;

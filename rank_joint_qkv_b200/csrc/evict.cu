@@ -3,28 +3,54 @@
 // A sequence with n > budget rows keeps its first `sink` rows, its last
 // `recent` rows and, of the rows between, the budget - sink - recent heaviest
 // (equal weights: the lower row first; a NaN weighs less than anything); the
-// kept rows stay in order.  Two steps:
+// kept rows stay in order.  Two kernels:
 //
 //   k_evict_select  the kept rows of each sequence, in order: the K-th
 //                   heaviest key by radix selection (weights mapped to
-//                   integers of the same order, three digits of 11, 11 and 10
-//                   bits, a shared-memory histogram each), then one pass that
-//                   compacts the rows above it and the first of those equal
-//   k_evict_move    the rows' bytes (and k_evict_small their scales and
-//                   weights): bound by HBM, each kept row read and written once
+//                   integers of the same order; three digits of 11, 11 and 10
+//                   bits, a shared-memory histogram each), then a compaction of
+//                   the rows above it and the first of those equal.  Latency
+//                   is its bound: 4 n bytes per sequence in a chain of
+//                   dependent steps.  So a sequence gets a cluster of CTAs,
+//                   one per 8192 rows up to eight, whose threads hold their
+//                   keys in registers across the steps and add up the
+//                   histograms over distributed shared memory.
+//   k_evict_move    the rows' bytes, scales and weights: bound by HBM, each
+//                   kept row read and written once
 //
 // In place the move has an order to keep: row j of the result is row
 // src[j] >= j of the source, src increasing.  A CTA owns a column slice of a
 // sequence and walks the rows in chunks, the whole chunk read before any of
 // it is written: what chunk k writes, rows below its end, no later chunk
-// reads, since src[j] >= j.
+// reads, since src[j] >= j.  Into other memory there is no order, and a CTA
+// copies whole rows.
 #include "internal.cuh"
 
 namespace qsvd {
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelKeys = 8;                              // consecutive rows per thread
+constexpr int kSelChunk = kSelThreads * kSelKeys;        // rows of a CTA held in registers at a time
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster, with release / acquire of its memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at p (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 
 // Order-preserving integer of a weight; NaN below everything, -0 equal to 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -60,186 +86,282 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t v, uint32_t* red, uin
   return before + x - v;
 }
 
-// grid B, block 1024.
+// grid B x CS in clusters of CS, block 1024.  CTA `rank` of a sequence's
+// cluster sees to rows [rank, rank + 1) x span.
 __global__ void __launch_bounds__(kSelThreads)
 k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int max_len, int budget, int sink,
                int recent, int32_t* __restrict__ src, int32_t* __restrict__ new_len, int32_t* dst_lengths,
-               int32_t* kept, int32_t* __restrict__ status) {
+               int32_t* kept, int32_t* __restrict__ status, int CS) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
-  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t hist[3][kBins];
   __shared__ uint32_t red[33];
-  __shared__ uint32_t found[2];   // digit, count above it
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int n = dev::clamp_len(lengths[b], max_len, tid == 0 ? status : nullptr);
+  __shared__ uint32_t found[2];    // digit, count above it
+  __shared__ uint32_t counts[2];   // this CTA's rows above the threshold (or kept anyway), and equal to it
+  const int b = int(blockIdx.x) / CS, tid = threadIdx.x;
+  const uint32_t rank = CS > 1 ? cluster_rank() : 0u;
+  const int n = dev::clamp_len(lengths[b], max_len, tid == 0 && rank == 0 ? status : nullptr);
   const float* w = weights + size_t(b) * max_len;
   int32_t* sb = src + size_t(b) * budget;
   int32_t* kb = kept ? kept + size_t(b) * budget : nullptr;
   const int m = min(n, budget);
-  __syncthreads();   // every thread has read the length: dst_lengths may be the same array
-  if (tid == 0) {
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
+  // every thread has read the length before dst_lengths, which may be the same array, is written
+  if (CS > 1) cluster_sync(); else __syncthreads();
+  if (tid == 0 && rank == 0) {
     new_len[b] = m;
     dst_lengths[b] = m;
   }
+  const unsigned step = unsigned(CS) * kSelThreads, first = rank * kSelThreads + unsigned(tid);
   if (kb)
-    for (unsigned j = unsigned(m + tid); j < unsigned(budget); j += kSelThreads) kb[j] = -1;
-  if (n <= budget) {
-    for (unsigned j = unsigned(tid); j < unsigned(n); j += kSelThreads) {
+    for (unsigned j = unsigned(m) + first; j < unsigned(budget); j += step) kb[j] = -1;
+  if (n <= budget) {   // uniform across the cluster
+    for (unsigned j = first; j < unsigned(n); j += step) {
       sb[j] = int32_t(j);
       if (kb) kb[j] = int32_t(j);
     }
     return;
   }
-  // threshold: the K-th largest key of rows [sink, n - recent)
-  const int lo = sink, hi = n - recent;
+  // this CTA's rows [r0, r1), the candidates [sink, n - recent) among them
+  const unsigned span = (unsigned(n) + unsigned(CS) - 1) / unsigned(CS);
+  const unsigned r0 = min(rank * span, unsigned(n)), r1 = min(r0 + span, unsigned(n));
+  const unsigned lo = unsigned(sink), hi = unsigned(n - recent);
+  const bool held = r1 - r0 <= unsigned(kSelChunk);   // one chunk: its keys stay in registers
+  uint32_t key[kSelKeys];
+  auto load = [&](unsigned c0) {   // thread's rows c0 + 8 tid .. + 7; rows that are no candidates: 0, and never counted
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
+      key[i] = t < r1 && t >= lo && t < hi ? weight_key(__ldg(w + t)) : 0u;
+    }
+  };
+  auto candidate = [&](unsigned c0, int i) {
+    const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
+    return t < r1 && t >= lo && t < hi;
+  };
+  if (held) load(r0);
+  // threshold: the K-th largest key of the candidates
+  const bool some = budget > sink + recent;   // else the budget is all sink and recent
   uint32_t K = uint32_t(budget - sink - recent), prefix = 0;
-  if (K > 0) {
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digits = pass == 2 ? 1024u : 2048u;
-      const int above = shift + (pass == 2 ? 10 : 11);   // bits decided before
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (unsigned t = unsigned(lo + tid); t < unsigned(hi); t += kSelThreads) {   // past 2^31 without wrapping
-        const uint32_t k = weight_key(w[t]);
-        if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & (digits - 1)], 1u);
+  for (int pass = 0; pass < 3 && some; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digits = pass == 2 ? 1024u : 2048u;
+    const int above = shift + (pass == 2 ? 10 : 11);   // bits decided before
+    for (unsigned c0 = r0; c0 < r1; c0 += kSelChunk) {
+      if (!held) load(c0);
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i)
+        if (candidate(c0, i) && (pass == 0 || (key[i] >> above) == (prefix >> above)))
+          atomicAdd(&hist[pass][(key[i] >> shift) & (digits - 1)], 1u);
+    }
+    if (CS > 1) cluster_sync(); else __syncthreads();
+    // thread i sees to bins 2 (1023 - i) + 1 and 2 (1023 - i): counted from the top, over the cluster
+    const int bin = 2 * (kSelThreads - 1 - tid);
+    uint32_t top = 0, low = 0;
+    if (CS > 1) {
+      for (int c = 0; c < CS; ++c) {
+        top += peer_word(&hist[pass][bin + 1], uint32_t(c));
+        low += peer_word(&hist[pass][bin], uint32_t(c));
       }
-      __syncthreads();
-      // thread i holds the bins 2 (1023 - i) + 1 and 2 (1023 - i): counted from the top
-      const uint32_t top = hist[2 * (kSelThreads - 1 - tid) + 1], low = hist[2 * (kSelThreads - 1 - tid)];
-      uint32_t total;
-      const uint32_t before = cta_exclusive(top + low, red, &total);
-      if (before < K && K <= before + top + low) {
-        const bool first = K <= before + top;
-        found[0] = uint32_t(2 * (kSelThreads - 1 - tid) + (first ? 1 : 0));
-        found[1] = before + (first ? 0u : top);
+    } else {
+      top = hist[pass][bin + 1];
+      low = hist[pass][bin];
+    }
+    uint32_t total;
+    const uint32_t before = cta_exclusive(top + low, red, &total);
+    if (before < K && K <= before + top + low) {   // one thread, the same in every CTA
+      const bool upper = K <= before + top;
+      found[0] = uint32_t(bin + (upper ? 1 : 0));
+      found[1] = before + (upper ? 0u : top);
+    }
+    __syncthreads();
+    prefix |= found[0] << shift;
+    K -= found[1];   // still to take among the keys equal so far
+  }
+  // The K lowest rows equal to the threshold are taken.  above: kept whatever the others are
+  auto above_at = [&](unsigned c0, int i) {
+    const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
+    return t < r1 && (t < lo || t >= hi || (some && key[i] > prefix));
+  };
+  auto equal_at = [&](unsigned c0, int i) { return some && candidate(c0, i) && key[i] == prefix; };
+  unsigned out = 0, eq = 0;   // kept rows and equal rows before this CTA's
+  if (CS > 1) {
+    unsigned na = 0, ne = 0;
+    for (unsigned c0 = r0; c0 < r1; c0 += kSelChunk) {
+      if (!held) load(c0);
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) {
+        na += above_at(c0, i);
+        ne += equal_at(c0, i);
       }
-      __syncthreads();
-      prefix |= found[0] << shift;
-      K -= found[1];   // still to take among the keys equal so far
-      __syncthreads();
+    }
+    uint32_t ta, te;
+    cta_exclusive(na, red, &ta);
+    cta_exclusive(ne, red, &te);
+    if (tid == 0) { counts[0] = ta; counts[1] = te; }
+    cluster_sync();
+    for (uint32_t c = 0; c < rank; ++c) {
+      const uint32_t e = peer_word(&counts[1], c);
+      out += peer_word(&counts[0], c) + min(e, K - min(K, eq));
+      eq += e;
     }
   }
-  // K rows equal to the threshold are taken, the lowest first; none when the budget is all sink and recent
-  const bool some = budget > sink + recent;
-  uint32_t taken_eq = 0, out = 0;
-  for (unsigned t0 = 0; t0 < unsigned(n); t0 += kSelThreads) {
-    const unsigned t = t0 + unsigned(tid);
-    const bool mid = t >= unsigned(lo) && t < unsigned(hi);
-    const uint32_t k = mid ? weight_key(w[t]) : 0u;
-    const bool eq = some && mid && k == prefix;
-    uint32_t neq, nkeep;
-    const uint32_t eq_before = cta_exclusive(eq ? 1u : 0u, red, &neq);
-    const bool keep = t < unsigned(n) && (!mid || (some && (k > prefix || (eq && taken_eq + eq_before < K))));
-    const uint32_t at = cta_exclusive(keep ? 1u : 0u, red, &nkeep);
-    if (keep) {
-      sb[out + at] = int32_t(t);
-      if (kb) kb[out + at] = int32_t(t);
+  for (unsigned c0 = r0; c0 < r1; c0 += kSelChunk) {
+    if (!held) load(c0);
+    uint32_t mine = 0;   // 16 bits each: rows above, rows equal (a chunk has 8192)
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) mine += (uint32_t(above_at(c0, i)) << 16) + uint32_t(equal_at(c0, i));
+    uint32_t all;
+    const uint32_t before = cta_exclusive(mine, red, &all);
+    const unsigned left = K - min(K, eq);   // equal rows still to take at the chunk's start
+    unsigned a = before >> 16, e = before & 0xFFFFu;
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const bool ab = above_at(c0, i), eqi = equal_at(c0, i);
+      if (ab || (eqi && e < left)) {
+        const unsigned at = out + a + min(e, left);
+        const int32_t t = int32_t(c0 + unsigned(tid) * kSelKeys + i);
+        sb[at] = t;
+        if (kb) kb[at] = t;
+      }
+      a += ab;
+      e += eqi;
     }
-    taken_eq += neq;
-    out += nkeep;
+    out += (all >> 16) + min(all & 0xFFFFu, left);
+    eq += all & 0xFFFFu;
   }
+  if (CS > 1) cluster_sync();   // no CTA leaves while another may read its counts
 }
 
 constexpr int kMvThreads = 256;
-constexpr int kMvUnroll = 8;   // 16-byte loads in flight per thread
+constexpr int kMvUnroll = 8;   // loads in flight per thread
 
-// Rows of 16-byte vectors.  A CTA owns the vectors [slice << ws, +1 << ws) of
-// sequence b's rows and walks their chunks of (256 >> ws) x 8 rows from
-// blockIdx.z on in steps of gridDim.z (1 in place: the order above).
-// grid (slices, B, chunk walkers), block 256.
-__global__ void __launch_bounds__(kMvThreads)
-k_evict_move(const uint8_t* src_rows, uint8_t* dst_rows, const int32_t* __restrict__ src,
-             const int32_t* __restrict__ new_len, int vecs, int ws, int max_len, int dst_max_len, int budget,
-             int in_place) {
-  dev::pdl_wait();   // see launch_pdl
-  dev::pdl_trigger();
-  const int b = blockIdx.y, m = new_len[b];
-  const int32_t* sb = src + size_t(b) * budget;
-  const int v = (int(blockIdx.x) << ws) + (int(threadIdx.x) & ((1 << ws) - 1));
-  const int rows = kMvThreads >> ws, row = int(threadIdx.x) >> ws;
-  const size_t rb = size_t(vecs) * 16;
-  const uint8_t* s0 = src_rows + size_t(b) * max_len * rb + size_t(v) * 16;
-  uint8_t* d0 = dst_rows + size_t(b) * dst_max_len * rb + size_t(v) * 16;
-  const int chunk = rows * kMvUnroll;
-  const bool mine = v < vecs;
-  for (long long j0 = (long long)blockIdx.z * chunk; j0 < m; j0 += (long long)gridDim.z * chunk) {
-    const int last = int(min((long long)m, j0 + chunk)) - 1;
-    if (in_place && sb[last] == last) continue;   // src[j] >= j, increasing: the whole chunk stays (uniform)
-    uint4 x[kMvUnroll];
-#pragma unroll
-    for (int i = 0; i < kMvUnroll; ++i) {
-      const long long j = j0 + i * rows + row;
-      if (mine && j <= last) {
-        const uint8_t* p = s0 + size_t(sb[j]) * rb;
-        asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w) : "l"(p) : "memory");
-      }
-    }
-    if (in_place) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMvUnroll; ++i) {
-      const long long j = j0 + i * rows + row;
-      if (mine && j <= last) *reinterpret_cast<uint4*>(d0 + size_t(j) * rb) = x[i];
-    }
-  }
-}
-
-constexpr int kSmThreads = 512;
-
-// The rows' group scales (ng 2-byte words each) and weights, in the same
-// ordered chunks; weights behind the new length become 0.  grid B, block 512.
-__global__ void __launch_bounds__(kSmThreads)
-k_evict_small(const uint16_t* scales, uint16_t* dst_scales, int ng, const float* weights, float* dst_weights,
-              const int32_t* __restrict__ src, const int32_t* __restrict__ new_len, int max_len, int dst_max_len,
-              int budget) {
-  dev::pdl_wait();   // see launch_pdl
-  dev::pdl_trigger();
-  const int b = blockIdx.x, m = new_len[b];
-  const int32_t* sb = src + size_t(b) * budget;
-  constexpr int U = 8;
+// The rows' group scales (ng 2-byte words each) and weights of sequence b, in
+// ordered chunks; weights behind the new length become 0.  One CTA.
+__device__ void move_small(const uint16_t* scales, uint16_t* dst_scales, int ng, const float* weights,
+                           float* dst_weights, const int32_t* sb, int b, int m, int max_len, int dst_max_len) {
+  constexpr int U = kMvUnroll;
   if (dst_scales) {
     const uint16_t* s0 = scales + size_t(b) * max_len * ng;
     uint16_t* d0 = dst_scales + size_t(b) * dst_max_len * ng;
-    const long long total = (long long)m * ng;
-    for (long long e0 = 0; e0 < total; e0 += kSmThreads * U) {
+    // thread = word g of rows j0 + its row: 256 / ng rows at a time (ng <= 256)
+    const int rows = kMvThreads / ng, row = int(threadIdx.x) / ng, g = int(threadIdx.x) % ng;
+    for (long long j0 = 0; j0 < m; j0 += rows * U) {
       uint16_t x[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const long long e = e0 + i * kSmThreads + threadIdx.x;
-        if (e < total) {
-          const int j = int(e / ng), g = int(e % ng);
+        const long long j = j0 + i * rows + row;
+        if (row < rows && j < m)
           asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(x[i]) : "l"(s0 + size_t(sb[j]) * ng + g) : "memory");
-        }
       }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const long long e = e0 + i * kSmThreads + threadIdx.x;
-        if (e < total) d0[e] = x[i];
+        const long long j = j0 + i * rows + row;
+        if (row < rows && j < m) d0[size_t(j) * ng + g] = x[i];
       }
     }
   }
   if (dst_weights) {
     const float* s0 = weights + size_t(b) * max_len;
     float* d0 = dst_weights + size_t(b) * dst_max_len;
-    for (long long j0 = 0; j0 < m; j0 += kSmThreads * U) {
+    for (long long j0 = 0; j0 < m; j0 += kMvThreads * U) {
       float x[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const long long j = j0 + i * kSmThreads + threadIdx.x;
+        const long long j = j0 + i * kMvThreads + threadIdx.x;
         if (j < m) asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x[i]) : "l"(s0 + sb[j]) : "memory");
       }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const long long j = j0 + i * kSmThreads + threadIdx.x;
+        const long long j = j0 + i * kMvThreads + threadIdx.x;
         if (j < m) d0[j] = x[i];
       }
     }
     __syncthreads();   // in place: the last rows are read before they are zeroed
-    for (long long j = m + int(threadIdx.x); j < dst_max_len; j += kSmThreads) d0[j] = 0.f;
+    for (long long j = m + int(threadIdx.x); j < dst_max_len; j += kMvThreads) d0[j] = 0.f;
+  }
+}
+
+__device__ __forceinline__ uint4 ld_cg(const uint8_t* p) {
+  uint4 x;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p) : "memory");
+  return x;
+}
+
+struct MoveArgs {
+  const uint8_t* rows;
+  uint8_t* dst_rows;
+  const uint16_t* scales;
+  uint16_t* dst_scales;     // null: none
+  const float* weights;
+  float* dst_weights;       // null: none
+  const int32_t *src, *new_len;
+  int vecs, ng, max_len, dst_max_len, budget;
+};
+
+// Rows of 16-byte vectors.  grid (1 + walkers, B), block 256; the first CTA
+// of a sequence moves its scales and weights.
+//   in place: walker = column slice of 1 << ws vectors, chunks of (256 >> ws) x 8 rows in order
+//   else:     walkers share the sequence's (row, vector) pairs in chunks of 2048, row after row
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMvThreads)
+k_evict_move(const MoveArgs a, int ws) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  const int b = blockIdx.y, m = a.new_len[b];
+  const int32_t* sb = a.src + size_t(b) * a.budget;
+  if (blockIdx.x == 0) {
+    move_small(a.scales, a.dst_scales, a.ng, a.weights, a.dst_weights, sb, b, m, a.max_len, a.dst_max_len);
+    return;
+  }
+  const int walker = int(blockIdx.x) - 1;
+  const size_t rb = size_t(a.vecs) * 16;
+  const uint8_t* s0 = a.rows + size_t(b) * a.max_len * rb;
+  uint8_t* d0 = a.dst_rows + size_t(b) * a.dst_max_len * rb;
+  if (IN_PLACE) {
+    const int v = (walker << ws) + (int(threadIdx.x) & ((1 << ws) - 1));
+    const int rows = kMvThreads >> ws, row = int(threadIdx.x) >> ws, chunk = rows * kMvUnroll;
+    const bool mine = v < a.vecs;
+    s0 += size_t(v) * 16;
+    d0 += size_t(v) * 16;
+    for (long long j0 = 0; j0 < m; j0 += chunk) {
+      const int last = int(min((long long)m, j0 + chunk)) - 1;
+      if (sb[last] == last) continue;   // src[j] >= j, increasing: the whole chunk stays (uniform)
+      uint4 x[kMvUnroll];
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i) {
+        const long long j = j0 + i * rows + row;
+        if (mine && j <= last) x[i] = ld_cg(s0 + size_t(sb[j]) * rb);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i) {
+        const long long j = j0 + i * rows + row;
+        if (mine && j <= last) *reinterpret_cast<uint4*>(d0 + size_t(j) * rb) = x[i];
+      }
+    }
+  } else {
+    const unsigned long long total = (unsigned long long)m * a.vecs;
+    const unsigned long long stride = (unsigned long long)(gridDim.x - 1) * (kMvThreads * kMvUnroll);
+    const unsigned vecs = unsigned(a.vecs);
+    for (unsigned long long e0 = (unsigned long long)walker * (kMvThreads * kMvUnroll); e0 < total; e0 += stride) {
+      const unsigned long long j0 = e0 / vecs;                 // row of the chunk's start: the only wide division
+      const unsigned v0 = unsigned(e0 - j0 * vecs);
+      uint4 x[kMvUnroll];
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i) {
+        const unsigned e = v0 + i * kMvThreads + threadIdx.x, j = e / vecs;
+        if (j0 + j < (unsigned long long)m) x[i] = ld_cg(s0 + size_t(sb[j0 + j]) * rb + size_t(e - j * vecs) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i) {
+        const unsigned e = v0 + i * kMvThreads + threadIdx.x;
+        if (j0 + e / vecs < (unsigned long long)m) *reinterpret_cast<uint4*>(d0 + size_t(j0) * rb + size_t(e) * 16) = x[i];
+      }
+    }
   }
 }
 
@@ -249,30 +371,46 @@ cudaError_t launch_evict(const qsvd_dims& d, const float* weights, const int32_t
                          int recent, const void* cache, const void* scales, int dst_max_len, void* dst_cache,
                          void* dst_scales, float* dst_weights, int32_t* dst_lengths, int32_t* kept, int32_t* src,
                          int32_t* new_len, int32_t* status, cudaStream_t s) {
-  cudaError_t e = launch_pdl(k_evict_select, dim3(unsigned(d.batch)), dim3(kSelThreads), 0, s, weights, lengths,
-                             d.max_len, budget, sink, recent, src, new_len, dst_lengths, kept, status);
+  // one CTA per 8192 rows of the longest sequence, a power of two up to eight
+  int CS = 1;
+  while (CS < kMaxCluster && (long long)CS * kSelChunk < d.max_len) CS *= 2;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(d.batch) * unsigned(CS));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = unsigned(CS);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_evict_select, weights, lengths, d.max_len, budget, sink, recent, src,
+                                     new_len, dst_lengths, kept, status, CS);
   if (e != cudaSuccess) return e;
   note_launch();
   if ((e = check_launch()) != cudaSuccess) return e;
-  const int vecs = int(cache_row_bytes(d) / 16);
-  const int in_place = cache == dst_cache;
-  int ws = 3;   // 128-byte slices; in place narrower ones where there are too few to fill the GPU
-  while (in_place && ws > 1 && (long long)((vecs + (1 << ws) - 1) >> ws) * d.batch < 296) --ws;
-  const int slices = (vecs + (1 << ws) - 1) >> ws;
-  const int chunk = (kMvThreads >> ws) * kMvUnroll;
-  long long walkers = in_place ? 1 : (budget + chunk - 1) / chunk;
-  if (walkers > 65535) walkers = 65535;
-  e = launch_pdl(k_evict_move, dim3(unsigned(slices), unsigned(d.batch), unsigned(walkers)), dim3(kMvThreads), 0, s,
-                 static_cast<const uint8_t*>(cache), static_cast<uint8_t*>(dst_cache), src, new_len, vecs, ws,
-                 d.max_len, dst_max_len, budget, in_place);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  if ((e = check_launch()) != cudaSuccess) return e;
-  if (!dst_weights && !cache_is_int(d)) return cudaSuccess;
-  e = launch_pdl(k_evict_small, dim3(unsigned(d.batch)), dim3(kSmThreads), 0, s, static_cast<const uint16_t*>(scales),
-                 static_cast<uint16_t*>(cache_is_int(d) ? dst_scales : nullptr),
-                 cache_is_int(d) ? d.r / d.group : 1, weights, dst_weights, src, new_len, d.max_len, dst_max_len,
-                 budget);
+  const bool q = cache_is_int(d), in_place = cache == dst_cache;
+  const MoveArgs a{static_cast<const uint8_t*>(cache), static_cast<uint8_t*>(dst_cache),
+                   static_cast<const uint16_t*>(scales), static_cast<uint16_t*>(q ? dst_scales : nullptr), weights,
+                   dst_weights, src, new_len, int(cache_row_bytes(d) / 16), q ? d.r / d.group : 1, d.max_len,
+                   dst_max_len, budget};
+  int ws = 0;
+  long long walkers;
+  if (in_place) {
+    // 128-byte slices, narrower ones where those are too few to fill the GPU (one sequence of 8192 rows of 1536
+    // fp16 channels: 24 slices of 128 bytes against 96 of 32)
+    for (ws = 3; ws > 1 && (long long)((a.vecs + (1 << ws) - 1) >> ws) * d.batch < 296; --ws) {}
+    walkers = (a.vecs + (1 << ws) - 1) >> ws;
+  } else {
+    walkers = ((long long)budget * a.vecs + kMvThreads * kMvUnroll - 1) / (kMvThreads * kMvUnroll);
+    if (walkers > (1 << 20)) walkers = 1 << 20;
+  }
+  e = launch_pdl(in_place ? k_evict_move<true> : k_evict_move<false>, dim3(unsigned(1 + walkers), unsigned(d.batch)),
+                 dim3(kMvThreads), 0, s, a, ws);
   if (e != cudaSuccess) return e;
   note_launch();
   return check_launch();

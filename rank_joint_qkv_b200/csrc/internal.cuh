@@ -310,11 +310,10 @@ cudaError_t launch_combine(const qsvd_dims& d, const WsHeader* hdr, const int32_
                            cudaStream_t s);
 
 // Attention weight of each cache row from the kept scores (row_weights.cu):
-// w[b][t] = (add ? w[b][t] : 0) + sum_h 2^(s - M_h) / L_h for t < len_b.  ml:
-// {M, 1 / L} [B][H], or null to merge them from the splits' pm and pl.
-cudaError_t launch_row_weights(const qsvd_dims& d, const WsHeader* hdr, const int32_t* sched, const float* pm,
-                               const float* pl, const float2* ml, const float* scores, float* w, int add,
-                               cudaStream_t s);
+// w[b][t] = (add ? w[b][t] : 0) + sum_h 2^(s - M_h) / L_h for t < len_b, with
+// ml = {M, 1 / L} [B][H].
+cudaError_t launch_row_weights(const qsvd_dims& d, const int32_t* sched, const float2* ml, const float* scores,
+                               float* w, int add, cudaStream_t s);
 
 // Cutting caches to a budget of rows (evict.cu).  src [B][budget] and new_len
 // [B] are scratch.
@@ -369,6 +368,11 @@ __device__ __forceinline__ void l2_prefetch_share(const uint8_t* p, unsigned lon
   }
 }
 
+
+// [p, p + bytes) requested into L2, both multiples of 16: a hint.
+__device__ __forceinline__ void l2_prefetch(const uint8_t* p, unsigned bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 // See launch_pdl.  A no-op when the kernel was launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -452,13 +456,18 @@ __device__ __forceinline__ int clamp_len(int n, int max_len, int32_t* status) {
   return n;
 }
 
+// x / y for x >= 0, y > 0: a 32-bit division where both fit (a 64-bit one is
+// a subroutine of some hundred cycles, on the merge's critical path).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) ? x / y : (long long)(unsigned(x) / unsigned(y));
+}
 // Split c of G covers global tiles [split_begin(c), split_begin(c + 1)).
 __device__ __forceinline__ long long split_begin(long long c, long long G, long long T) {
-  return (c * T) / G;
+  return quotient(c * T, G);
 }
 // The split whose range contains global tile t.
 __device__ __forceinline__ long long split_of_tile(long long t, long long G, long long T) {
-  return ((t + 1) * G - 1) / T;
+  return quotient((t + 1) * G - 1, T);
 }
 
 // Sixteen bytes of a cache row converted to float.  Element index j0 is the

@@ -19,10 +19,11 @@
 //   k_prefix_gemm<values>   128 query rows x 256 channels per unit over a
 //                           split's tokens; float32 partials for the merge
 //
-// A tile's reference is its maximum rounded down to a multiple of 8 (log2
-// units): P <= 2^8 as in the split kernels, and neighbouring tiles mostly
-// share it, so k_prefix_norm rewrites few of them; where it does, the factor
-// is a power of two and the only loss is a fp16 subnormal's.
+// A tile's reference is its maximum rounded down to a multiple of 15 (log2
+// units): P < 2^15 is within fp16, and a row's tiles mostly share it, so that
+// k_prefix_norm rewrites few of them (multiples of 8: three times as many, and
+// 7.6 instead of 3 us at B 16, H 32, P 8192); where it does, the factor is a
+// power of two and the only loss is a fp16 subnormal's.
 //
 // Precision as in the split kernels: the query as two 16-bit parts (both
 // products accumulate in float32), P as two for bf16; a quantised prefix is
@@ -48,6 +49,8 @@ constexpr int kPxThreads = 192;
 constexpr int kPxA = 128 * 128;            // A box: 128 rows x 64 K x 2 bytes
 constexpr int kPxB = 256 * 128;            // B: 256 N x 64 K x 2 bytes
 constexpr int kPxMaxSlots = 4;
+constexpr int kPxStage = 32 * 128;         // epilogue staging: 32 rows x 128 bytes, two per warp
+constexpr float kRefStep = 15.f;           // log2 units between references
 constexpr int kPxSmem = 232448;            // opt-in dynamic shared memory per block on sm_100
 
 template <int AP>
@@ -81,7 +84,8 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + size_t(ns) * kSlot);
+  uint8_t* stage0 = base + size_t(ns) * kSlot;              // [4 warps][2][32 rows][128 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage0 + 8 * kPxStage);
   uint64_t* full = bars;                    // [kPxMaxSlots]
   uint64_t* empty = bars + kPxMaxSlots;     // [kPxMaxSlots]
   uint64_t* afull = bars + 2 * kPxMaxSlots; // [2] accumulator complete
@@ -229,8 +233,26 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const int q = warp & 3;
     const int t = 32 * q + lane;   // query row of the block == TMEM lane
     const uint32_t lane_off = uint32_t(32 * q) << 16;
-    const int seq = t / g.H, head = t - seq * g.H;
     const size_t rows = size_t(g.MB) * 128;
+    // A lane holds a row's values; stored as they are, 16 bytes a lane, a store
+    // instruction would touch 32 rows.  So the warp turns 32 rows x 128 bytes
+    // around in shared memory (16-byte chunks, swizzled by row) and stores
+    // four whole lines an instruction.
+    const uint32_t st0 = saddr(stage0) + uint32_t(q) * (2 * kPxStage);
+    auto put = [&](int buf, int c, uint4 v) {   // chunk c of this lane's row
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st0 + buf * kPxStage + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    };
+    auto flush = [&](int buf, uint8_t* row0, size_t pitch, int live_rows) {   // the warp's 32 rows from row0 on
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rr = 4 * i + (lane >> 3), c = lane & 7;
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(st0 + buf * kPxStage + rr * 128 + ((c ^ (rr & 7)) << 4)) : "memory");
+        if (32 * q + rr < live_rows) *reinterpret_cast<uint4*>(row0 + size_t(rr) * pitch + c * 16) = v;
+      }
+    };
     for (int j = 0; j < mine; ++j) {
       int mb, n, sp, k0, k1;
       unit(j, &mb, &n, &sp, &k0, &k1);
@@ -241,23 +263,30 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         break;
       }
       tc_fence_after();
-      const int b = mb * g.nb + seq;
-      const bool live = seq < g.nb && b < g.B;
+      const int live_rows = min(g.nb, g.B - mb * g.nb) * g.H;   // rows of the block that are queries
       const uint32_t ta = tmem + lane_off + uint32_t(ab * 256);
       if (VALUES) {
-        float* z = g.pz + ((size_t(sp) * g.B + b) * g.H + head) * g.r + size_t(n) * 256;
+        // rows mb nb H + t of the split's [B H][r]
+        uint8_t* z = reinterpret_cast<uint8_t*>(g.pz + ((size_t(sp) * g.B + size_t(mb) * g.nb) * g.H + 32 * q) * g.r +
+                                                size_t(n) * 256);
         const int nc = min(256, g.r - n * 256);   // a multiple of 64
 #pragma unroll 1
-        for (int c = 0; c < nc; c += 32) {
-          float v[32];
-          tmem_ld16(ta + uint32_t(c), v);
-          tmem_ld16(ta + uint32_t(c + 16), v + 16);
-          tmem_wait_ld();
-          if (live) {
+        for (int c = 0; c < nc; c += 64) {
+          float v[64];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(z + c)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          }
+          for (int i = 0; i < 4; ++i) tmem_ld16(ta + uint32_t(c + 16 * i), v + 16 * i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float* x = v + 32 * half + 4 * e;
+              put(half, e, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
+            }
+          __syncwarp();
+          flush(0, z + c * 4, size_t(g.r) * 4, live_rows);
+          flush(1, z + c * 4 + 128, size_t(g.r) * 4, live_rows);
+          __syncwarp();
         }
       } else {
         const int nv = min(kPxTile, g.plen - n * kPxTile);   // tokens of the tile, >= 1
@@ -271,35 +300,36 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 32; ++e) mx = c + e < nv ? fmaxf(mx, v[e]) : mx;
         }
-        const float ref = 8.f * floorf(mx * g.gain * 0.125f);
+        const float ref = kRefStep * floorf(mx * g.gain / kRefStep);
         float sum = 0.f;
-        T16* prow = static_cast<T16*>(g.p) + (size_t(mb) * 128 + t) * g.ppad + size_t(n) * kPxTile;
+        uint8_t* prow = reinterpret_cast<uint8_t*>(static_cast<T16*>(g.p) + (size_t(mb) * 128 + 32 * q) * g.ppad + size_t(n) * kPxTile);
 #pragma unroll 1
-        for (int c = 0; c < kPxTile; c += 32) {
-          float v[32];
-          tmem_ld16(ta + uint32_t(c), v);
-          tmem_ld16(ta + uint32_t(c + 16), v + 16);
+        for (int c = 0; c < kPxTile; c += 64) {
+          float v[64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld16(ta + uint32_t(c + 16 * i), v + 16 * i);
           tmem_wait_ld();
-          uint4 hi[4], lo[4];
-          T16* hv = reinterpret_cast<T16*>(hi);
-          T16* lv = reinterpret_cast<T16*>(lo);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p = c + e < nv ? exp2f(fmaf(v[e], g.gain, -ref)) : 0.f;
-            sum += p;
-            hv[e] = dev::from_f<T16>(p);
-            if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
-          }
-          if (live) {
+          for (int e8 = 0; e8 < 8; ++e8) {
+            uint4 hi, lo;
+            T16* hv = reinterpret_cast<T16*>(&hi);
+            T16* lv = reinterpret_cast<T16*>(&lo);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(prow + c)[e] = hi[e];
-            if (PS == 2) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(prow + rows * g.ppad + c)[e] = lo[e];
+            for (int e = 0; e < 8; ++e) {
+              const float p = c + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], g.gain, -ref)) : 0.f;
+              sum += p;
+              hv[e] = dev::from_f<T16>(p);
+              if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
             }
+            put(0, e8, hi);
+            if (PS == 2) put(1, e8, lo);
           }
+          __syncwarp();
+          flush(0, prow + c * 2, size_t(g.ppad) * 2, live_rows);
+          if (PS == 2) flush(1, prow + rows * g.ppad * 2 + c * 2, size_t(g.ppad) * 2, live_rows);
+          __syncwarp();
         }
-        if (live) {
+        if (t < live_rows) {
           g.mt[size_t(n) * rows + size_t(mb) * 128 + t] = ref;
           g.lt[size_t(n) * rows + size_t(mb) * 128 + t] = sum;
         }
@@ -548,8 +578,8 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
   const long long units = (long long)g.MB * (VALUES ? (long long)((g.r + 255) / 256) * g.SP : g.tiles);
   if (units > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int grid = units < sms ? int(units) : sms;
-  const size_t smem = 1024 + size_t(px_slots<AP>()) * px_slot<AP>() + (2 * kPxMaxSlots + 5) * 8 + 16;
-  static_assert(1024 + px_slots<AP>() * px_slot<AP>() + (2 * kPxMaxSlots + 5) * 8 + 16 <= kPxSmem, "ring fits");
+  const size_t smem = 1024 + size_t(px_slots<AP>()) * px_slot<AP>() + 8 * kPxStage + (2 * kPxMaxSlots + 5) * 8 + 16;
+  static_assert(1024 + px_slots<AP>() * px_slot<AP>() + 8 * kPxStage + (2 * kPxMaxSlots + 5) * 8 + 16 <= kPxSmem, "ring fits");
   auto kern = k_prefix_gemm<BF16, AP, CP, PS, VALUES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;

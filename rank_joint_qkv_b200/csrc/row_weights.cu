@@ -1,8 +1,7 @@
 // Attention weight of each cache row, summed over the heads, from the scores
 // the split phase kept and the merged softmax statistics:
 //
-//   w_t (+)= sum_h 2^(s_{h,t} - M_h) / L_h,
-//   M_h = max_s m_s,  L_h = sum_s 2^(m_s - M_h) l_s   (log2 domain)
+//   w_t (+)= sum_h 2^(s_{h,t} - M_h) / L_h   (log2 domain; M and L from the merge)
 //
 // the quantity by which rows of a cache are kept or dropped.  It reads the
 // scores once, 4 H bytes per row (16 MB at LLaVA-7B shapes, B 16, L 8192),
@@ -15,13 +14,10 @@ namespace {
 constexpr int kRwThreads = 256;
 constexpr int kRwHeads = 1024;   // heads' statistics held at a time
 
-// grid (ceil(max_len / 256), B), block 256: thread = row; 1024 heads at a
-// time.  ml: the statistics {M, 1 / L} [B][H] when they are merged already,
-// else null and each CTA merges the splits' m and l of its sequence.
+// grid (ceil(max_len / 256), B), block 256: thread = row; 1024 heads at a time.
 __global__ void __launch_bounds__(kRwThreads)
-k_row_weights(const WsHeader* __restrict__ hdr, const int32_t* __restrict__ sched,
-              const float* __restrict__ pm, const float* __restrict__ pl, const float2* __restrict__ ml,
-              const float* __restrict__ scores, float* __restrict__ w, int add, int B, int H, int max_len) {
+k_row_weights(const int32_t* __restrict__ sched, const float2* __restrict__ ml, const float* __restrict__ scores,
+              float* __restrict__ w, int add, int B, int H, int max_len) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   __shared__ float2 stat[kRwHeads];
@@ -29,40 +25,21 @@ k_row_weights(const WsHeader* __restrict__ hdr, const int32_t* __restrict__ sche
   const long long t = (long long)blockIdx.x * kRwThreads + threadIdx.x;
   const int n = sched[B + 1 + b];
   if (t - threadIdx.x >= n) return;   // uniform across the CTA
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long G = hdr->G, T = sched[B];
-  const int c0 = int(dev::split_of_tile(sched[b], G, T)), c1 = int(dev::split_of_tile(sched[b + 1] - 1, G, T));
   float acc = 0.f;
   for (int h0 = 0; h0 < H; h0 += kRwHeads) {
     const int nh = min(kRwHeads, H - h0);
     if (h0) __syncthreads();   // every thread is done with the heads before
-    if (ml) {
-      for (int h = threadIdx.x; h < nh; h += kRwThreads) stat[h] = __ldcg(ml + size_t(b) * H + h0 + h);
-    } else {
-      for (int h = warp; h < nh; h += kRwThreads / 32) {
-        const float* pmh = pm + size_t(b) * H + h0 + h;
-        const float* plh = pl + size_t(b) * H + h0 + h;
-        float M = -INFINITY, L = 0.f;
-        for (int c = c0 + lane; c <= c1; c += 32)
-          if (dev::split_begin(c, G, T) != dev::split_begin(c + 1, G, T)) M = fmaxf(M, __ldcg(pmh + size_t(c) * H));
-        M = dev::warp_max(M);
-        for (int c = c0 + lane; c <= c1; c += 32)
-          if (dev::split_begin(c, G, T) != dev::split_begin(c + 1, G, T))
-            L += exp2f(__ldcg(pmh + size_t(c) * H) - M) * __ldcg(plh + size_t(c) * H);
-        L = dev::warp_sum(L);
-        if (lane == 0) stat[h] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
-      }
-    }
+    for (int h = threadIdx.x; h < nh; h += kRwThreads) stat[h] = __ldcg(ml + size_t(b) * H + h0 + h);
     __syncthreads();
     if (t >= n) continue;
     const float* sc = scores + (size_t(b) * H + h0) * max_len + t;
     int h = 0;
-    for (; h + 8 <= nh; h += 8) {   // eight loads in flight, added in head order
-      float v[8];
+    for (; h + 16 <= nh; h += 16) {   // sixteen loads in flight, added in head order
+      float v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __ldcg(sc + size_t(h + i) * max_len);
+      for (int i = 0; i < 16; ++i) v[i] = __ldcg(sc + size_t(h + i) * max_len);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc = fmaf(exp2f(v[i] - stat[h + i].x), stat[h + i].y, acc);
+      for (int i = 0; i < 16; ++i) acc = fmaf(exp2f(v[i] - stat[h + i].x), stat[h + i].y, acc);
     }
     for (; h < nh; ++h) acc = fmaf(exp2f(__ldcg(sc + size_t(h) * max_len) - stat[h].x), stat[h].y, acc);
   }
@@ -73,12 +50,11 @@ k_row_weights(const WsHeader* __restrict__ hdr, const int32_t* __restrict__ sche
 
 }  // namespace
 
-cudaError_t launch_row_weights(const qsvd_dims& d, const WsHeader* hdr, const int32_t* sched, const float* pm,
-                               const float* pl, const float2* ml, const float* scores, float* w, int add,
-                               cudaStream_t s) {
+cudaError_t launch_row_weights(const qsvd_dims& d, const int32_t* sched, const float2* ml, const float* scores,
+                               float* w, int add, cudaStream_t s) {
   const dim3 grid(unsigned((d.max_len + kRwThreads - 1) / kRwThreads), unsigned(d.batch));
-  const cudaError_t e = launch_pdl(k_row_weights, grid, dim3(kRwThreads), 0, s, hdr,
-                                   sched, pm, pl, ml, scores, w, add, d.batch, d.H, d.max_len);
+  const cudaError_t e = launch_pdl(k_row_weights, grid, dim3(kRwThreads), 0, s, sched,
+                                   ml, scores, w, add, d.batch, d.H, d.max_len);
   if (e != cudaSuccess) return e;
   note_launch();
   return check_launch();

@@ -687,7 +687,8 @@ template <int NP, bool BF16, int QS, int PS, int QB, bool SG, bool KEEP>
 __global__ void __launch_bounds__(split_threads<NP, QB>(), 1)
 k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CUtensorMap tm_cz,
            const __grid_constant__ CUtensorMap tm_q,
-           const __half* __restrict__ scales, float* __restrict__ scores, const int32_t* __restrict__ sched,
+           const uint8_t* __restrict__ cache, const __half* __restrict__ scales,
+           float* __restrict__ scores, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
            int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int ns, int nz,
            int nsg, int nraw, int ch, const float* __restrict__ qsh) {
@@ -760,6 +761,16 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
     // ----------------------------------------------------------- producers
     bool ok = true;
     long long issued = 0, raw_issued = 0;
+    if (warp == 2 && lane == 0) {
+      // the first tile's rows towards L2 at once (a hint): a CTA with a single
+      // tile would else meet HBM's latency once per turn of the S ring
+      TileIter it0;
+      it0.init(sched, B, tb, te);
+      const unsigned long long rb = (unsigned long long)r * (QB ? QB : 16) / 8;
+      const uint8_t* p0 = cache + (size_t(it0.b) * max_len + it0.t0()) * rb;
+      for (unsigned long long at = 0, end = it0.nvalid() * rb; at < end; at += 16384)
+        dev::l2_prefetch(p0 + at, unsigned(end - at < 16384 ? end - at : 16384));
+    }
     if constexpr (QB != 0) {
       // quantised latent.  S: warp 0 loads int8 codes by TMA; int4 raw codes
       // are unpacked by warps 0 and 9.  Z: warp 2 issues the raw codes and
@@ -1567,7 +1578,7 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   if (e != cudaSuccess) return e;
   {
     const cudaError_t le = launch_pdl(kern, dim3(G * ch), dim3(split_threads<NP, QB>()), smem, s,
-                                     tcs, tcz, tq, static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
+                                     tcs, tcz, tq, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
     if (le != cudaSuccess) return le;
   }
   note_launch();

@@ -32,10 +32,10 @@ def weights_call(d, ws_bytes=None, workspace=OK, weights=OK + 4096, cache=OK, sc
 
 def test_weights_workspace_has_room_for_the_scores():
     d = dims()
-    room = q.decode_weights_workspace_bytes(d, 4) - q.decode_workspace_bytes(d, 4)
-    assert 2 * 4 * 300 * 4 <= room <= 2 * 4 * 300 * 4 + 256
-    r = dims(rope=True)   # the rotary decode keeps its scores in any case
-    assert q.decode_weights_workspace_bytes(r, 4) == q.decode_workspace_bytes(r, 4)
+    scores = 2 * 4 * 300 * 4   # B x H x max_len
+    assert q.decode_weights_workspace_bytes(d, 4) >= q.decode_workspace_bytes(d, 4) + scores
+    r = dims(rope=True)        # the rotary decode keeps its scores in any case
+    assert q.decode_weights_workspace_bytes(r, 4) - q.decode_workspace_bytes(r, 4) < scores
 
 
 def test_weights_refusals():

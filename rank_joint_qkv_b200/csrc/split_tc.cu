@@ -214,13 +214,14 @@ __device__ __forceinline__ void sts128z(uint32_t a) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
 }
 // Zeros in rows [r0, r1) of a Z slot (two 64-channel boxes of 64 rows; whole
-// rows, so the swizzle has no bearing), by one thread.
-__device__ __forceinline__ void zero_z_rows(uint32_t d, int r0, int r1) {
-  for (int i = r0 * 8; i < r1 * 8; ++i) {
+// rows, so the swizzle has no bearing), by one warp.
+__device__ __forceinline__ void zero_z_rows(uint32_t d, int r0, int r1, int lane) {
+  for (int i = r0 * 8 + lane; i < r1 * 8; i += 32) {
     sts128z(d + uint32_t(i) * 16);
     sts128z(d + uint32_t(kZBoxBytes) + uint32_t(i) * 16);
   }
   fence_proxy_async();   // generic-proxy stores -> visible to the tensor core
+  __syncwarp();
 }
 
 // ------------------------------------------------- quantised latent rows
@@ -894,63 +895,74 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
     __syncwarp();
   } else if (warp == 3 || (SG && warp == 1)) {
     // ----------------------------------------------------------- Z MMAs
-    if (lane == 0) {
+    // Lane 0 waits and issues; the others walk the items along with it and
+    // help where a ragged last tile's rows are zeroed.  An expired wait ends
+    // lane 0's work, not the walk (the lanes meet in the warp's shuffles).
+    {
       const int kind = warp >> 1;   // SG: ring and chunk parity of this issuer
       const bool ra = SG && kind == 0;
       uint64_t* zfull = ra ? s.s_full : s.z_full;
       uint64_t* zempty = ra ? s.s_empty : s.z_empty;
       constexpr uint32_t id_z = idesc_f16(128, NP, BF16, true, false);
-      const uint64_t za0 = sdesc(saddr(ra ? s.sring : s.zring), kZBoxBytes, 1024);  // MN-major C^T
-      const uint64_t pb0 = sdesc(saddr(s.pbuf), 16, 1024);                          // P^T, K-major
+      const uint32_t zring = saddr(ra ? s.sring : s.zring);
+      const uint64_t za0 = sdesc(zring, kZBoxBytes, 1024);   // MN-major C^T
+      const uint64_t pb0 = sdesc(saddr(s.pbuf), 16, 1024);   // P^T, K-major
       TileIter it;
       it.init(sched, B, tb, te);
       Ring rg(ra ? ns : nz);
       int sbi = 0;   // quantised latent: scale table of the tile
       bool ok = true;
-      for (int i = 0; i < n && ok; ++i) {
+      for (int i = 0; i < n; ++i) {
         const bool first = it.first(tb);
         const int nv = it.nvalid();
-        if (!mbar_wait(saddr(&s.p_full[i & 1]), uint32_t(i >> 1) & 1u)) { ok = false; break; }
+        if (lane == 0 && ok) ok = mbar_wait(saddr(&s.p_full[i & 1]), uint32_t(i >> 1) & 1u);
         const uint64_t pb = pb0 + uint64_t(((i & 1) * PS * pbuf_bytes<NP>()) >> 4);
         for (int u = 0; u < NI; ++u) {
           const int j = u >> 1, h = u & 1;   // 128-channel chunk, 64-token half
           if (SG && !sg_owns(j, ch, cpart, kind)) continue;
-          if (!mbar_wait(saddr(&zfull[rg.slot]), rg.phase)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t d = tmem + uint32_t(ZC0 + (SG ? j / ch : j) * NP);
-          const uint64_t za = za0 + uint64_t((rg.slot * kZSlotBytes) >> 4);
+          if (lane == 0 && ok) ok = mbar_wait(saddr(&zfull[rg.slot]), rg.phase);
           // a ragged last tile: groups of 16 tokens without an attended one are
           // left out, and the rest of the last group becomes zeros (a NaN or
           // Inf stored past the length would leak through P = 0).  The
           // quantised path's rows are dequantised to zeros already.
           const int nk = QB ? 4 : min(4, max(0, (nv - 64 * h + 15) >> 4));
-          if (!QB && nk > 0 && nv - 64 * h < 16 * nk)
-            zero_z_rows(saddr(ra ? s.sring : s.zring) + uint32_t(rg.slot * kZSlotBytes), nv - 64 * h, 16 * nk);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {   // K = 16 tokens per MMA
-            if (!QB && kk >= nk) break;
-            const uint64_t a = za + uint64_t((kk * 16 * 128) >> 4);
-#pragma unroll
-            for (int part = 0; part < PS; ++part) {   // P = P_hi (+ P_lo for bf16)
-              const uint64_t bd = pb + uint64_t((part * pbuf_bytes<NP>() + h * NP * 128 + kk * 32) >> 4);
-              tc_mma(d, a, bd, id_z, (first && h == 0 && kk == 0 && part == 0) ? 0u : 1u);
-            }
+          if (!QB && nk > 0 && nv - 64 * h < 16 * nk) {
+            if (__shfl_sync(0xffffffffu, int(ok), 0))
+              zero_z_rows(zring + uint32_t(rg.slot * kZSlotBytes), nv - 64 * h, 16 * nk, lane);
           }
-          tc_commit(saddr(&zempty[rg.slot]));
+          if (lane == 0 && ok) {
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(ZC0 + (SG ? j / ch : j) * NP);
+            const uint64_t za = za0 + uint64_t((rg.slot * kZSlotBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {   // K = 16 tokens per MMA
+              if (!QB && kk >= nk) break;
+              const uint64_t a = za + uint64_t((kk * 16 * 128) >> 4);
+#pragma unroll
+              for (int part = 0; part < PS; ++part) {   // P = P_hi (+ P_lo for bf16)
+                const uint64_t bd = pb + uint64_t((part * pbuf_bytes<NP>() + h * NP * 128 + kk * 32) >> 4);
+                tc_mma(d, a, bd, id_z, (first && h == 0 && kk == 0 && part == 0) ? 0u : 1u);
+              }
+            }
+            tc_commit(saddr(&zempty[rg.slot]));
+          }
           rg.advance();
         }
-        if (!ok) break;
-        tc_commit(saddr(&s.z_done[i & 1]));
-        if (QB) {   // the tile's scale table is free once its Z MMAs are complete
-          tc_commit(saddr(&s.zsc_empty[sbi]));
-          if (++sbi == kScaleBufs) sbi = 0;
+        if (lane == 0 && ok) {
+          tc_commit(saddr(&s.z_done[i & 1]));
+          if (QB) {   // the tile's scale table is free once its Z MMAs are complete
+            tc_commit(saddr(&s.zsc_empty[sbi]));
+            if (++sbi == kScaleBufs) sbi = 0;
+          }
+          if (*s.abort_flag) ok = false;
         }
         it.next();
-        if (*s.abort_flag) ok = false;
       }
-      if (!ok) set_abort(s, status);
-      tc_commit(saddr(&s.drain[kind]));
-      mbar_wait(saddr(&s.drain[kind]), 0);
+      if (lane == 0) {
+        if (!ok) set_abort(s, status);
+        tc_commit(saddr(&s.drain[kind]));
+        mbar_wait(saddr(&s.drain[kind]), 0);
+      }
     }
     __syncwarp();
   } else {

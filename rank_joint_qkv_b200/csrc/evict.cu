@@ -52,6 +52,15 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
   return v;
 }
 
+// Two consecutive words from an even one on.
+__device__ __forceinline__ unsigned long long peer_pair(const uint32_t* p, uint32_t rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  unsigned long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
+  return v;
+}
+
 // Order-preserving integer of a weight; NaN below everything, -0 equal to 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) return 0u;
@@ -94,7 +103,7 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
                int32_t* kept, int32_t* __restrict__ status, int CS) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
-  __shared__ uint32_t hist[3][kBins];
+  __shared__ __align__(8) uint32_t hist[3][kBins];
   __shared__ uint32_t red[33];
   __shared__ uint32_t found[2];    // digit, count above it
   __shared__ uint32_t counts[2];   // this CTA's rows above the threshold (or kept anyway), and equal to it
@@ -160,9 +169,13 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
     const int bin = 2 * (kSelThreads - 1 - tid);
     uint32_t top = 0, low = 0;
     if (CS > 1) {
-      for (int c = 0; c < CS; ++c) {
-        top += peer_word(&hist[pass][bin + 1], uint32_t(c));
-        low += peer_word(&hist[pass][bin], uint32_t(c));
+      unsigned long long v[kMaxCluster];   // both bins of every CTA, the loads in flight together
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) v[c] = c < CS ? peer_pair(&hist[pass][bin], uint32_t(c)) : 0ull;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        top += uint32_t(v[c] >> 32);
+        low += uint32_t(v[c]);
       }
     } else {
       top = hist[pass][bin + 1];

@@ -1241,7 +1241,9 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
 // 1); the scores go to the workspace, [B][H][max_len] fp32, and the split
 // kernel that follows takes them instead of computing C . q~.
 //
-// Per CTA: the flattened tile range of the split schedule.  Per tile and head
+// Per CTA: an equal run of the flattened (tile, head pair) units, so that a
+// few long tiles' worth of heads still fill the GPU (82 tiles of 16 pairs on
+// 148 SMs: nine units a CTA instead of sixteen).  Per tile and head
 // pair the producer streams (latent box, W^u_k^T box) pairs through a ring,
 // one thread issues the MMAs into one of two TMEM buffers (256 columns each),
 // and four epilogue warps (one TMEM lane per token) apply the rotation with
@@ -1276,10 +1278,16 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NI = r / 64, NPAIR = (H + 1) / 2;
   const long long T = sched[B];
-  const long long tb = dev::split_begin(blockIdx.x, G, T);
-  const long long te = dev::split_begin(blockIdx.x + 1, G, T);
-  if (tb >= te) return;   // uniform across the CTA, before any barrier or TMEM use
+  // this CTA's run of (tile, head pair) units [ub, ue): tiles [tb, te), the
+  // first and last of them perhaps with some of their pairs
+  const long long ub = dev::split_begin(blockIdx.x, G, T * NPAIR);
+  const long long ue = dev::split_begin(blockIdx.x + 1, G, T * NPAIR);
+  if (ub >= ue) return;   // uniform across the CTA, before any barrier or TMEM use
+  const long long tb = dev::quotient(ub, NPAIR), te = dev::quotient(ue + NPAIR - 1, NPAIR);
   const int n = int(te - tb);
+  const int p_first = int(ub - tb * NPAIR), p_last = int(ue - (te - 1) * NPAIR);
+  auto pair_lo = [&](int i) { return i == 0 ? p_first : 0; };
+  auto pair_hi = [&](int i) { return i == n - 1 ? p_last : NPAIR; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ns; ++i) {
@@ -1315,7 +1323,7 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
       const int row = it.b * max_len + it.t0();   // rows past the length give keys nobody reads
-      for (int p = 0; p < NPAIR && ok; ++p)
+      for (int p = pair_lo(i); p < pair_hi(i) && ok; ++p)
         for (int u = 0; u < NI; ++u) {
           if (!__all_sync(0xffffffffu, mbar_wait(saddr(&empty[rg.slot]), rg.phase ^ 1u))) { ok = false; break; }
           const uint32_t dst = ring0 + uint32_t(rg.slot) * kRopeSlotBytes;
@@ -1347,7 +1355,7 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
       long long pc = 0;   // head pairs issued
       bool ok = true;
       for (int i = 0; i < n && ok; ++i)
-        for (int p = 0; p < NPAIR && ok; ++p, ++pc) {
+        for (int p = pair_lo(i); p < pair_hi(i) && ok; ++p, ++pc) {
           const int kb = int(pc & 1);
           if (pc >= 2 && !mbar_wait(saddr(&kempty[kb]), uint32_t((pc - 2) >> 1) & 1u)) { ok = false; break; }
           const uint32_t d = tmem + uint32_t(kb * 256);
@@ -1396,7 +1404,7 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
       }
       const float* qb = qrot + size_t(b) * E;
       int fail = 0;
-      for (int p = 0; p < NPAIR; ++p, ++pc) {
+      for (int p = pair_lo(i); p < pair_hi(i); ++p, ++pc) {
         const int kb = int(pc & 1);
         fail = group_or(!mbar_wait(saddr(&kfull[kb]), uint32_t(pc >> 1) & 1u));   // uniform
         if (fail) break;

@@ -137,16 +137,17 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
   const unsigned lo = unsigned(sink), hi = unsigned(n - recent);
   const bool held = r1 - r0 <= unsigned(kSelChunk);   // one chunk: its keys stay in registers
   uint32_t key[kSelKeys];
-  auto load = [&](unsigned c0) {   // thread's rows c0 + 8 tid .. + 7; rows that are no candidates: 0, and never counted
+  uint32_t cand = 0, fixed = 0;   // bit i: row c0 + 8 tid + i is a candidate; is kept whatever the weights
+  auto load = [&](unsigned c0) {
+    cand = fixed = 0;
 #pragma unroll
     for (int i = 0; i < kSelKeys; ++i) {
       const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
-      key[i] = t < r1 && t >= lo && t < hi ? weight_key(__ldg(w + t)) : 0u;
+      const bool in = t < r1, mid = t >= lo && t < hi;
+      cand |= uint32_t(in && mid) << i;
+      fixed |= uint32_t(in && !mid) << i;
+      key[i] = in && mid ? weight_key(__ldg(w + t)) : 0u;
     }
-  };
-  auto candidate = [&](unsigned c0, int i) {
-    const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
-    return t < r1 && t >= lo && t < hi;
   };
   if (held) load(r0);
   // threshold: the K-th largest key of the candidates
@@ -161,7 +162,7 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
       if (!held) load(c0);
 #pragma unroll
       for (int i = 0; i < kSelKeys; ++i)
-        if (candidate(c0, i) && (pass == 0 || (key[i] >> above) == (prefix >> above)))
+        if ((cand >> i & 1u) && (pass == 0 || (key[i] >> above) == (prefix >> above)))
           atomicAdd(&hist[pass][(key[i] >> shift) & (digits - 1)], 1u);
     }
     if (CS > 1) cluster_sync(); else __syncthreads();
@@ -192,27 +193,36 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
     prefix |= found[0] << shift;
     K -= found[1];   // still to take among the keys equal so far
   }
-  // The K lowest rows equal to the threshold are taken.  above: kept whatever the others are
-  auto above_at = [&](unsigned c0, int i) {
-    const unsigned t = c0 + unsigned(tid) * kSelKeys + i;
-    return t < r1 && (t < lo || t >= hi || (some && key[i] > prefix));
+  // The K lowest rows equal to the threshold are taken.  Bits of the thread's
+  // rows kept whatever the others are, and of those equal.
+  auto sort_out = [&](uint32_t* above, uint32_t* equal) {
+    *above = fixed;
+    *equal = 0;
+    if (!some) return;
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      *above |= (cand & (uint32_t(key[i] > prefix) << i));
+      *equal |= (cand & (uint32_t(key[i] == prefix) << i));
+    }
   };
-  auto equal_at = [&](unsigned c0, int i) { return some && candidate(c0, i) && key[i] == prefix; };
   unsigned out = 0, eq = 0;   // kept rows and equal rows before this CTA's
   if (CS > 1) {
     unsigned na = 0, ne = 0;
     for (unsigned c0 = r0; c0 < r1; c0 += kSelChunk) {
       if (!held) load(c0);
-#pragma unroll
-      for (int i = 0; i < kSelKeys; ++i) {
-        na += above_at(c0, i);
-        ne += equal_at(c0, i);
-      }
+      uint32_t above, equal;
+      sort_out(&above, &equal);
+      na += __popc(above);
+      ne += __popc(equal);
     }
-    uint32_t ta, te;
-    cta_exclusive(na, red, &ta);
-    cta_exclusive(ne, red, &te);
-    if (tid == 0) { counts[0] = ta; counts[1] = te; }
+    if (tid < 2) counts[tid] = 0;
+    __syncthreads();
+    na = __reduce_add_sync(0xffffffffu, na);
+    ne = __reduce_add_sync(0xffffffffu, ne);
+    if ((tid & 31) == 0) {
+      atomicAdd(&counts[0], na);
+      atomicAdd(&counts[1], ne);
+    }
     cluster_sync();
     for (uint32_t c = 0; c < rank; ++c) {
       const uint32_t e = peer_word(&counts[1], c);
@@ -222,24 +232,23 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
   }
   for (unsigned c0 = r0; c0 < r1; c0 += kSelChunk) {
     if (!held) load(c0);
-    uint32_t mine = 0;   // 16 bits each: rows above, rows equal (a chunk has 8192)
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) mine += (uint32_t(above_at(c0, i)) << 16) + uint32_t(equal_at(c0, i));
-    uint32_t all;
-    const uint32_t before = cta_exclusive(mine, red, &all);
+    uint32_t above, equal;
+    sort_out(&above, &equal);
+    uint32_t all;   // 16 bits each: rows above, rows equal (a chunk has 8192)
+    const uint32_t before = cta_exclusive((uint32_t(__popc(above)) << 16) + uint32_t(__popc(equal)), red, &all);
     const unsigned left = K - min(K, eq);   // equal rows still to take at the chunk's start
     unsigned a = before >> 16, e = before & 0xFFFFu;
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) {
-      const bool ab = above_at(c0, i), eqi = equal_at(c0, i);
-      if (ab || (eqi && e < left)) {
+    for (uint32_t rest = above | equal; rest; rest &= rest - 1) {
+      const int i = __ffs(rest) - 1;
+      const bool ab = above >> i & 1u;
+      if (ab || e < left) {
         const unsigned at = out + a + min(e, left);
         const int32_t t = int32_t(c0 + unsigned(tid) * kSelKeys + i);
         sb[at] = t;
         if (kb) kb[at] = t;
       }
       a += ab;
-      e += eqi;
+      e += !ab;
     }
     out += (all >> 16) + min(all & 0xFFFFu, left);
     eq += all & 0xFFFFu;

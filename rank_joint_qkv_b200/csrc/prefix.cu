@@ -31,7 +31,7 @@
 // a pass of both products, so that the scores are as good as the integer ones
 // of the sequences' own rows.
 //
-// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM and the MMA thread,
+// Roles (192 threads per CTA): warp 0 TMA producer, warp 1 TMEM and the MMA thread,
 // warps 2-5 epilogue; two TMEM accumulators of 256 columns, so the epilogue
 // of a unit runs under the next one's products.  Every wait is bounded.
 #include <cuda.h>
@@ -48,15 +48,17 @@ namespace {
 constexpr int kPxThreads = 192;
 constexpr int kPxA = 128 * 128;            // A box: 128 rows x 64 K x 2 bytes
 constexpr int kPxB = 256 * 128;            // B: 256 N x 64 K x 2 bytes
-constexpr int kPxMaxSlots = 4;
+constexpr int kPxMaxSlots = 6;
 constexpr int kPxStage = 32 * 128;         // epilogue staging: 32 rows x 128 bytes, two per warp
 constexpr float kRefStep = 15.f;           // log2 units between references
 constexpr int kPxSmem = 232448;            // opt-in dynamic shared memory per block on sm_100
 
-template <int AP>
-__host__ __device__ constexpr int px_slot() { return AP * kPxA + kPxB; }
-template <int AP>
-__host__ __device__ constexpr int px_slots() { return AP == 2 ? 3 : 4; }
+// One ring slot per CTA, and slots in 192 KB.  A CTA of a pair holds its own
+// 128 query rows and half of B.
+template <int AP, bool PAIR>
+__host__ __device__ constexpr int px_slot() { return AP * kPxA + (PAIR ? kPxB / 2 : kPxB); }
+template <int AP, bool PAIR>
+__host__ __device__ constexpr int px_slots() { return 192 * 1024 / px_slot<AP, PAIR>(); }
 
 struct PxArgs {
   int B, H, r, plen, nb, MB, tiles, ppad, SP;
@@ -71,16 +73,23 @@ struct PxArgs {
 // Tiles [t0, t1) of token split sp.
 __device__ __forceinline__ int split_tile(int sp, int tiles, int SP) { return int((long long)sp * tiles / SP); }
 
+// PAIR: two CTAs of a cluster work on 256 query rows, each with its own 128 in
+// its shared memory and TMEM and half of the B tile (tcgen05 cta_group::2;
+// the first CTA issues).  The products are bound by what L2 feeds the SMs:
+// per 64 K of two A parts a CTA alone reads 64 KB for 1024 cycles of MMA, one
+// of a pair 48 KB (one A part: 48 KB for 512 cycles, and 32 KB).
+//
 // AP: 16-bit parts of A in pass 0 (a second pass, for the lo part of an
 // expanded prefix, takes A's first part only).  CP: passes (parts of C).
 // PS: parts of P that the scores' epilogue writes.
-template <bool BF16, int AP, int CP, int PS, bool VALUES>
+template <bool BF16, int AP, int CP, int PS, bool VALUES, bool PAIR>
 __global__ void __launch_bounds__(kPxThreads, 1)
 k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
               const __grid_constant__ CUtensorMap tm_b1, const PxArgs g) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
-  constexpr int kSlot = px_slot<AP>(), ns = px_slots<AP>();
+  constexpr int kSlot = px_slot<AP, PAIR>(), ns = px_slots<AP, PAIR>();
+  constexpr int W = PAIR ? 2 : 1;            // CTAs, and row blocks, per unit
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -95,15 +104,19 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NB = VALUES ? (g.r + 255) / 256 : g.tiles;       // column blocks of the product
-  const int units = g.MB * NB * (VALUES ? g.SP : 1);
-  const int mine = units > int(blockIdx.x) ? (units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
-  if (mine == 0) return;   // uniform across the CTA
-  // unit u: row block u % MB, so that the blocks in flight share their B tiles in L2
+  const int MU = (g.MB + W - 1) / W;                          // row blocks per column block, in units
+  const int units = MU * NB * (VALUES ? g.SP : 1);
+  const int walker = int(blockIdx.x) / W, walkers = int(gridDim.x) / W;
+  const uint32_t rank = PAIR ? pair_rank() : 0u;
+  const int mine = units > walker ? (units - 1 - walker) / walkers + 1 : 0;
+  if (mine == 0) return;   // uniform across the CTA (and the pair)
+  // unit u: row block(s) u % MU, so that the blocks in flight share their B
+  // tiles in L2.  mb: this CTA's; the last pair's second may lie past MB (zeros)
   auto unit = [&](int j, int* mb, int* n, int* sp, int* k0, int* k1) {
-    const int u = int(blockIdx.x) + j * int(gridDim.x);
-    *mb = u % g.MB;
-    *n = (u / g.MB) % NB;
-    *sp = (u / g.MB) / NB;
+    const int u = walker + j * walkers;
+    *mb = (u % MU) * W + int(rank);
+    *n = (u / MU) % NB;
+    *sp = (u / MU) / NB;
     if (VALUES) {   // 64-token blocks of the split's tiles
       *k0 = 4 * split_tile(*sp, g.tiles, g.SP);
       *k1 = min(4 * split_tile(*sp + 1, g.tiles, g.SP), (g.plen + 63) / 64);
@@ -120,20 +133,26 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(saddr(&afull[i]), 1);
-      mbar_init(saddr(&aempty[i]), 1);
+      mbar_init(saddr(&aempty[i]), W);
     }
     mbar_init(saddr(drain), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     saddr(tmem_holder))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     tc_fence_before();
   }
   __syncthreads();
+  if (PAIR) pair_sync();   // both CTAs' barriers and TMEM stand before either is used by the other
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t ring0 = saddr(base);
@@ -153,18 +172,34 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
           if (!__all_sync(0xffffffffu, mbar_wait(saddr(&empty[rg.slot]), rg.phase ^ 1u))) { ok = false; break; }
           const uint32_t dst = ring0 + uint32_t(rg.slot) * kSlot;
           const uint32_t fb = saddr(&full[rg.slot]);
-          if (lane == 0) mbar_expect_tx(fb, parts * abytes + uint32_t(kPxB));
-          __syncwarp();
           const int ln = int(k % 10) * 3;   // rotating issuing lanes, one per operation
-          if (lane >= ln && lane < ln + parts) {
-            const int part = lane - ln;
-            if (VALUES) tma_load_3d(dst + part * kPxA, &tm_a, 64 * ki, mb * 128, part, fb);
-            else tma_load_4d(dst + part * kPxA, &tm_a, 64 * ki, 0, part, mb * g.nb, fb);
-          }
-          if (lane == ln + 2) {
-            const CUtensorMap* tb = pass == 0 ? &tm_b0 : &tm_b1;
-            if (VALUES) tma_load_3d(dst + AP * kPxA, tb, 0, 64 * ki, 4 * n, fb);
-            else tma_load_2d(dst + AP * kPxA, tb, 64 * ki, kPxTile * n, fb);
+          const CUtensorMap* tb = pass == 0 ? &tm_b0 : &tm_b1;
+          const int part = lane - ln;
+          if constexpr (PAIR) {
+            // both CTAs' bytes are counted on the first's barrier, which its
+            // MMA thread waits for
+            if (rank == 0 && lane == 0) mbar_expect_tx(fb, 2u * parts * abytes + uint32_t(kPxB));
+            __syncwarp();
+            const uint32_t lb = pair_leader(fb);
+            if (lane >= ln && lane < ln + parts) {
+              if (VALUES) tma_load_3d(dst + part * kPxA, &tm_a, 64 * ki, mb * 128, part, lb, PairLoad());
+              else tma_load_4d(dst + part * kPxA, &tm_a, 64 * ki, 0, part, mb * g.nb, lb, PairLoad());
+            }
+            if (lane == ln + 2) {
+              if (VALUES) tma_load_3d(dst + AP * kPxA, tb, 0, 64 * ki, 4 * n + 2 * int(rank), lb, PairLoad());
+              else tma_load_2d(dst + AP * kPxA, tb, 64 * ki, kPxTile * n + 128 * int(rank), lb, PairLoad());
+            }
+          } else {
+            if (lane == 0) mbar_expect_tx(fb, parts * abytes + uint32_t(kPxB));
+            __syncwarp();
+            if (lane >= ln && lane < ln + parts) {
+              if (VALUES) tma_load_3d(dst + part * kPxA, &tm_a, 64 * ki, mb * 128, part, fb);
+              else tma_load_4d(dst + part * kPxA, &tm_a, 64 * ki, 0, part, mb * g.nb, fb);
+            }
+            if (lane == ln + 2) {
+              if (VALUES) tma_load_3d(dst + AP * kPxA, tb, 0, 64 * ki, 4 * n, fb);
+              else tma_load_2d(dst + AP * kPxA, tb, 64 * ki, kPxTile * n, fb);
+            }
           }
           __syncwarp();
           rg.advance();
@@ -176,14 +211,17 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     if (!ok && lane == 0) {
       *abort_flag = 1;
       atomicOr(g.status, QSVD_STATUS_TIMEOUT);
-      for (long long kk = (k > ns ? k - ns : 0); kk < k; ++kk)
-        mbar_wait(saddr(&full[int(kk % ns)]), uint32_t(kk / ns) & 1u);
+      // copies in flight land before the CTA leaves (of a pair: on the first
+      // CTA's barriers, and the second waits for it at the end)
+      if (rank == 0)
+        for (long long kk = (k > ns ? k - ns : 0); kk < k; ++kk)
+          mbar_wait(saddr(&full[int(kk % ns)]), uint32_t(kk / ns) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(128, 256, BF16, false, VALUES);   // values: C is the MN-major operand
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id = idesc_f16(128 * W, 256, BF16, false, VALUES);   // values: C is the MN-major operand
       const uint64_t da0 = sdesc(ring0, 16, 1024);                          // K-major
       const uint64_t db0 = sdesc(ring0 + AP * kPxA, VALUES ? 64 * 128 : 16, 1024);
       constexpr int kBStep = VALUES ? 16 * 128 : 32;                        // 16 tokens, or 16 channels
@@ -206,24 +244,29 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             for (int part = 0; part < parts; ++part) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {   // K = 16 per MMA
-                tc_mma(d, da0 + off + uint64_t((part * kPxA + kk * 32) >> 4), db0 + off + uint64_t((kk * kBStep) >> 4), id,
-                       acc);
+                const uint64_t a = da0 + off + uint64_t((part * kPxA + kk * 32) >> 4);
+                const uint64_t b = db0 + off + uint64_t((kk * kBStep) >> 4);
+                if (PAIR) tc_mma_pair(d, a, b, id, acc);
+                else tc_mma(d, a, b, id, acc);
                 acc = 1;
               }
             }
-            tc_commit(saddr(&empty[rg.slot]));
+            if (PAIR) tc_commit_pair(saddr(&empty[rg.slot]));
+            else tc_commit(saddr(&empty[rg.slot]));
             rg.advance();
           }
         }
         if (!ok) break;
-        tc_commit(saddr(&afull[ab]));
+        if (PAIR) tc_commit_pair(saddr(&afull[ab]));
+        else tc_commit(saddr(&afull[ab]));
         if (*abort_flag) ok = false;
       }
       if (!ok) {
         *abort_flag = 1;
         atomicOr(g.status, QSVD_STATUS_TIMEOUT);
       }
-      tc_commit(saddr(drain));
+      if (PAIR) tc_commit_pair(saddr(drain));
+      else tc_commit(saddr(drain));
       mbar_wait(saddr(drain), 0);
     }
     __syncwarp();
@@ -263,7 +306,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         break;
       }
       tc_fence_after();
-      const int live_rows = min(g.nb, g.B - mb * g.nb) * g.H;   // rows of the block that are queries
+      const int live_rows = min(g.nb, g.B - mb * g.nb) * g.H;   // rows of the block that are queries (none past MB)
       const uint32_t ta = tmem + lane_off + uint32_t(ab * 256);
       if (VALUES) {
         // rows mb nb H + t of the split's [B H][r]
@@ -336,15 +379,20 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       }
       tc_fence_before();
       group_sync();
-      if (t == 0) mbar_arrive(saddr(&aempty[ab]));
+      if (t == 0) {
+        if (PAIR) pair_arrive(pair_leader(saddr(&aempty[ab])));
+        else mbar_arrive(saddr(&aempty[ab]));
+      }
       if (group_or(*abort_flag)) break;
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) pair_sync();   // no CTA of a pair leaves while the other's copies, MMAs or arrivals still reach it
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -572,21 +620,46 @@ bool encode(CUtensorMap* tm, bool bf16, int rank, const void* p, const cuuint64_
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16, int AP, int CP, int PS, bool VALUES>
-cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, int sms,
+template <bool BF16, int AP, int CP, int PS, bool VALUES, bool PAIR>
+cudaError_t gemm_p(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, int sms,
                    cudaStream_t s) {
-  const long long units = (long long)g.MB * (VALUES ? (long long)((g.r + 255) / 256) * g.SP : g.tiles);
+  constexpr int W = PAIR ? 2 : 1;
+  const long long units = (long long)((g.MB + W - 1) / W) * (VALUES ? (long long)((g.r + 255) / 256) * g.SP : g.tiles);
   if (units > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  const int grid = units < sms ? int(units) : sms;
-  const size_t smem = 1024 + size_t(px_slots<AP>()) * px_slot<AP>() + 8 * kPxStage + (2 * kPxMaxSlots + 5) * 8 + 16;
-  static_assert(1024 + px_slots<AP>() * px_slot<AP>() + 8 * kPxStage + (2 * kPxMaxSlots + 5) * 8 + 16 <= kPxSmem, "ring fits");
-  auto kern = k_prefix_gemm<BF16, AP, CP, PS, VALUES>;
+  const int walkers = units < sms / W ? int(units) : sms / W;
+  constexpr size_t smem = 1024 + size_t(px_slots<AP, PAIR>()) * px_slot<AP, PAIR>() + 8 * kPxStage +
+                          (2 * kPxMaxSlots + 5) * 8 + 16;
+  static_assert(px_slots<AP, PAIR>() <= kPxMaxSlots && smem <= kPxSmem, "ring fits");
+  auto kern = k_prefix_gemm<BF16, AP, CP, PS, VALUES, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kPxThreads), smem, s, ta, tb0, tb1, g);
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(walkers * W));
+  cfg.blockDim = dim3(kPxThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tb0, tb1, g);
   if (e != cudaSuccess) return e;
   note_launch();
   return check_launch();
+}
+
+// Pairs where there is a second block of query rows.
+template <bool BF16, int AP, int CP, int PS, bool VALUES>
+cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, int sms,
+                   cudaStream_t s) {
+  return g.MB > 1 ? gemm_p<BF16, AP, CP, PS, VALUES, true>(ta, tb0, tb1, g, sms, s)
+                  : gemm_p<BF16, AP, CP, PS, VALUES, false>(ta, tb0, tb1, g, sms, s);
 }
 
 // C parts: CP copies of [plen][r] 16-bit rows at `c`, one after another.
@@ -614,9 +687,9 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
   for (int part = 0; part < 2; ++part) {
     const uint8_t* cp = static_cast<const uint8_t*>(c) + (part < CP ? size_t(part) * L.plen * d.r * 2 : 0);
     const cuuint64_t sd[2] = {r, P}, ss[1] = {r * 2};   // scores: 256 tokens x 64 channels, K-major; rows past P zeros
-    const cuuint32_t sb[2] = {64, kPxTile};
+    const cuuint32_t sb[2] = {64, cuuint32_t(L.MB > 1 ? kPxTile / 2 : kPxTile)};   // (a pair's CTA loads half)
     const cuuint64_t vd[3] = {64, P, r / 64}, vs[2] = {r * 2, 128};   // values: 64 tokens x 256 channels, MN-major
-    const cuuint32_t vb[3] = {64, 64, 4};
+    const cuuint32_t vb[3] = {64, 64, cuuint32_t(L.MB > 1 ? 2 : 4)};
     if (!encode(&tbs[part], BF16, 2, cp, sd, ss, sb) || !encode(&tbv[part], BF16, 3, cp, vd, vs, vb))
       return cudaErrorInvalidValue;
   }
@@ -663,11 +736,12 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     // token splits of the value product: the fewest that come within 3% of
     // the best fill of the GPU's waves (a split costs B H r float32 partials,
     // written and merged)
-    const long long units = (long long)L.MB * ((d.r + 255) / 256);
+    const int W = L.MB > 1 ? 2 : 1;   // CTAs per unit
+    const long long units = (long long)((L.MB + W - 1) / W) * ((d.r + 255) / 256), walkers = sms / W > 0 ? sms / W : 1;
     double best = 1e30;
     for (int pass = 0; pass < 2; ++pass)
       for (int sp = 1; sp <= 16 && sp <= L.tiles; ++sp) {
-        const double cost = double((units * sp + sms - 1) / sms) / sp;
+        const double cost = double((units * sp + walkers - 1) / walkers) / sp;
         if (pass == 0 && cost < best) best = cost;
         if (pass == 1 && cost <= best * 1.03) { L.SP = sp; break; }
       }

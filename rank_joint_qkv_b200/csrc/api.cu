@@ -474,6 +474,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     }
     if (e != cudaSuccess) return cuda_fail(e, "query prologue");
   }
+  if (px && (e = launch_prefix_expand(d, X, Wb, x.prefix, x.prefix_scales, s)) != cudaSuccess)
+    return cuda_fail(e, "prefix");
   if (split_any) {
     if (d.rope && kernel == QSVD_KERNEL_TCGEN05_CTA) {
       e = cudaSuccess;

@@ -169,6 +169,11 @@ cudaError_t check_launch();         // cudaGetLastError after a launch
 // memory.  It calls dev::pdl_trigger() after the wait, so a kernel starts
 // only once its predecessor's predecessor has completed, and a chain of such
 // kernels stays ordered transitively.
+// A kernel that needs nothing of its predecessor in the stream, only of the
+// ones before that, may leave the wait to its end (before it triggers): it
+// started once every CTA of the predecessor had passed its own wait, so what
+// came before the predecessor is complete and visible, and it runs beside the
+// predecessor; the wait at its end keeps the chain ordered for what follows.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {

@@ -15,7 +15,8 @@
 //                           (thread = query row) takes the tile's maximum,
 //                           writes 2^(s - ref) and keeps ref and the sum
 //   k_prefix_norm           per row and token split: the reference of the
-//                           split's tiles made one, m and l of the split
+//                           split's tiles made one, m and l of the split (not
+//                           needed where each split is one tile)
 //   k_prefix_gemm<values>   128 query rows x 256 channels per unit over a
 //                           split's tokens; float32 partials for the merge
 //
@@ -63,8 +64,10 @@ __host__ __device__ constexpr int px_slots() { return 192 * 1024 / px_slot<AP, P
 struct PxArgs {
   int B, H, r, plen, nb, MB, tiles, ppad, SP;
   void* p;        // [AP parts][MB 128][ppad] P (scores: written)
-  float* mt;      // [tiles][MB 128] reference of a tile
-  float* lt;      // [tiles][MB 128] sum of its P
+  float* mt;      // [tiles][MB 128] reference of a tile ...
+  float* lt;      // [tiles][MB 128] ... and the sum of its P
+  float* pm;      // [SP B][H] instead of both, where every tile is a token
+  float* pl;      // split of its own (tiles == SP)
   float* pz;      // [SP B][H][r] (values: written)
   float gain;     // on the scores (see launch_prefix)
   int32_t* status;
@@ -75,9 +78,8 @@ __device__ __forceinline__ int split_tile(int sp, int tiles, int SP) { return in
 
 // PAIR: two CTAs of a cluster work on 256 query rows, each with its own 128 in
 // its shared memory and TMEM and half of the B tile (tcgen05 cta_group::2;
-// the first CTA issues).  The products are bound by what L2 feeds the SMs:
-// per 64 K of two A parts a CTA alone reads 64 KB for 1024 cycles of MMA, one
-// of a pair 48 KB (one A part: 48 KB for 512 cycles, and 32 KB).
+// the first CTA issues): per 64 K of two A parts a CTA alone reads 64 KB from
+// L2, one of a pair 48 KB (one A part: 48 KB, and 32 KB).
 //
 // AP: 16-bit parts of A in pass 0 (a second pass, for the lo part of an
 // expanded prefix, takes A's first part only).  CP: passes (parts of C).
@@ -86,8 +88,13 @@ template <bool BF16, int AP, int CP, int PS, bool VALUES, bool PAIR>
 __global__ void __launch_bounds__(kPxThreads, 1)
 k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
               const __grid_constant__ CUtensorMap tm_b1, const PxArgs g) {
-  dev::pdl_wait();   // see launch_pdl
-  dev::pdl_trigger();
+  if (VALUES) {
+    dev::pdl_wait();   // see launch_pdl
+    dev::pdl_trigger();
+  }
+  // (the scores run beside the own rows' split kernel before them in the
+  // stream: its CTAs have waited for the query's parts, and nothing of its own
+  // is read here; this kernel's wait is at its end)
   constexpr int kSlot = px_slot<AP, PAIR>(), ns = px_slots<AP, PAIR>();
   constexpr int W = PAIR ? 2 : 1;            // CTAs, and row blocks, per unit
   extern __shared__ uint8_t smem_raw[];
@@ -109,7 +116,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   const int walker = int(blockIdx.x) / W, walkers = int(gridDim.x) / W;
   const uint32_t rank = PAIR ? pair_rank() : 0u;
   const int mine = units > walker ? (units - 1 - walker) / walkers + 1 : 0;
-  if (mine == 0) return;   // uniform across the CTA (and the pair)
+  if (mine == 0) return;   // uniform across the CTA (and the pair); no launch has such CTAs
   // unit u: row block(s) u % MU, so that the blocks in flight share their B
   // tiles in L2.  mb: this CTA's; the last pair's second may lie past MB (zeros)
   auto unit = [&](int j, int* mb, int* n, int* sp, int* k0, int* k1) {
@@ -373,8 +380,10 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
           __syncwarp();
         }
         if (t < live_rows) {
-          g.mt[size_t(n) * rows + size_t(mb) * 128 + t] = ref;
-          g.lt[size_t(n) * rows + size_t(mb) * 128 + t] = sum;
+          const bool own = g.tiles == g.SP;
+          const size_t at = own ? (size_t(n) * g.B + size_t(mb) * g.nb) * g.H + t : size_t(n) * rows + size_t(mb) * 128 + t;
+          (own ? g.pm : g.mt)[at] = ref;
+          (own ? g.pl : g.lt)[at] = sum;
         }
       }
       tc_fence_before();
@@ -385,6 +394,10 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       }
       if (group_or(*abort_flag)) break;
     }
+  }
+  if (!VALUES) {
+    dev::pdl_wait();
+    dev::pdl_trigger();
   }
   tc_fence_before();
   __syncthreads();
@@ -654,11 +667,10 @@ cudaError_t gemm_p(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
   return check_launch();
 }
 
-// Pairs where there is a second block of query rows.
 template <bool BF16, int AP, int CP, int PS, bool VALUES>
-cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, int sms,
-                   cudaStream_t s) {
-  return g.MB > 1 ? gemm_p<BF16, AP, CP, PS, VALUES, true>(ta, tb0, tb1, g, sms, s)
+cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const PxArgs& g, bool pair,
+                   int sms, cudaStream_t s) {
+  return pair ? gemm_p<BF16, AP, CP, PS, VALUES, true>(ta, tb0, tb1, g, sms, s)
                   : gemm_p<BF16, AP, CP, PS, VALUES, false>(ta, tb0, tb1, g, sms, s);
 }
 
@@ -687,25 +699,28 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
   for (int part = 0; part < 2; ++part) {
     const uint8_t* cp = static_cast<const uint8_t*>(c) + (part < CP ? size_t(part) * L.plen * d.r * 2 : 0);
     const cuuint64_t sd[2] = {r, P}, ss[1] = {r * 2};   // scores: 256 tokens x 64 channels, K-major; rows past P zeros
-    const cuuint32_t sb[2] = {64, cuuint32_t(L.MB > 1 ? kPxTile / 2 : kPxTile)};   // (a pair's CTA loads half)
+    const cuuint32_t sb[2] = {64, cuuint32_t(L.pair ? kPxTile / 2 : kPxTile)};   // (a pair's CTA loads half)
     const cuuint64_t vd[3] = {64, P, r / 64}, vs[2] = {r * 2, 128};   // values: 64 tokens x 256 channels, MN-major
-    const cuuint32_t vb[3] = {64, 64, cuuint32_t(L.MB > 1 ? 2 : 4)};
+    const cuuint32_t vb[3] = {64, 64, cuuint32_t(L.pair ? 2 : 4)};
     if (!encode(&tbs[part], BF16, 2, cp, sd, ss, sb) || !encode(&tbv[part], BF16, 3, cp, vd, vs, vb))
       return cudaErrorInvalidValue;
   }
   PxArgs g{d.batch, d.H, d.r, L.plen, L.nb, L.MB, L.tiles, L.ppad, L.SP, ws + L.p,
-           reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pz),
+           reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pm),
+           reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz),
            gain, status};
-  cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, sms, s);
+  cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
   if (e != cudaSuccess) return e;
-  const long long bh = (long long)d.batch * d.H;
-  e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned((bh + 7) / 8), unsigned(L.SP)), dim3(256), 0, s,
-                 reinterpret_cast<T16*>(ws + L.p), g.mt, g.lt, reinterpret_cast<float*>(ws + L.pm),
-                 reinterpret_cast<float*>(ws + L.pl), d.batch, d.H, L.nb, L.MB, L.tiles, L.ppad, L.SP);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  if ((e = check_launch()) != cudaSuccess) return e;
-  return gemm_t<BF16, PS, CP, PS, true>(tp, tbv[0], tbv[1], g, sms, s);
+  if (L.tiles != L.SP) {
+    const long long bh = (long long)d.batch * d.H;
+    e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned((bh + 7) / 8), unsigned(L.SP)), dim3(256), 0, s,
+                   reinterpret_cast<T16*>(ws + L.p), g.mt, g.lt, g.pm, g.pl, d.batch, d.H, L.nb, L.MB, L.tiles, L.ppad,
+                   L.SP);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    if ((e = check_launch()) != cudaSuccess) return e;
+  }
+  return gemm_t<BF16, PS, CP, PS, true>(tp, tbv[0], tbv[1], g, L.pair, sms, s);
 }
 
 }  // namespace
@@ -736,7 +751,11 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     // token splits of the value product: the fewest that come within 3% of
     // the best fill of the GPU's waves (a split costs B H r float32 partials,
     // written and merged)
-    const int W = L.MB > 1 ? 2 : 1;   // CTAs per unit
+    // pairs once the scores take more than a wave of single CTAs: at B 64, H 32,
+    // P 16384 (1024 tiles) the step took 395 us without and 377 us with; at
+    // B 16, P 8192 (128 tiles) 128 and 130 us
+    L.pair = L.MB > 1 && (long long)L.MB * L.tiles > sms;
+    const int W = L.pair ? 2 : 1;   // CTAs per unit
     const long long units = (long long)((L.MB + W - 1) / W) * ((d.r + 255) / 256), walkers = sms / W > 0 ? sms / W : 1;
     double best = 1e30;
     for (int pass = 0; pass < 2; ++pass)
@@ -782,15 +801,20 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
   }
   if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
   if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
+  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, status, s);
+}
+
+cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                                 const void* scales, cudaStream_t s) {
+  if (!L.fast || !cache_is_int(d)) return cudaSuccess;
   const size_t vecs = size_t(L.plen) * cache_row_bytes(d) / 16;
-  const unsigned grid = unsigned(vecs / 256 + 1 < size_t(sms) * 8 ? vecs / 256 + 1 : size_t(sms) * 8);
-  cudaError_t e = launch_pdl(d.cache_dtype == QSVD_I8 ? k_prefix_expand<QSVD_I8> : k_prefix_expand<QSVD_I4>, dim3(grid),
+  const unsigned grid = unsigned(vecs / 256 + 1 < 1184 ? vecs / 256 + 1 : 1184);   // eight CTAs an SM
+  const cudaError_t e = launch_pdl(d.cache_dtype == QSVD_I8 ? k_prefix_expand<QSVD_I8> : k_prefix_expand<QSVD_I4>, dim3(grid),
                              dim3(256), 0, s, static_cast<const uint8_t*>(prefix), static_cast<const __half*>(scales),
                              reinterpret_cast<__half*>(ws + L.cparts), L.plen, d.r, d.group);
   if (e != cudaSuccess) return e;
   note_launch();
-  if ((e = check_launch()) != cudaSuccess) return e;
-  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, status, s);
+  return check_launch();
 }
 
 int prefix_score_steps(const qsvd_dims& d) { return d.r / 16 * (cache_is_int(d) ? 3 : 2); }

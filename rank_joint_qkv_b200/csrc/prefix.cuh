@@ -10,6 +10,7 @@ constexpr int kPxTile = 256;   // tokens per score tile
 
 // Sections behind the decode's own workspace.
 struct PrefixLayout {
+  bool pair;        // fast: CTA pairs
   bool fast;        // tensor cores; else the CUDA-core split kernel on B views of the prefix
   int plen, tiles;  // prefix rows, score tiles
   int nb, MB;       // sequences per block of 128 query rows, blocks
@@ -24,6 +25,10 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 // The prefix's partials (m, l, z per slot) from the absorbed query: qt16 its
 // 16-bit parts [B][2][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
 // the tensor cores' scores, for what their accumulation truncates.
+// launch_prefix_expand goes before the own rows' split kernel and
+// launch_prefix directly behind it: the scores wait for nothing of it.
+cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                                 const void* scales, cudaStream_t s);
 cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
                           const void* scales, const void* qt16, const float* qt32, float gain, int sms, int32_t* status,
                           cudaStream_t s);

@@ -15,37 +15,42 @@ constexpr int kRwThreads = 256;
 constexpr int kRwHeads = 1024;   // heads' statistics held at a time
 
 // grid (ceil(max_len / 256), B), block 256: thread = row; 1024 heads at a time.
+// Runs beside the value up-projection (see launch_pdl): it reads what the
+// merge and the split phase wrote, and the up-projection's CTAs have waited
+// for the merge before this kernel starts.
 __global__ void __launch_bounds__(kRwThreads)
 k_row_weights(const int32_t* __restrict__ sched, const float2* __restrict__ ml, const float* __restrict__ scores,
               float* __restrict__ w, int add, int B, int H, int max_len) {
-  dev::pdl_wait();   // see launch_pdl
-  dev::pdl_trigger();
   __shared__ float2 stat[kRwHeads];
   const int b = blockIdx.y;
   const long long t = (long long)blockIdx.x * kRwThreads + threadIdx.x;
   const int n = sched[B + 1 + b];
-  if (t - threadIdx.x >= n) return;   // uniform across the CTA
-  float acc = 0.f;
-  for (int h0 = 0; h0 < H; h0 += kRwHeads) {
-    const int nh = min(kRwHeads, H - h0);
-    if (h0) __syncthreads();   // every thread is done with the heads before
-    for (int h = threadIdx.x; h < nh; h += kRwThreads) stat[h] = __ldcg(ml + size_t(b) * H + h0 + h);
-    __syncthreads();
-    if (t >= n) continue;
-    const float* sc = scores + (size_t(b) * H + h0) * max_len + t;
-    int h = 0;
-    for (; h + 16 <= nh; h += 16) {   // sixteen loads in flight, added in head order
-      float v[16];
+  if (t - threadIdx.x < n) {   // uniform across the CTA
+    float acc = 0.f;
+    for (int h0 = 0; h0 < H; h0 += kRwHeads) {
+      const int nh = min(kRwHeads, H - h0);
+      if (h0) __syncthreads();   // every thread is done with the heads before
+      for (int h = threadIdx.x; h < nh; h += kRwThreads) stat[h] = __ldcg(ml + size_t(b) * H + h0 + h);
+      __syncthreads();
+      if (t >= n) continue;
+      const float* sc = scores + (size_t(b) * H + h0) * max_len + t;
+      int h = 0;
+      for (; h + 16 <= nh; h += 16) {   // sixteen loads in flight, added in head order
+        float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __ldcg(sc + size_t(h + i) * max_len);
+        for (int i = 0; i < 16; ++i) v[i] = __ldcg(sc + size_t(h + i) * max_len);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc = fmaf(exp2f(v[i] - stat[h + i].x), stat[h + i].y, acc);
+        for (int i = 0; i < 16; ++i) acc = fmaf(exp2f(v[i] - stat[h + i].x), stat[h + i].y, acc);
+      }
+      for (; h < nh; ++h) acc = fmaf(exp2f(__ldcg(sc + size_t(h) * max_len) - stat[h].x), stat[h].y, acc);
     }
-    for (; h < nh; ++h) acc = fmaf(exp2f(__ldcg(sc + size_t(h) * max_len) - stat[h].x), stat[h].y, acc);
+    if (t < n) {
+      float* o = w + size_t(b) * max_len + t;
+      *o = add ? *o + acc : acc;
+    }
   }
-  if (t >= n) return;
-  float* o = w + size_t(b) * max_len + t;
-  *o = add ? *o + acc : acc;
+  dev::pdl_wait();
+  dev::pdl_trigger();
 }
 
 }  // namespace

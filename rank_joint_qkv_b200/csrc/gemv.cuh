@@ -181,8 +181,26 @@ constexpr int CT = 64;                       // columns per CTA: 8 n-tiles of 8
 constexpr int TSTRIDE = CT * 2;              // tile row: 128 bytes, TMA 128-byte swizzle
 constexpr int TBOX = 256;                    // rows per TMA box (box dims are at most 256)
 constexpr int XSTRIDE = RT * 2 + 16;         // activation row pitch in bytes (padded: ldmatrix rows hit distinct banks)
+// Behind the weight tile: the activations of 16 sequences, then (they are
+// read by then) the four warps' partial tiles and their sum.
 template <int NPART>
-__host__ __device__ constexpr int smem_bytes() { return 1024 + RT * TSTRIDE + NPART * 16 * XSTRIDE; }
+__host__ __device__ constexpr int smem_bytes() {
+  const int xs = NPART * 16 * XSTRIDE, red = 5 * 16 * CT * 4;
+  return 1024 + RT * TSTRIDE + (xs > red ? xs : red);
+}
+constexpr int kMaxClusterK = 8;              // CTAs along K that reduce over distributed shared memory
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t local, int rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
 
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -224,23 +242,33 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 }  // namespace gemv_mma
 
-// grid (ceil(N/64), KS = ceil(K/512), ceil(B/16)), block 128.  Writes partials
-// part[ks][b][n]; with `ticket` non-null the last CTA of each (column block,
-// sequence block) adds the KS partials in split order into `out` (converted
-// to OT).  Activation row of sequence b for output column n:
+// grid (ceil(N/64), KS = ceil(K/512), z), block 128: a CTA keeps its weight
+// tile and walks the blocks of 16 sequences z apart (64 sequences: one fetch
+// of the tile instead of four).  The KS partials of an output are added in
+// split order and converted to OT by one of three ways:
+//   CLUSTER  KS <= 8: the KS CTAs of a column block are a cluster, each adds a
+//            share of the block over distributed shared memory (KS = 1: writes
+//            its own) -- no partials in global memory, no ticket
+//   TICKET   more: partials part[ks][b][n], and the last CTA of each (column
+//            block, sequence block) to take a ticket adds them
+//   PARTIAL  the partials are the result (the caller adds them)
+// Activation row of sequence b for output column n:
 // x + b * xg.row + (n / xg.cols) * xg.step (xg.cols a multiple of 64); the
 // plain GEMV has row = K, step = 0.
+// late: the kernel runs beside its predecessor in the stream and waits for it
+// at its end (see launch_pdl; CLUSTER only).
+enum { GEMV_CLUSTER, GEMV_TICKET, GEMV_PARTIAL };
 struct XGroups {
   long long row;    // elements between sequences
   int cols;         // output columns sharing one activation row
   long long step;   // elements between consecutive column groups' rows
 };
-template <typename XT, typename WT, typename OT = float>
+template <typename XT, typename WT, typename OT, int MODE>
 __global__ void __launch_bounds__(128)
 k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, XGroups xg,
            float* __restrict__ part, int B, int K, int N, int KS, OT* __restrict__ out,
            int32_t* __restrict__ ticket, int32_t* status, const uint8_t* __restrict__ pf,
-           unsigned long long pf_bytes) {
+           unsigned long long pf_bytes, int late) {
   using namespace gemv_mma;
   constexpr bool BF16 = std::is_same<WT, __nv_bfloat16>::value;
   constexpr bool SPLIT = !std::is_same<XT, WT>::value;   // activation wider than the weights
@@ -256,7 +284,6 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   __shared__ int last_cta;
   const int col0 = blockIdx.x * CT, ncols = min(CT, N - col0);
   const int ks = blockIdx.y, row0 = ks * RT, rows = min(RT, K - row0);
-  const int b0 = blockIdx.z * 16, bn = min(16, B - b0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // weight tile: two TMA boxes of 256 rows x 64 columns (zeros outside the
@@ -280,9 +307,14 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   // the next kernel's weights towards L2 (constant: no need to wait for anything)
   if (pf_bytes && tid == 32) dev::l2_prefetch_share(pf, pf_bytes);
   // the weight tile is in flight; everything below reads what earlier kernels wrote
-  dev::pdl_wait();   // see launch_pdl
-  dev::pdl_trigger();
+  if (!late) {
+    dev::pdl_wait();   // see launch_pdl
+    dev::pdl_trigger();
+  }
 
+  bool waited = false, ok = true;
+  for (int b0 = 16 * int(blockIdx.z); b0 < B; b0 += 16 * int(gridDim.z)) {
+  const int bn = min(16, B - b0);
   // activation slice, row k of sequence j at xs[j][k]; thread tid covers
   // k = 4 tid .. 4 tid + 3 of every sequence with one vector load each, all
   // 16 issued before any is used (rows is a multiple of 32)
@@ -337,17 +369,18 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
     if (SPLIT) *reinterpret_cast<uint2*>(xs + (16 + j) * XSTRIDE + 8 * tid) = *reinterpret_cast<const uint2*>(lo);
     if (tid == 0) inv_scale[j] = inv;
   }
-  // wait for the tile (bounded: 2 s); on expiry flag it and skip the work
-  __syncthreads();   // the barrier is initialised before anyone polls it
-  bool ok = mbar_try(bar_s, 0);
-  if (!ok) {
-    const uint64_t t0 = gtimer();
-    while (!(ok = mbar_try(bar_s, 0)))
-      if (gtimer() - t0 > 2000000000ull) break;
-  }
-  if (!__syncthreads_and(ok)) {
-    if (tid == 0 && status) atomicOr(status, QSVD_STATUS_TIMEOUT);
-    return;
+  // wait for the tile (bounded: 2 s); on expiry flag it and leave the products out
+  __syncthreads();   // the barrier is initialised before anyone polls it; the activations are staged
+  if (!waited) {
+    ok = mbar_try(bar_s, 0);
+    if (!ok) {
+      const uint64_t t0 = gtimer();
+      while (!(ok = mbar_try(bar_s, 0)))
+        if (gtimer() - t0 > 2000000000ull) break;
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok && tid == 0 && status) atomicOr(status, QSVD_STATUS_TIMEOUT);
+    waited = true;
   }
 
   // warp w: k-steps w, w + 4, ... over all 8 n-tiles
@@ -358,7 +391,7 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   const int mrow = (lane & 7) + 8 * ((lane >> 3) & 1);   // ldmatrix: this lane's row of its 8x8 matrix
   const int mcol = 8 * (lane >> 4);
 #pragma unroll 2
-  for (int kk = warp; kk < RT / 16; kk += 4) {
+  for (int kk = ok ? warp : RT; kk < RT / 16; kk += 4) {
     uint32_t a[NPART][4];
 #pragma unroll
     for (int p = 0; p < NPART; ++p)
@@ -375,10 +408,10 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
       }
     }
   }
-  // the four warps' partial tiles, summed in shared memory (over the tile,
-  // no longer needed); fragment: (row g, cols 2t, 2t+1) and (row g + 8)
+  // the four warps' partial tiles, summed in shared memory (over the
+  // activations, no longer needed); fragment: (row g, cols 2t, 2t+1) and (row g + 8)
   __syncthreads();
-  float* red = reinterpret_cast<float*>(tile);   // [4][16][CT]
+  float* red = reinterpret_cast<float*>(xs);   // [4][16][CT], then their sum [16][CT]
   {
     const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
@@ -396,50 +429,90 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
     o[e] = (red[i] + red[16 * CT + i] + red[32 * CT + i] + red[48 * CT + i]) * inv_scale[ob];
   }
   const bool live = ob < bn && oc < ncols;   // ncols is a multiple of 32
-  float* prow = part + (size_t(ks) * B + b0 + ob) * N + col0 + oc;
-  if (live) {
-    reinterpret_cast<float4*>(prow)[0] = make_float4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<float4*>(prow)[1] = make_float4(o[4], o[5], o[6], o[7]);
-  }
-  if (ticket == nullptr) return;
-  __threadfence();
-  __syncthreads();
-  int32_t* tk = ticket + blockIdx.z * gridDim.x + blockIdx.x;
-  if (tid == 0) last_cta = (atomicAdd(tk, 1) == KS - 1);
-  __syncthreads();
-  if (!last_cta) return;
-  __threadfence();
-  if (live) {
-    // partials added in split order; all splits' loads are in flight together
-    const float* pp = part + size_t(b0 + ob) * N + col0 + oc;
-    float sum[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-    for (int k = 0; k < KS; k += 4) {
-      float4 v[4][2];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const bool ok = k + u < KS;
-        const float4* src = reinterpret_cast<const float4*>(pp + size_t(k + u) * B * N);
-        v[u][0] = ok ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[u][1] = ok ? __ldcg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sum[0] += v[u][0].x; sum[1] += v[u][0].y; sum[2] += v[u][0].z; sum[3] += v[u][0].w;
-        sum[4] += v[u][1].x; sum[5] += v[u][1].y; sum[6] += v[u][1].z; sum[7] += v[u][1].w;
-      }
-    }
-    OT* orow = out + size_t(b0 + ob) * N + col0 + oc;
+  auto store4 = [&](OT* dst, float4 v) {
     if constexpr (std::is_same<OT, float>::value) {
-      reinterpret_cast<float4*>(orow)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      reinterpret_cast<float4*>(orow)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      *reinterpret_cast<float4*>(dst) = v;
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) orow[e] = dev::from_f<OT>(sum[e]);
+      dst[0] = dev::from_f<OT>(v.x); dst[1] = dev::from_f<OT>(v.y);
+      dst[2] = dev::from_f<OT>(v.z); dst[3] = dev::from_f<OT>(v.w);
     }
+  };
+  if constexpr (MODE == GEMV_CLUSTER) {
+    if (KS == 1) {
+      if (live) {
+        OT* orow = out + size_t(b0 + ob) * N + col0 + oc;
+        store4(orow, make_float4(0.f + o[0], 0.f + o[1], 0.f + o[2], 0.f + o[3]));
+        store4(orow + 4, make_float4(0.f + o[4], 0.f + o[5], 0.f + o[6], 0.f + o[7]));
+      }
+      __syncthreads();   // red is read before the next block's activations overwrite it
+    } else {
+      float* sum = red + 4 * 16 * CT;
+      reinterpret_cast<float4*>(sum + ob * CT + oc)[0] = make_float4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<float4*>(sum + ob * CT + oc)[1] = make_float4(o[4], o[5], o[6], o[7]);
+      cluster_sync();
+      // this CTA's share of the block's 256 quads, the splits' loads together and added in split order
+      for (int qd = ks * 128 + tid; qd < 16 * CT / 4; qd += KS * 128) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(sum + 4 * qd));
+        float4 v[kMaxClusterK];
+#pragma unroll
+        for (int k = 0; k < kMaxClusterK; ++k) v[k] = k < KS ? ld_peer(at, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMaxClusterK; ++k) { t.x += v[k].x; t.y += v[k].y; t.z += v[k].z; t.w += v[k].w; }
+        const int qb = qd / (CT / 4), qc = 4 * (qd % (CT / 4));
+        if (qb < bn && qc < ncols) store4(out + size_t(b0 + qb) * N + col0 + qc, t);
+      }
+      cluster_sync();   // every share is read before a sum is overwritten, or its CTA leaves
+    }
+  } else {
+    float* prow = part + (size_t(ks) * B + b0 + ob) * N + col0 + oc;
+    if (live) {
+      reinterpret_cast<float4*>(prow)[0] = make_float4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<float4*>(prow)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+    if constexpr (MODE == GEMV_TICKET) {
+      __threadfence();
+      __syncthreads();
+      int32_t* tk = ticket + (b0 / 16) * gridDim.x + blockIdx.x;
+      if (tid == 0) last_cta = (atomicAdd(tk, 1) == KS - 1);
+      __syncthreads();
+      if (last_cta) {
+        __threadfence();
+        if (live) {
+          // partials added in split order; all splits' loads are in flight together
+          const float* pp = part + size_t(b0 + ob) * N + col0 + oc;
+          float sum[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+          for (int k = 0; k < KS; k += 4) {
+            float4 v[4][2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool in = k + u < KS;
+              const float4* src = reinterpret_cast<const float4*>(pp + size_t(k + u) * B * N);
+              v[u][0] = in ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[u][1] = in ? __ldcg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              sum[0] += v[u][0].x; sum[1] += v[u][0].y; sum[2] += v[u][0].z; sum[3] += v[u][0].w;
+              sum[4] += v[u][1].x; sum[5] += v[u][1].y; sum[6] += v[u][1].z; sum[7] += v[u][1].w;
+            }
+          }
+          OT* orow = out + size_t(b0 + ob) * N + col0 + oc;
+          store4(orow, make_float4(sum[0], sum[1], sum[2], sum[3]));
+          store4(orow + 4, make_float4(sum[4], sum[5], sum[6], sum[7]));
+        }
+        if (tid == 0) *tk = 0;   // ready for the next call
+      }
+    }
+    __syncthreads();   // red is read before the next block's activations overwrite it
   }
-  if (tid == 0) *tk = 0;   // ready for the next call
+  }   // blocks of 16 sequences
+  if (late) {
+    dev::pdl_wait();
+    dev::pdl_trigger();
+  }
 }
 
 // Launch the GEMV: tensor cores for 16-bit weights, CUDA cores for fp32.
@@ -450,11 +523,11 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
 template <typename XT, typename WT, typename OT = float>
 cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int N, int KS,
                         OT* out, int32_t* ticket, int32_t* status, cudaStream_t s,
-                        XGroups xg = XGroups{0, 0, 0}, const void* pf = nullptr, size_t pf_bytes = 0) {
+                        XGroups xg = XGroups{0, 0, 0}, const void* pf = nullptr, size_t pf_bytes = 0,
+                        bool late = false) {
   if (xg.cols == 0) xg = XGroups{K, N, 0};
   cudaError_t e;
   if constexpr (sizeof(WT) == 2) {
-    const dim3 grid((N + gemv_mma::CT - 1) / gemv_mma::CT, KS, (B + 15) / 16);
     constexpr int NPART = std::is_same<XT, WT>::value ? 1 : 2;
     TensorMapEncode enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
@@ -469,18 +542,37 @@ cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-    auto kern = k_gemv_mma<XT, WT, OT>;
+    const bool cluster = ticket != nullptr && KS <= gemv_mma::kMaxClusterK;
+    auto kern = cluster ? k_gemv_mma<XT, WT, OT, GEMV_CLUSTER>
+                        : ticket ? k_gemv_mma<XT, WT, OT, GEMV_TICKET> : k_gemv_mma<XT, WT, OT, GEMV_PARTIAL>;
     const int smem = gemv_mma::smem_bytes<NPART>();
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
-    {
-      const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(128), smem, s, tm, x, xg, part, B, K, N, KS,
-                                       out, ticket, status, static_cast<const uint8_t*>(pf),
-                                       (unsigned long long)pf_bytes);
-      if (le != cudaSuccess) return le;
-    }
+    // blocks of 16 sequences side by side while the CTAs still fit at once (two
+    // per SM); beyond that a CTA walks several with its weight tile in place
+    const int cols = (N + gemv_mma::CT - 1) / gemv_mma::CT, blocks = (B + 15) / 16;
+    int z = 296 / (cols * KS);
+    z = z < 1 ? 1 : z > blocks ? blocks : z;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(unsigned(cols), unsigned(KS), unsigned(z));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = unsigned(KS);
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster && KS > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tm, x, xg, part, B, K, N, KS, out, ticket, status,
+                           static_cast<const uint8_t*>(pf), (unsigned long long)pf_bytes, int(late && cluster));
+    if (e != cudaSuccess) return e;
   } else {
     static_assert(std::is_same<OT, float>::value, "CUDA-core GEMV writes fp32");
     if (xg.step != 0 || xg.row != K) return cudaErrorInvalidValue;

@@ -374,11 +374,6 @@ __device__ __forceinline__ void l2_prefetch_share(const uint8_t* p, unsigned lon
 }
 
 
-// [p, p + bytes) requested into L2, both multiples of 16: a hint.
-__device__ __forceinline__ void l2_prefetch(const uint8_t* p, unsigned bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // See launch_pdl.  A no-op when the kernel was launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {

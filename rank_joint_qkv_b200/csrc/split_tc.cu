@@ -688,8 +688,7 @@ template <int NP, bool BF16, int QS, int PS, int QB, bool SG, bool KEEP>
 __global__ void __launch_bounds__(split_threads<NP, QB>(), 1)
 k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CUtensorMap tm_cz,
            const __grid_constant__ CUtensorMap tm_q,
-           const uint8_t* __restrict__ cache, const __half* __restrict__ scales,
-           float* __restrict__ scores, const int32_t* __restrict__ sched,
+           const __half* __restrict__ scales, float* __restrict__ scores, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
            int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int ns, int nz,
            int nsg, int nraw, int ch, const float* __restrict__ qsh) {
@@ -762,16 +761,6 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
     // ----------------------------------------------------------- producers
     bool ok = true;
     long long issued = 0, raw_issued = 0;
-    if (warp == 2 && lane == 0) {
-      // the first tile's rows towards L2 at once (a hint): a CTA with a single
-      // tile would else meet HBM's latency once per turn of the S ring
-      TileIter it0;
-      it0.init(sched, B, tb, te);
-      const unsigned long long rb = (unsigned long long)r * (QB ? QB : 16) / 8;
-      const uint8_t* p0 = cache + (size_t(it0.b) * max_len + it0.t0()) * rb;
-      for (unsigned long long at = 0, end = it0.nvalid() * rb; at < end; at += 16384)
-        dev::l2_prefetch(p0 + at, unsigned(end - at < 16384 ? end - at : 16384));
-    }
     if constexpr (QB != 0) {
       // quantised latent.  S: warp 0 loads int8 codes by TMA; int4 raw codes
       // are unpacked by warps 0 and 9.  Z: warp 2 issues the raw codes and
@@ -895,9 +884,12 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
     __syncwarp();
   } else if (warp == 3 || (SG && warp == 1)) {
     // ----------------------------------------------------------- Z MMAs
-    // Lane 0 waits and issues; the others walk the items along with it and
-    // help where a ragged last tile's rows are zeroed.  An expired wait ends
-    // lane 0's work, not the walk (the lanes meet in the warp's shuffles).
+    // Lane 0 waits and issues.  The other lanes join it where a ragged last
+    // tile's rows are zeroed: groups of 16 tokens without an attended one are
+    // left out there, and the rest of the last group becomes zeros (a NaN or
+    // Inf stored past the length would leak through P = 0; the quantised path's
+    // rows are dequantised to zeros already).  An expired wait ends lane 0's
+    // work, not the walk over the tiles: the lanes meet in the shuffles.
     {
       const int kind = warp >> 1;   // SG: ring and chunk parity of this issuer
       const bool ra = SG && kind == 0;
@@ -912,41 +904,49 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
       Ring rg(ra ? ns : nz);
       int sbi = 0;   // quantised latent: scale table of the tile
       bool ok = true;
-      for (int i = 0; i < n; ++i) {
+      // the MMAs of one item: nk groups of 16 tokens (K = 16 per MMA)
+      auto issue = [&](int u, uint64_t pb, bool first, int nk) {
+        const int j = u >> 1, h = u & 1;   // 128-channel chunk, 64-token half
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(ZC0 + (SG ? j / ch : j) * NP);
+        const uint64_t za = za0 + uint64_t((rg.slot * kZSlotBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk >= nk) break;
+          const uint64_t a = za + uint64_t((kk * 16 * 128) >> 4);
+#pragma unroll
+          for (int part = 0; part < PS; ++part) {   // P = P_hi (+ P_lo for bf16)
+            const uint64_t bd = pb + uint64_t((part * pbuf_bytes<NP>() + h * NP * 128 + kk * 32) >> 4);
+            tc_mma(d, a, bd, id_z, (first && h == 0 && kk == 0 && part == 0) ? 0u : 1u);
+          }
+        }
+        tc_commit(saddr(&zempty[rg.slot]));
+      };
+      for (int i = 0; i < n && (!QB || (lane == 0 && ok)); ++i) {
         const bool first = it.first(tb);
         const int nv = it.nvalid();
-        if (lane == 0 && ok) ok = mbar_wait(saddr(&s.p_full[i & 1]), uint32_t(i >> 1) & 1u);
         const uint64_t pb = pb0 + uint64_t(((i & 1) * PS * pbuf_bytes<NP>()) >> 4);
-        for (int u = 0; u < NI; ++u) {
-          const int j = u >> 1, h = u & 1;   // 128-channel chunk, 64-token half
-          if (SG && !sg_owns(j, ch, cpart, kind)) continue;
-          if (lane == 0 && ok) ok = mbar_wait(saddr(&zfull[rg.slot]), rg.phase);
-          // a ragged last tile: groups of 16 tokens without an attended one are
-          // left out, and the rest of the last group becomes zeros (a NaN or
-          // Inf stored past the length would leak through P = 0).  The
-          // quantised path's rows are dequantised to zeros already.
-          const int nk = QB ? 4 : min(4, max(0, (nv - 64 * h + 15) >> 4));
-          if (!QB && nk > 0 && nv - 64 * h < 16 * nk) {
-            if (__shfl_sync(0xffffffffu, int(ok), 0))
-              zero_z_rows(zring + uint32_t(rg.slot * kZSlotBytes), nv - 64 * h, 16 * nk, lane);
-          }
-          if (lane == 0 && ok) {
-            tc_fence_after();
-            const uint32_t d = tmem + uint32_t(ZC0 + (SG ? j / ch : j) * NP);
-            const uint64_t za = za0 + uint64_t((rg.slot * kZSlotBytes) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {   // K = 16 tokens per MMA
-              if (!QB && kk >= nk) break;
-              const uint64_t a = za + uint64_t((kk * 16 * 128) >> 4);
-#pragma unroll
-              for (int part = 0; part < PS; ++part) {   // P = P_hi (+ P_lo for bf16)
-                const uint64_t bd = pb + uint64_t((part * pbuf_bytes<NP>() + h * NP * 128 + kk * 32) >> 4);
-                tc_mma(d, a, bd, id_z, (first && h == 0 && kk == 0 && part == 0) ? 0u : 1u);
-              }
+        if (lane == 0 && ok) ok = mbar_wait(saddr(&s.p_full[i & 1]), uint32_t(i >> 1) & 1u);
+        if (QB || nv == kTile) {
+          if (lane == 0 && ok)
+            for (int u = 0; u < NI; ++u) {
+              if (SG && !sg_owns(u >> 1, ch, cpart, kind)) continue;
+              if (!mbar_wait(saddr(&zfull[rg.slot]), rg.phase)) { ok = false; break; }
+              issue(u, pb, first, 4);
+              rg.advance();
             }
-            tc_commit(saddr(&zempty[rg.slot]));
+        } else {
+          // the other lanes' ring positions: lane 0's
+          rg.slot = __shfl_sync(0xffffffffu, rg.slot, 0);
+          for (int u = 0; u < NI; ++u) {
+            if (SG && !sg_owns(u >> 1, ch, cpart, kind)) continue;
+            if (lane == 0 && ok) ok = mbar_wait(saddr(&zfull[rg.slot]), rg.phase);
+            const int left = nv - 64 * (u & 1), nk = min(4, max(0, (left + 15) >> 4));
+            if (nk > 0 && left < 16 * nk && __shfl_sync(0xffffffffu, int(ok), 0))
+              zero_z_rows(zring + uint32_t(rg.slot * kZSlotBytes), left, 16 * nk, lane);
+            if (lane == 0 && ok) issue(u, pb, first, nk);
+            rg.advance();
           }
-          rg.advance();
         }
         if (lane == 0 && ok) {
           tc_commit(saddr(&s.z_done[i & 1]));
@@ -1280,8 +1280,12 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
   const long long T = sched[B];
   // this CTA's run of (tile, head pair) units [ub, ue): tiles [tb, te), the
   // first and last of them perhaps with some of their pairs
-  const long long ub = dev::split_begin(blockIdx.x, G, T * NPAIR);
-  const long long ue = dev::split_begin(blockIdx.x + 1, G, T * NPAIR);
+  // (from four tiles a CTA on whole tiles: CTAs at the same pair at the same
+  // time share W^u_k's boxes in L2; 1024 tiles of 16 pairs on 148 SMs took
+  // 1.53 ms so, 1.60 ms in even runs)
+  const long long unit = T >= 4LL * G ? NPAIR : 1;
+  const long long ub = dev::split_begin(blockIdx.x, G, T * (NPAIR / unit)) * unit;
+  const long long ue = dev::split_begin(blockIdx.x + 1, G, T * (NPAIR / unit)) * unit;
   if (ub >= ue) return;   // uniform across the CTA, before any barrier or TMEM use
   const long long tb = dev::quotient(ub, NPAIR), te = dev::quotient(ue + NPAIR - 1, NPAIR);
   const int n = int(te - tb);
@@ -1598,7 +1602,7 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   if (e != cudaSuccess) return e;
   {
     const cudaError_t le = launch_pdl(kern, dim3(G * ch), dim3(split_threads<NP, QB>()), smem, s,
-                                     tcs, tcz, tq, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
+                                     tcs, tcz, tq, static_cast<const __half*>(scales), scores, sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, ns, nz, nsg, nraw, ch, qsh);
     if (le != cudaSuccess) return le;
   }
   note_launch();

@@ -312,6 +312,18 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
     dev::pdl_trigger();
   }
 
+  using Raw = typename std::conditional<sizeof(XT) == 4, float4, uint2>::type;
+  const bool kin = 4 * tid < rows;
+  // The loads are unconditional (a clamped, valid address) and masked after,
+  // so that nothing stands between them.
+  Raw raw[16];
+  auto load_block = [&](int b0) {
+    const XT* xrow = x + size_t(b0) * xg.row + size_t(col0 / xg.cols) * xg.step + row0 + (kin ? 4 * tid : 0);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      raw[j] = __ldg(reinterpret_cast<const Raw*>(xrow + size_t(b0 + j < B ? j : 0) * xg.row));
+  };
+  load_block(16 * int(blockIdx.z));
   bool waited = false, ok = true;
   for (int b0 = 16 * int(blockIdx.z); b0 < B; b0 += 16 * int(gridDim.z)) {
   const int bn = min(16, B - b0);
@@ -319,15 +331,6 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   // k = 4 tid .. 4 tid + 3 of every sequence with one vector load each, all
   // 16 issued before any is used (rows is a multiple of 32)
   static_assert(RT == 4 * 128, "four activation rows per thread");
-  // The loads are unconditional (a clamped, valid address) and masked after,
-  // so that nothing stands between them.
-  using Raw = typename std::conditional<sizeof(XT) == 4, float4, uint2>::type;
-  const bool kin = 4 * tid < rows;
-  const XT* xrow = x + size_t(b0) * xg.row + size_t(col0 / xg.cols) * xg.step + row0 + (kin ? 4 * tid : 0);
-  Raw raw[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    raw[j] = __ldg(reinterpret_cast<const Raw*>(xrow + size_t(j < bn ? j : 0) * xg.row));
   float xv[16][4];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -369,6 +372,7 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
     if (SPLIT) *reinterpret_cast<uint2*>(xs + (16 + j) * XSTRIDE + 8 * tid) = *reinterpret_cast<const uint2*>(lo);
     if (tid == 0) inv_scale[j] = inv;
   }
+  if (b0 + 16 * int(gridDim.z) < B) load_block(b0 + 16 * int(gridDim.z));   // the next block's, under this one's products
   // wait for the tile (bounded: 2 s); on expiry flag it and leave the products out
   __syncthreads();   // the barrier is initialised before anyone polls it; the activations are staged
   if (!waited) {

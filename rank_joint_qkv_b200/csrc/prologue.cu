@@ -162,21 +162,27 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
   const int mcol = 8 * (lane >> 4);
   const uint32_t xs_s = static_cast<uint32_t>(__cvta_generic_to_shared(xs));
   bool waited = false;
-  for (int b0 = 0; b0 < B; b0 += 16) {
-    const int bn = min(16, B - b0);
-    // q slice of head h: thread tid holds dd = tid + 128 u of every sequence
-    float xv[16][2];
+  // q slice of head h, 16 sequences: thread tid holds dd = tid + 128 u of each
+  // (clamped: the loads stay unconditional)
+  float xv[16][2];
+  auto load_block = [&](int b0) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int dd = tid + 128 * u;
-      const int ddc = dd < d_h ? dd : 0;   // clamped: the loads stay unconditional
+      const int ddc = dd < d_h ? dd : 0;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        xv[j][u] = __ldg(q + size_t(b0 + (j < bn ? j : 0)) * E + h * d_h + ddc);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (!(j < bn && dd < d_h)) xv[j][u] = 0.f;
+        xv[j][u] = __ldg(q + size_t(b0 + (b0 + j < B ? j : 0)) * E + h * d_h + ddc);
     }
+  };
+  load_block(0);
+  for (int b0 = 0; b0 < B; b0 += 16) {
+    const int bn = min(16, B - b0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (!(j < bn && tid + 128 * u < d_h)) xv[j][u] = 0.f;
     if (SCALE) {
       if (tid < 16) smax[tid] = 0u;
       float m[16];
@@ -210,6 +216,7 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
       }
       if (tid == 0) inv_scale[j] = inv;
     }
+    if (b0 + 16 < B) load_block(b0 + 16);   // the next block's, under this one's products
     if (!waited) {   // the W^u_k tile (bounded wait: 2 s; on expiry flag it and stop)
       bool ok = mbar_try(bar_s, 0);
       if (!ok) {

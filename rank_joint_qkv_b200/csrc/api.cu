@@ -449,10 +449,11 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     if (x.on && ((px && !X.fast) || !combine_uses_gemv(d)) &&
         (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
       return cuda_fail(e, "prefix schedule");
+    const bool third = x.weights != nullptr;   // see launch_absorb
     // q = c_new W^u_q (reduced into the workspace), or the query as given
     const float* qsrc = qin;
     if (qin_is_latent) {
-      if ((e = launch_q_partial(d, qin, P + L.wuq, qpart, W.KS, q, tickets, &hdr->status, s)) != cudaSuccess)
+      if ((e = launch_q_partial(d, qin, P + L.wuq, qpart, W.KS, q, tickets, &hdr->status, s, third)) != cudaSuccess)
         return cuda_fail(e, "query projection");
       qsrc = q;
     }
@@ -468,7 +469,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       const bool codes = kernel != QSVD_KERNEL_SIMT && cache_is_int(d);
       const bool need32 = kernel == QSVD_KERNEL_SIMT || codes || (px && !X.fast);
       void* parts = (kernel != QSVD_KERNEL_SIMT && !codes) || (px && X.fast) ? (px && cache_is_int(d) ? px16 : qt16) : nullptr;
-      e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s);
+      e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s, third);
       if (e == cudaSuccess && codes)
         e = launch_quant_query(d, qt32, static_cast<int8_t*>(qt16), quant_query_scales(d, qt16), s);
     }

@@ -12,7 +12,7 @@
 //                   the rows above it and the first of those equal.  Latency
 //                   is its bound: 4 n bytes per sequence in a chain of
 //                   dependent steps.  So a sequence gets a cluster of CTAs,
-//                   one per 8192 rows up to eight, whose threads hold their
+//                   one per 4096 rows up to eight, whose threads hold their
 //                   keys in registers across the steps and add up the
 //                   histograms over distributed shared memory.
 //   k_evict_move    the rows' bytes, scales and weights: bound by HBM, each
@@ -393,9 +393,9 @@ cudaError_t launch_evict(const qsvd_dims& d, const float* weights, const int32_t
                          int recent, const void* cache, const void* scales, int dst_max_len, void* dst_cache,
                          void* dst_scales, float* dst_weights, int32_t* dst_lengths, int32_t* kept, int32_t* src,
                          int32_t* new_len, int32_t* status, cudaStream_t s) {
-  // one CTA per 8192 rows of the longest sequence, a power of two up to eight
+  // one CTA per 4096 rows of the longest sequence, a power of two up to eight
   int CS = 1;
-  while (CS < kMaxCluster && (long long)CS * kSelChunk < d.max_len) CS *= 2;
+  while (CS < kMaxCluster && (long long)CS * (kSelChunk / 2) < d.max_len) CS *= 2;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(unsigned(d.batch) * unsigned(CS));

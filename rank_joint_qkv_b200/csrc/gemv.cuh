@@ -255,6 +255,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // Activation row of sequence b for output column n:
 // x + b * xg.row + (n / xg.cols) * xg.step (xg.cols a multiple of 64); the
 // plain GEMV has row = K, step = 0.
+// THIRD (bf16 weights): the residual of the activation's two parts as a third
+// one, staged and multiplied after them -- two bf16 parts carry 16 bits of an
+// activation, which float32 attention weights would show; three carry 24.
 // late: the kernel runs beside its predecessor in the stream and waits for it
 // at its end (see launch_pdl; CLUSTER only).
 enum { GEMV_CLUSTER, GEMV_TICKET, GEMV_PARTIAL };
@@ -263,7 +266,7 @@ struct XGroups {
   int cols;         // output columns sharing one activation row
   long long step;   // elements between consecutive column groups' rows
 };
-template <typename XT, typename WT, typename OT, int MODE>
+template <typename XT, typename WT, typename OT, int MODE, bool THIRD>
 __global__ void __launch_bounds__(128)
 k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, XGroups xg,
            float* __restrict__ part, int B, int K, int N, int KS, OT* __restrict__ out,
@@ -331,6 +334,7 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   // k = 4 tid .. 4 tid + 3 of every sequence with one vector load each, all
   // 16 issued before any is used (rows is a multiple of 32)
   static_assert(RT == 4 * 128, "four activation rows per thread");
+  uint2 third[THIRD ? 16 : 1];
   float xv[16][4];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -361,13 +365,15 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
         inv = __uint_as_float(unsigned(113 + e) << 23);
       }
     }
-    WT hi[4], lo[4];
+    WT hi[4], lo[4], rest[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float v = xv[j][e] * s;
       hi[e] = dev::from_f<WT>(v);
       lo[e] = dev::from_f<WT>(v - dev::to_f(hi[e]));
+      if (THIRD) rest[e] = dev::from_f<WT>(v - dev::to_f(hi[e]) - dev::to_f(lo[e]));
     }
+    if (THIRD) third[j] = *reinterpret_cast<const uint2*>(rest);
     *reinterpret_cast<uint2*>(xs + j * XSTRIDE + 8 * tid) = *reinterpret_cast<const uint2*>(hi);
     if (SPLIT) *reinterpret_cast<uint2*>(xs + (16 + j) * XSTRIDE + 8 * tid) = *reinterpret_cast<const uint2*>(lo);
     if (tid == 0) inv_scale[j] = inv;
@@ -394,23 +400,34 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   const uint32_t xs_s = static_cast<uint32_t>(__cvta_generic_to_shared(xs));
   const int mrow = (lane & 7) + 8 * ((lane >> 3) & 1);   // ldmatrix: this lane's row of its 8x8 matrix
   const int mcol = 8 * (lane >> 4);
+  auto products = [&](int parts) {
 #pragma unroll 2
-  for (int kk = ok ? warp : RT; kk < RT / 16; kk += 4) {
-    uint32_t a[NPART][4];
+    for (int kk = ok ? warp : RT; kk < RT / 16; kk += 4) {
+      uint32_t a[NPART][4];
 #pragma unroll
-    for (int p = 0; p < NPART; ++p)
-      ldsm_x4(xs_s + (p * 16 + mrow) * XSTRIDE + (16 * kk + mcol) * 2, a[p]);
+      for (int p = 0; p < NPART; ++p)
+        if (p < parts) ldsm_x4(xs_s + (p * 16 + mrow) * XSTRIDE + (16 * kk + mcol) * 2, a[p]);
 #pragma unroll
-    for (int jp = 0; jp < 4; ++jp) {
-      uint32_t bfr[4];   // k rows 16 kk + (0..7 | 8..15), n-tiles 2 jp and 2 jp + 1
-      const int row = 16 * kk + mrow, chunk = 2 * jp + (lane >> 4);   // 16-byte chunk of the row
-      ldsm_x4_t(tile_s + row * TSTRIDE + ((chunk ^ (row & 7)) << 4), bfr);
+      for (int jp = 0; jp < 4; ++jp) {
+        uint32_t bfr[4];   // k rows 16 kk + (0..7 | 8..15), n-tiles 2 jp and 2 jp + 1
+        const int row = 16 * kk + mrow, chunk = 2 * jp + (lane >> 4);   // 16-byte chunk of the row
+        ldsm_x4_t(tile_s + row * TSTRIDE + ((chunk ^ (row & 7)) << 4), bfr);
 #pragma unroll
-      for (int p = 0; p < NPART; ++p) {
-        mma16816<BF16>(acc[2 * jp], a[p], bfr[0], bfr[1]);
-        mma16816<BF16>(acc[2 * jp + 1], a[p], bfr[2], bfr[3]);
+        for (int p = 0; p < NPART; ++p)
+          if (p < parts) {
+            mma16816<BF16>(acc[2 * jp], a[p], bfr[0], bfr[1]);
+            mma16816<BF16>(acc[2 * jp + 1], a[p], bfr[2], bfr[3]);
+          }
       }
     }
+  };
+  products(NPART);
+  if constexpr (THIRD) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint2*>(xs + j * XSTRIDE + 8 * tid) = third[j];
+    __syncthreads();
+    products(1);
   }
   // the four warps' partial tiles, summed in shared memory (over the
   // activations, no longer needed); fragment: (row g, cols 2t, 2t+1) and (row g + 8)
@@ -523,12 +540,12 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
 // Per-group activation rows (xg) and a non-float output need the tensor-core
 // variant (16-bit weights).  pf / pf_bytes: constant bytes the next kernel
 // reads (its weights), requested into L2 while this one runs (tensor-core
-// variant; a hint only).
+// variant; a hint only).  third: see k_gemv_mma (bf16 weights, fp32 output).
 template <typename XT, typename WT, typename OT = float>
 cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int N, int KS,
                         OT* out, int32_t* ticket, int32_t* status, cudaStream_t s,
                         XGroups xg = XGroups{0, 0, 0}, const void* pf = nullptr, size_t pf_bytes = 0,
-                        bool late = false) {
+                        bool late = false, bool third = false) {
   if (xg.cols == 0) xg = XGroups{K, N, 0};
   cudaError_t e;
   if constexpr (sizeof(WT) == 2) {
@@ -547,8 +564,10 @@ cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
     const bool cluster = ticket != nullptr && KS <= gemv_mma::kMaxClusterK;
-    auto kern = cluster ? k_gemv_mma<XT, WT, OT, GEMV_CLUSTER>
-                        : ticket ? k_gemv_mma<XT, WT, OT, GEMV_TICKET> : k_gemv_mma<XT, WT, OT, GEMV_PARTIAL>;
+    auto kern = cluster ? k_gemv_mma<XT, WT, OT, GEMV_CLUSTER, false>
+                        : ticket ? k_gemv_mma<XT, WT, OT, GEMV_TICKET, false> : k_gemv_mma<XT, WT, OT, GEMV_PARTIAL, false>;
+    if constexpr (std::is_same<WT, __nv_bfloat16>::value && std::is_same<XT, float>::value && std::is_same<OT, float>::value)
+      if (third && ticket) kern = cluster ? k_gemv_mma<XT, WT, OT, GEMV_CLUSTER, true> : k_gemv_mma<XT, WT, OT, GEMV_TICKET, true>;
     const int smem = gemv_mma::smem_bytes<NPART>();
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)

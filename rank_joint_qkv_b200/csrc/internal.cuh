@@ -207,11 +207,13 @@ cudaError_t launch_schedule(const qsvd_dims& d, const int32_t* lengths, int G, i
                             cudaStream_t s);
 cudaError_t launch_q_partial(const qsvd_dims& d, const float* qin, const void* wuq,
                              float* qpart, int KS, float* q, int32_t* tickets, int32_t* status,
-                             cudaStream_t s);
+                             cudaStream_t s, bool third = false);
+// third: bf16 weights take a third part of the activations (k_gemv_mma,
+// k_absorb_mma), for float32 attention weights.
 // qt32 (fp32, for the CUDA-core split) and qt16 ([B][2][H][r] hi/lo, for the
 // tensor cores) are each written only when non-null.
 cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, float scale_log2,
-                          float* qt32, void* qt16, int32_t* status, cudaStream_t s);
+                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third = false);
 // Quantised latent on the tensor cores: qt32 [B][H][r] -> three int8 parts
 // qp [B][3][H][r] and one power-of-two scale qs [B][H] per (sequence, head).
 cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s);

@@ -32,8 +32,8 @@
 // a pass of both products, so that the scores are as good as the integer ones
 // of the sequences' own rows.
 //
-// Roles (192 threads per CTA): warp 0 TMA producer, warp 1 TMEM and the MMA thread,
-// warps 2-5 epilogue; two TMEM accumulators of 256 columns, so the epilogue
+// Roles (320 threads per CTA): warp 0 TMA producer, warp 1 TMEM and the MMA thread,
+// warps 2-9 epilogue; two TMEM accumulators of 256 columns, so the epilogue
 // of a unit runs under the next one's products.  Every wait is bounded.
 #include <cuda.h>
 
@@ -46,11 +46,12 @@
 namespace qsvd {
 namespace {
 
-constexpr int kPxThreads = 192;
+constexpr int kPxThreads = 320;
+constexpr int kPxEpi = 256;                // epilogue threads: two warps per 32 TMEM lanes, half of the columns each
 constexpr int kPxA = 128 * 128;            // A box: 128 rows x 64 K x 2 bytes
 constexpr int kPxB = 256 * 128;            // B: 256 N x 64 K x 2 bytes
 constexpr int kPxMaxSlots = 6;
-constexpr int kPxStage = 32 * 128;         // epilogue staging: 32 rows x 128 bytes, two per warp
+constexpr int kPxStage = 32 * 128;         // epilogue staging per warp: 32 rows x 128 bytes
 constexpr float kRefStep = 15.f;           // log2 units between references
 constexpr int kPxSmem = 232448;            // opt-in dynamic shared memory per block on sm_100
 
@@ -100,7 +101,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* stage0 = base + size_t(ns) * kSlot;              // [4 warps][2][32 rows][128 bytes]
+  uint8_t* stage0 = base + size_t(ns) * kSlot;              // [8 warps][32 rows][128 bytes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage0 + 8 * kPxStage);
   uint64_t* full = bars;                    // [kPxMaxSlots]
   uint64_t* empty = bars + kPxMaxSlots;     // [kPxMaxSlots]
@@ -280,36 +281,49 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   } else {
     // ------------------------------------------------------------ epilogue
     using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const int t = 32 * q + lane;   // query row of the block == TMEM lane
+    const int c_lo = 128 * half;   // this warp's columns [c_lo, c_lo + 128)
     const uint32_t lane_off = uint32_t(32 * q) << 16;
     const size_t rows = size_t(g.MB) * 128;
     // A lane holds a row's values; stored as they are, 16 bytes a lane, a store
     // instruction would touch 32 rows.  So the warp turns 32 rows x 128 bytes
     // around in shared memory (16-byte chunks, swizzled by row) and stores
     // four whole lines an instruction.
-    const uint32_t st0 = saddr(stage0) + uint32_t(q) * (2 * kPxStage);
-    auto put = [&](int buf, int c, uint4 v) {   // chunk c of this lane's row
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st0 + buf * kPxStage + lane * 128 + ((c ^ (lane & 7)) << 4)),
+    const uint32_t st0 = saddr(stage0) + uint32_t(warp - 2) * kPxStage;
+    const uint32_t mate0 = saddr(stage0) + uint32_t((warp - 2) ^ 4) * kPxStage;   // the same rows, the other columns
+    auto put = [&](int c, uint4 v) {   // chunk c of this lane's row
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st0 + lane * 128 + ((c ^ (lane & 7)) << 4)),
                    "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     };
-    auto flush = [&](int buf, uint8_t* row0, size_t pitch, int live_rows) {   // the warp's 32 rows from row0 on
+    auto flush = [&](uint8_t* row0, size_t pitch, int live_rows) {   // the warp's 32 rows from row0 on
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int rr = 4 * i + (lane >> 3), c = lane & 7;
         uint4 v;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(st0 + buf * kPxStage + rr * 128 + ((c ^ (rr & 7)) << 4)) : "memory");
+                     : "r"(st0 + rr * 128 + ((c ^ (rr & 7)) << 4)) : "memory");
         if (32 * q + rr < live_rows) *reinterpret_cast<uint4*>(row0 + size_t(rr) * pitch + c * 16) = v;
       }
+      __syncwarp();
+    };
+    // this row's value in the other warp, through the two staging buffers (not in use)
+    auto exchange = [&](float mine) {
+      float other;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(st0 + lane * 4), "f"(mine) : "memory");
+      bar_sync(1, kPxEpi);
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(mate0 + lane * 4) : "memory");
+      bar_sync(1, kPxEpi);
+      return other;
     };
     for (int j = 0; j < mine; ++j) {
       int mb, n, sp, k0, k1;
       unit(j, &mb, &n, &sp, &k0, &k1);
       const int ab = j & 1;
-      const int fail = group_or(!mbar_wait(saddr(&afull[ab]), uint32_t(j >> 1) & 1u));
+      const int fail = bar_or(!mbar_wait(saddr(&afull[ab]), uint32_t(j >> 1) & 1u), 1, kPxEpi);
       if (fail) {
-        if (t == 0) { *abort_flag = 1; atomicOr(g.status, QSVD_STATUS_TIMEOUT); }
+        if (t == 0 && half == 0) { *abort_flag = 1; atomicOr(g.status, QSVD_STATUS_TIMEOUT); }
         break;
       }
       tc_fence_after();
@@ -319,30 +333,24 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         // rows mb nb H + t of the split's [B H][r]
         uint8_t* z = reinterpret_cast<uint8_t*>(g.pz + ((size_t(sp) * g.B + size_t(mb) * g.nb) * g.H + 32 * q) * g.r +
                                                 size_t(n) * 256);
-        const int nc = min(256, g.r - n * 256);   // a multiple of 64
+        const int nc = min(c_lo + 128, g.r - n * 256);   // a multiple of 64
 #pragma unroll 1
-        for (int c = 0; c < nc; c += 64) {
-          float v[64];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld16(ta + uint32_t(c + 16 * i), v + 16 * i);
+        for (int c = c_lo; c < nc; c += 32) {
+          float v[32];
+          tmem_ld16(ta + uint32_t(c), v);
+          tmem_ld16(ta + uint32_t(c + 16), v + 16);
           tmem_wait_ld();
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float* x = v + 32 * half + 4 * e;
-              put(half, e, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
-            }
-          __syncwarp();
-          flush(0, z + c * 4, size_t(g.r) * 4, live_rows);
-          flush(1, z + c * 4 + 128, size_t(g.r) * 4, live_rows);
-          __syncwarp();
+          for (int e = 0; e < 8; ++e)
+            put(e, make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]),
+                              __float_as_uint(v[4 * e + 3])));
+          flush(z + c * 4, size_t(g.r) * 4, live_rows);
         }
       } else {
         const int nv = min(kPxTile, g.plen - n * kPxTile);   // tokens of the tile, >= 1
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < kPxTile; c += 32) {
+        for (int c = c_lo; c < c_lo + 128; c += 32) {
           float v[32];
           tmem_ld16(ta + uint32_t(c), v);
           tmem_ld16(ta + uint32_t(c + 16), v + 16);
@@ -350,36 +358,43 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 32; ++e) mx = c + e < nv ? fmaxf(mx, v[e]) : mx;
         }
+        mx = fmaxf(mx, exchange(mx));
         const float ref = kRefStep * floorf(mx * g.gain / kRefStep);
         float sum = 0.f;
         uint8_t* prow = reinterpret_cast<uint8_t*>(static_cast<T16*>(g.p) + (size_t(mb) * 128 + 32 * q) * g.ppad + size_t(n) * kPxTile);
 #pragma unroll 1
-        for (int c = 0; c < kPxTile; c += 64) {
-          float v[64];
+        for (int c = c_lo; c < c_lo + 128; c += 64) {
+          uint4 lo[PS == 2 ? 8 : 1];   // the lo parts, staged after the hi parts are stored
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld16(ta + uint32_t(c + 16 * i), v + 16 * i);
-          tmem_wait_ld();
+          for (int e32 = 0; e32 < 2; ++e32) {
+            float v[32];
+            tmem_ld16(ta + uint32_t(c + 32 * e32), v);
+            tmem_ld16(ta + uint32_t(c + 32 * e32 + 16), v + 16);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e8 = 0; e8 < 8; ++e8) {
-            uint4 hi, lo;
-            T16* hv = reinterpret_cast<T16*>(&hi);
-            T16* lv = reinterpret_cast<T16*>(&lo);
+            for (int e8 = 0; e8 < 4; ++e8) {
+              uint4 hi;
+              T16* hv = reinterpret_cast<T16*>(&hi);
+              T16* lv = reinterpret_cast<T16*>(&lo[PS == 2 ? 4 * e32 + e8 : 0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = c + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], g.gain, -ref)) : 0.f;
-              sum += p;
-              hv[e] = dev::from_f<T16>(p);
-              if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
+              for (int e = 0; e < 8; ++e) {
+                const float p = c + 32 * e32 + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], g.gain, -ref)) : 0.f;
+                sum += p;
+                hv[e] = dev::from_f<T16>(p);
+                if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
+              }
+              put(4 * e32 + e8, hi);
             }
-            put(0, e8, hi);
-            if (PS == 2) put(1, e8, lo);
           }
-          __syncwarp();
-          flush(0, prow + c * 2, size_t(g.ppad) * 2, live_rows);
-          if (PS == 2) flush(1, prow + rows * g.ppad * 2 + c * 2, size_t(g.ppad) * 2, live_rows);
-          __syncwarp();
+          flush(prow + c * 2, size_t(g.ppad) * 2, live_rows);
+          if (PS == 2) {
+#pragma unroll
+            for (int e8 = 0; e8 < 8; ++e8) put(e8, lo[PS == 2 ? e8 : 0]);
+            flush(prow + rows * g.ppad * 2 + c * 2, size_t(g.ppad) * 2, live_rows);
+          }
         }
-        if (t < live_rows) {
+        sum += exchange(sum);   // the same two terms in both warps
+        if (half == 0 && t < live_rows) {
           const bool own = g.tiles == g.SP;
           const size_t at = own ? (size_t(n) * g.B + size_t(mb) * g.nb) * g.H + t : size_t(n) * rows + size_t(mb) * 128 + t;
           (own ? g.pm : g.mt)[at] = ref;
@@ -387,12 +402,12 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
       }
       tc_fence_before();
-      group_sync();
-      if (t == 0) {
+      bar_sync(1, kPxEpi);
+      if (t == 0 && half == 0) {
         if (PAIR) pair_arrive(pair_leader(saddr(&aempty[ab])));
         else mbar_arrive(saddr(&aempty[ab]));
       }
-      if (group_or(*abort_flag)) break;
+      if (bar_or(*abort_flag, 1, kPxEpi)) break;
     }
   }
   if (!VALUES) {

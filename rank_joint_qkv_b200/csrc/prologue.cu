@@ -120,9 +120,11 @@ k_absorb(const float* __restrict__ q, const WT* __restrict__ W, float scale,
 // into 128-byte-swizzled rows whose d_h values are K-contiguous (ldmatrix
 // gives the B fragments directly), q enters as a 16-bit part plus its
 // rounding residual, with fp16 weights scaled per sequence by a power of two.
+// THIRD (bf16 weights): what two bf16 parts leave of q as a third one, staged
+// and multiplied after them (see k_gemv_mma).
 // grid (H, ceil(r / 128)), block 128.
 // ---------------------------------------------------------------------------
-template <typename WT, typename QT16>
+template <typename WT, typename QT16, bool THIRD>
 __global__ void __launch_bounds__(128)
 k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__ q, float scale,
              float* __restrict__ qt32, QT16* __restrict__ qt16, int B, int H, int d_h, int r, int E,
@@ -183,6 +185,7 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (!(j < bn && tid + 128 * u < d_h)) xv[j][u] = 0.f;
+    WT third[THIRD ? 16 : 1][2];
     if (SCALE) {
       if (tid < 16) smax[tid] = 0u;
       float m[16];
@@ -209,9 +212,10 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
         const int dd = tid + 128 * u;
         if (dd < d_h) {
           const float v = xv[j][u] * s;
-          const WT hi = dev::from_f<WT>(v);
+          const WT hi = dev::from_f<WT>(v), lo = dev::from_f<WT>(v - dev::to_f(hi));
           reinterpret_cast<WT*>(xs + j * XP)[dd] = hi;
-          reinterpret_cast<WT*>(xs + (16 + j) * XP)[dd] = dev::from_f<WT>(v - dev::to_f(hi));
+          reinterpret_cast<WT*>(xs + (16 + j) * XP)[dd] = lo;
+          if (THIRD) third[j][u] = dev::from_f<WT>(v - dev::to_f(hi) - dev::to_f(lo));
         }
       }
       if (tid == 0) inv_scale[j] = inv;
@@ -236,23 +240,38 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
     float acc[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-    for (int kk = 0; kk < d_h / 16; ++kk) {
-      uint32_t a[2][4];
+    auto products = [&](int parts) {
+      for (int kk = 0; kk < d_h / 16; ++kk) {
+        uint32_t a[2][4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) ldsm_x4(xs_s + (p * 16 + mrow) * XP + (16 * kk + mcol) * 2, a[p]);
-      const int dd = 16 * kk + 8 * ((lane >> 3) & 1);
-      const int c = dd >> 6, chunk = (dd & 63) >> 3;
+        for (int p = 0; p < 2; ++p)
+          if (p < parts) ldsm_x4(xs_s + (p * 16 + mrow) * XP + (16 * kk + mcol) * 2, a[p]);
+        const int dd = 16 * kk + 8 * ((lane >> 3) & 1);
+        const int c = dd >> 6, chunk = (dd & 63) >> 3;
 #pragma unroll
-      for (int jp = 0; jp < 2; ++jp) {
-        const int j = 32 * warp + 8 * (2 * jp + (lane >> 4)) + (lane & 7);
-        uint32_t bfr[4];   // n-tile 2 jp: k lo, k hi; n-tile 2 jp + 1: k lo, k hi
-        ldsm_x4(tile_s + c * 16384 + j * 128 + ((chunk ^ (j & 7)) << 4), bfr);
+        for (int jp = 0; jp < 2; ++jp) {
+          const int j = 32 * warp + 8 * (2 * jp + (lane >> 4)) + (lane & 7);
+          uint32_t bfr[4];   // n-tile 2 jp: k lo, k hi; n-tile 2 jp + 1: k lo, k hi
+          ldsm_x4(tile_s + c * 16384 + j * 128 + ((chunk ^ (j & 7)) << 4), bfr);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          mma16816<BF16>(acc[2 * jp], a[p], bfr[0], bfr[1]);
-          mma16816<BF16>(acc[2 * jp + 1], a[p], bfr[2], bfr[3]);
+          for (int p = 0; p < 2; ++p)
+            if (p < parts) {
+              mma16816<BF16>(acc[2 * jp], a[p], bfr[0], bfr[1]);
+              mma16816<BF16>(acc[2 * jp + 1], a[p], bfr[2], bfr[3]);
+            }
         }
       }
+    };
+    products(2);
+    if constexpr (THIRD) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (tid + 128 * u < d_h) reinterpret_cast<WT*>(xs + j * XP)[tid + 128 * u] = third[j][u];
+      __syncthreads();
+      products(1);
     }
     // fragment: (row g = sequence, cols 2t, 2t+1 = rows j) and (row g + 8)
     const int g = lane >> 2, t4 = lane & 3;
@@ -414,15 +433,15 @@ k_schedule(const int32_t* __restrict__ lengths, int B, int max_len, int G,
 
 template <typename WT>
 cudaError_t q_partial_t(const qsvd_dims& d, const float* qin, const void* wuq, float* qpart,
-                        int KS, float* q, int32_t* tickets, int32_t* status, cudaStream_t s) {
+                        int KS, float* q, int32_t* tickets, int32_t* status, bool third, cudaStream_t s) {
   // beside the schedule before it, of which it needs nothing where it takes no tickets
   return launch_gemv<float, WT>(qin, static_cast<const WT*>(wuq), qpart, d.batch, d.r, d.E, KS, q,
-                                tickets, status, s, XGroups{0, 0, 0}, nullptr, 0, true);
+                                tickets, status, s, XGroups{0, 0, 0}, nullptr, 0, true, third);
 }
 
 template <typename WT, typename QT16>
 cudaError_t absorb_t(const qsvd_dims& d, const float* q, const void* wuk, float scale,
-                     float* qt32, void* qt16, int32_t* status, cudaStream_t s) {
+                     float* qt32, void* qt16, int32_t* status, bool third, cudaStream_t s) {
   if constexpr (sizeof(WT) == 2) {
     if (d.d_h % 64 == 0 && d.d_h <= 256) {
       TensorMapEncode enc = tensor_map_encoder();
@@ -439,7 +458,9 @@ cudaError_t absorb_t(const qsvd_dims& d, const float* q, const void* wuk, float 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
       const int smem = 1024 + d.d_h * 256 + 2 * 16 * (d.d_h * 2 + 16);
-      auto kern = k_absorb_mma<WT, QT16>;
+      auto kern = k_absorb_mma<WT, QT16, false>;
+      if constexpr (std::is_same<WT, __nv_bfloat16>::value)
+        if (third) kern = k_absorb_mma<WT, QT16, true>;
       cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       dim3 grid(d.H, (d.r + 127) / 128);
@@ -487,28 +508,28 @@ cudaError_t launch_schedule(const qsvd_dims& d, const int32_t* lengths, int G, i
 
 cudaError_t launch_q_partial(const qsvd_dims& d, const float* qin, const void* wuq,
                              float* qpart, int KS, float* q, int32_t* tickets, int32_t* status,
-                             cudaStream_t s) {
+                             cudaStream_t s, bool third) {
   switch (d.weight_dtype) {
-    case QSVD_F32: return q_partial_t<float>(d, qin, wuq, qpart, KS, q, tickets, status, s);
-    case QSVD_F16: return q_partial_t<__half>(d, qin, wuq, qpart, KS, q, tickets, status, s);
-    case QSVD_BF16: return q_partial_t<__nv_bfloat16>(d, qin, wuq, qpart, KS, q, tickets, status, s);
+    case QSVD_F32: return q_partial_t<float>(d, qin, wuq, qpart, KS, q, tickets, status, third, s);
+    case QSVD_F16: return q_partial_t<__half>(d, qin, wuq, qpart, KS, q, tickets, status, third, s);
+    case QSVD_BF16: return q_partial_t<__nv_bfloat16>(d, qin, wuq, qpart, KS, q, tickets, status, third, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, float scale,
-                          float* qt32, void* qt16, int32_t* status, cudaStream_t s) {
+                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third) {
   const bool bf = d.cache_dtype == QSVD_BF16;
   switch (d.weight_dtype) {
     case QSVD_F32:
-      return bf ? absorb_t<float, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, s)
-                : absorb_t<float, __half>(d, q, wuk, scale, qt32, qt16, status, s);
+      return bf ? absorb_t<float, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
+                : absorb_t<float, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
     case QSVD_F16:
-      return bf ? absorb_t<__half, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, s)
-                : absorb_t<__half, __half>(d, q, wuk, scale, qt32, qt16, status, s);
+      return bf ? absorb_t<__half, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
+                : absorb_t<__half, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
     case QSVD_BF16:
-      return bf ? absorb_t<__nv_bfloat16, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, s)
-                : absorb_t<__nv_bfloat16, __half>(d, q, wuk, scale, qt32, qt16, status, s);
+      return bf ? absorb_t<__nv_bfloat16, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
+                : absorb_t<__nv_bfloat16, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -84,7 +84,9 @@ def test_against_the_definition(cuda_ok, name):
     close_weights(w, want_w, 3 * bound, m.lens)
     for b, n in enumerate(m.lens):
         assert bool((w[b, n:] == 7.0).all())
-    assert torch.equal(run(m), out)   # weights are optional
+    # weights are optional; without them bf16 weights take the query in two parts instead of three (2^-16 of it)
+    again = run(m)
+    assert torch.equal(again, out) if m.weight != "bf16" else rel_err(again, out) <= 2e-3 + 8 * torch.finfo(out.dtype).eps
 
 
 @pytest.mark.parametrize("cache", ["f16", "bf16", "i8"])

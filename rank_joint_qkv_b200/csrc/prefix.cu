@@ -296,7 +296,8 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st0 + lane * 128 + ((c ^ (lane & 7)) << 4)),
                    "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     };
-    auto flush = [&](uint8_t* row0, size_t pitch, int live_rows) {   // the warp's 32 rows from row0 on
+    // the warp's 32 rows from row0 on; the rows' second halves `skip` bytes further
+    auto flush = [&](uint8_t* row0, size_t skip, size_t pitch, int live_rows) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -304,7 +305,8 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         uint4 v;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                      : "r"(st0 + rr * 128 + ((c ^ (rr & 7)) << 4)) : "memory");
-        if (32 * q + rr < live_rows) *reinterpret_cast<uint4*>(row0 + size_t(rr) * pitch + c * 16) = v;
+        if (32 * q + rr < live_rows)
+          *reinterpret_cast<uint4*>(row0 + size_t(rr) * pitch + c * 16 + (c >= 4 ? skip : 0)) = v;
       }
       __syncwarp();
     };
@@ -344,7 +346,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
           for (int e = 0; e < 8; ++e)
             put(e, make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]),
                               __float_as_uint(v[4 * e + 3])));
-          flush(z + c * 4, size_t(g.r) * 4, live_rows);
+          flush(z + c * 4, 0, size_t(g.r) * 4, live_rows);
         }
       } else {
         const int nv = min(kPxTile, g.plen - n * kPxTile);   // tokens of the tile, >= 1
@@ -362,20 +364,20 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         const float ref = kRefStep * floorf(mx * g.gain / kRefStep);
         float sum = 0.f;
         uint8_t* prow = reinterpret_cast<uint8_t*>(static_cast<T16*>(g.p) + (size_t(mb) * 128 + 32 * q) * g.ppad + size_t(n) * kPxTile);
+        constexpr int kStep = PS == 2 ? 32 : 64;   // tokens staged at a time: hi parts, and lo parts beside them
 #pragma unroll 1
-        for (int c = c_lo; c < c_lo + 128; c += 64) {
-          uint4 lo[PS == 2 ? 8 : 1];   // the lo parts, staged after the hi parts are stored
+        for (int c = c_lo; c < c_lo + 128; c += kStep) {
 #pragma unroll
-          for (int e32 = 0; e32 < 2; ++e32) {
+          for (int e32 = 0; e32 < kStep / 32; ++e32) {
             float v[32];
             tmem_ld16(ta + uint32_t(c + 32 * e32), v);
             tmem_ld16(ta + uint32_t(c + 32 * e32 + 16), v + 16);
             tmem_wait_ld();
 #pragma unroll
             for (int e8 = 0; e8 < 4; ++e8) {
-              uint4 hi;
+              uint4 hi, lo;
               T16* hv = reinterpret_cast<T16*>(&hi);
-              T16* lv = reinterpret_cast<T16*>(&lo[PS == 2 ? 4 * e32 + e8 : 0]);
+              T16* lv = reinterpret_cast<T16*>(&lo);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float p = c + 32 * e32 + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], g.gain, -ref)) : 0.f;
@@ -384,14 +386,11 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
               }
               put(4 * e32 + e8, hi);
+              if (PS == 2) put(4 + e8, lo);
             }
           }
-          flush(prow + c * 2, size_t(g.ppad) * 2, live_rows);
-          if (PS == 2) {
-#pragma unroll
-            for (int e8 = 0; e8 < 8; ++e8) put(e8, lo[PS == 2 ? e8 : 0]);
-            flush(prow + rows * g.ppad * 2 + c * 2, size_t(g.ppad) * 2, live_rows);
-          }
+          // chunks 4-7: the next 32 tokens, or (PS == 2) the lo parts
+          flush(prow + c * 2, PS == 2 ? rows * g.ppad * 2 - 64 : 0, size_t(g.ppad) * 2, live_rows);
         }
         sum += exchange(sum);   // the same two terms in both warps
         if (half == 0 && t < live_rows) {

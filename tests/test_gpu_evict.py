@@ -150,3 +150,50 @@ def test_graph_replay(cuda_ok):
             at = keep_rows(w2[b, :n], n, 100, 1, 20)
             assert kept[b, :len(at)].tolist() == at
             assert np.array_equal(dst[b, :len(at)].cpu().numpy(), rows[b, at])
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_caches_beyond_32_bit_offsets(cuda_ok, in_place):
+    """Two sequences of 800,000 rows of 3 KB: bytes past 2^32, rows compared with a gather by the kept indices."""
+    B, n, r, budget = 2, 800_000, 1536, 700_000
+    dims = q.make_dims(64, 1, 64, r, B, n, cache="f16")
+    rows = torch.arange(B * n, device=DEV, dtype=torch.int64)
+    cache = ((rows[:, None] * 7 + torch.arange(r, device=DEV)) % 2039).to(torch.float16).view(B, n, r)
+    w = torch.rand(B, n, device=DEV)
+    w0 = w.clone()
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    kept = torch.zeros(B, budget, dtype=torch.int32, device=DEV)
+    if in_place:
+        q.qsvd_evict_rows(dims, w, lens, budget, cache, sink=4, recent=1000, kept=kept)
+        got = cache
+    else:
+        got = torch.zeros(B, budget, r, dtype=torch.float16, device=DEV)
+        q.qsvd_evict_rows(dims, w, lens, budget, cache, sink=4, recent=1000, kept=kept, dst_max_len=budget, dst_cache=got,
+                          dst_lengths=torch.zeros_like(lens))
+    torch.cuda.synchronize()
+    for b in range(B):
+        key = w0[b].clone()
+        key[:4] = key[n - 1000:] = 2.0
+        want = torch.sort(key, descending=True, stable=True).indices[:budget].sort().values
+        assert torch.equal(kept[b].long(), want)
+        values = ((want[:, None] + b * n) * 7 + torch.arange(r, device=DEV)) % 2039
+        assert torch.equal(got[b, :budget], values.to(torch.float16))
+        del values
+
+
+def test_two_cuts_at_once(cuda_ok):
+    """Two batches cut in place on two streams."""
+    sets = []
+    for seed in (1, 2):
+        dims, rows, _, w = setup("f16", 256, 128, 3000, (3000, 2500, 100), seed)
+        sets.append((dims, rows, w, to_dev(rows), to_dev(w), torch.tensor([3000, 2500, 100], dtype=torch.int32, device=DEV),
+                     torch.empty(q.evict_workspace_bytes(dims, 900), dtype=torch.uint8, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for dims, _, _, d_rows, d_w, lens, ws, st in sets:
+        q.qsvd_evict_rows(dims, d_w, lens, 900, d_rows, sink=3, recent=64, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for _, rows, w, d_rows, _, lens, _, _ in sets:
+        assert lens.tolist() == [900, 900, 100]
+        for b, n in enumerate((3000, 2500, 100)):
+            at = keep_rows(w[b, :n], n, 900, 3, 64)
+            assert np.array_equal(d_rows[b, :len(at)].cpu().numpy(), rows[b, at])

@@ -32,6 +32,10 @@ CASES = {
     "i4": dict(cache="i4", prefix=500, lens=(1, 129), r=384),
     "i4-group": dict(cache="i4", prefix=130, lens=(40, 3), r=192, group=64),
     "mixed-weights": dict(cache="f16", weight="f32", prefix=400, lens=(20, 60)),
+    "f16-cluster": dict(prefix=300, lens=(0, 257, 40), H=8, r=512, kernel=q.QSVD_KERNEL_TCGEN05_CLUSTER),
+    "f16-pairs": dict(prefix=9300, lens=(3, 0, 130) * 6, H=32, r=128),   # 5 blocks of query rows in pairs, 37 tiles
+    "bf16-pairs": dict(cache="bf16", weight="bf16", out="bf16", prefix=10001, lens=(1,) * 16, H=32, r=192),
+    "i8-pairs": dict(cache="i8", prefix=9999, lens=(20,) * 16, H=32, r=256),
     # CUDA cores: fp32 rows, other ranks, by request, more heads than a block has rows
     "f32": dict(cache="f32", weight="f32", prefix=300, lens=(0, 140, 7), r=96),
     "f16-simt": dict(prefix=300, lens=(5, 0), kernel=S),
@@ -230,6 +234,36 @@ def test_empty_everything_gives_zero_rows(cuda_ok):
     assert bool((run(m) == 0).all())
     m = Layer(prefix=0, lens=(0, 3), H=8, d_h=24, r=64)
     assert bool((run(m)[0] == 0).all())
+
+
+def test_two_calls_at_once(cuda_ok):
+    """Two batches on two streams with workspaces of their own, over one prefix, many times over."""
+    a, b = (Layer(prefix=1200, lens=lens, H=8, r=256, seed=5) for lens in ((300, 0, 77), (10, 900, 128)))
+    b.prefix, b.prefix_values, b.packed = a.prefix, a.prefix_values, a.packed
+    b.wuq, b.wuk, b.wuv = a.wuq, a.wuk, a.wuv
+    want = [run(m) for m in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[m.empty_out() for _ in range(20)] for m in (a, b)]
+    wss = [torch.empty(q.decode_shared_workspace_bytes(m.dims, 1200), dtype=torch.uint8, device=DEV) for m in (a, b)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for m, st, o, ws in zip((a, b), streams, outs, wss):
+            q.qsvd_decode_attn_shared(m.dims, m.packed, m.qin, True, m.prefix, None, 1200, m.cache, None, m.lengths, o[i],
+                                      workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for x in o:
+            assert torch.equal(x, w)
+
+
+def test_the_query_as_given(cuda_ok):
+    """qin as the B x E query itself instead of the token's latent."""
+    m = Layer(prefix=300, lens=(20, 0, 129), H=8)
+    query = m.qin.double() @ m.wuq.double()
+    out = m.empty_out()
+    q.qsvd_decode_attn_shared(m.dims, m.packed, query.float().contiguous(), False, m.prefix, None, 300, m.cache, None,
+                              m.lengths, out)
+    close_out(m, out, m.exact()[0])
 
 
 def test_on_the_other_current_stream(cuda_ok):

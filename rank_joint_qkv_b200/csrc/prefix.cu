@@ -423,37 +423,50 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   }
 }
 
-// One warp per (query row, token split): m = the largest reference of the
-// split's tiles, l = their sums brought to it, and P of the tiles with a lower
-// one scaled to it.  grid (B H / 8 rounded up, SP), block 256.
+// Per (query row, token split): m = the largest reference of the split's
+// tiles, l = their sums brought to it, and P of the tiles with a lower one
+// scaled to it.  A CTA has 32 rows: lane = row for the statistics (whole lines
+// of them), which each of its eight warps takes for itself; the tiles to
+// rescale are shared out over the warps, one row of one at a time.
+// grid (MB 4, SP), block 256.
 template <typename T16, int PS>
 __global__ void __launch_bounds__(256)
 k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __restrict__ lt, float* __restrict__ pm,
               float* __restrict__ pl, int B, int H, int nb, int MB, int tiles, int ppad, int SP) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long bh = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (bh >= (long long)B * H) return;
-  const int b = int(bh / H), h = int(bh % H), sp = blockIdx.y;
-  const size_t rows = size_t(MB) * 128, row = size_t(b / nb) * 128 + size_t(b % nb) * H + h;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mb = int(blockIdx.x) >> 2, i0 = 32 * (int(blockIdx.x) & 3), sp = blockIdx.y;
+  const int live = min(nb, B - mb * nb) * H;   // rows of the block that are queries
+  if (i0 >= live) return;
+  const size_t rows = size_t(MB) * 128, row0 = size_t(mb) * 128 + i0;
+  const bool mine = i0 + lane < live;
+  const float* mr = mt + row0 + (mine ? lane : 0);
+  const float* lr = lt + row0 + (mine ? lane : 0);
   const int t0 = split_tile(sp, tiles, SP), t1 = split_tile(sp + 1, tiles, SP);
   float m = -INFINITY;
-  for (int t = t0 + lane; t < t1; t += 32) m = fmaxf(m, __ldcg(mt + size_t(t) * rows + row));
-  m = dev::warp_max(m);
-  float l = 0.f;
-  for (int tb = t0; tb < t1; tb += 32) {
-    const int t = tb + lane;
-    const float f = t < t1 ? exp2f(__ldcg(mt + size_t(t) * rows + row) - m) : 1.f;   // a power of two
-    if (t < t1) l += f * __ldcg(lt + size_t(t) * rows + row);
-    unsigned lower = __ballot_sync(0xffffffffu, f != 1.f);
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) m = fmaxf(m, __ldcg(mr + size_t(t) * rows));
+  if (warp == 0) {
+    float l = 0.f;
+#pragma unroll 8
+    for (int t = t0; t < t1; ++t) l = fmaf(exp2f(__ldcg(mr + size_t(t) * rows) - m), __ldcg(lr + size_t(t) * rows), l);
+    if (mine) {
+      const size_t at = (size_t(sp) * B + size_t(mb) * nb) * H + i0 + lane;
+      pm[at] = m;
+      pl[at] = l;
+    }
+  }
+  for (int t = t0 + warp; t < t1; t += 8) {
+    const float f = exp2f(__ldcg(mr + size_t(t) * rows) - m);   // a power of two
+    unsigned lower = __ballot_sync(0xffffffffu, mine && f != 1.f);
     while (lower) {
       const int i = __ffs(lower) - 1;
       lower &= lower - 1;
       const float fi = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll
       for (int part = 0; part < PS; ++part) {
-        uint4* v = reinterpret_cast<uint4*>(p + (part * rows + row) * ppad + size_t(tb + i) * kPxTile) + lane;
+        uint4* v = reinterpret_cast<uint4*>(p + (part * rows + row0 + i) * ppad + size_t(t) * kPxTile) + lane;
         uint4 x = __ldcg(v);
         T16* e = reinterpret_cast<T16*>(&x);
 #pragma unroll
@@ -461,11 +474,6 @@ k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __
         *v = x;
       }
     }
-  }
-  l = dev::warp_sum(l);
-  if (lane == 0) {
-    pm[(size_t(sp) * B + b) * H + h] = m;
-    pl[(size_t(sp) * B + b) * H + h] = l;
   }
 }
 
@@ -726,8 +734,7 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
   cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
   if (e != cudaSuccess) return e;
   if (L.tiles != L.SP) {
-    const long long bh = (long long)d.batch * d.H;
-    e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned((bh + 7) / 8), unsigned(L.SP)), dim3(256), 0, s,
+    e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned(4 * L.MB), unsigned(L.SP)), dim3(256), 0, s,
                    reinterpret_cast<T16*>(ws + L.p), g.mt, g.lt, g.pm, g.pl, d.batch, d.H, L.nb, L.MB, L.tiles, L.ppad,
                    L.SP);
     if (e != cudaSuccess) return e;

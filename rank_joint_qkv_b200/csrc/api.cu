@@ -510,7 +510,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     float* zm = reinterpret_cast<float*>(Wb + W.zm);
     const bool fold = d.out_proj == QSVD_OUT_PROJ_FOLD;
     const size_t wb = dtype_bytes(d.weight_dtype);
-    e = launch_merge_shared(d, X, Wb, hdr, sched, pm, pl, pz, zm, !gemv, fold ? P + L.wo : P + L.wuv,
+    e = launch_merge_shared(d, X, Wb, hdr, G, sched, pm, pl, pz, zm, !gemv, fold ? P + L.wo : P + L.wuv,
                             !gemv ? 0 : (fold ? out_proj_rows(d) : size_t(d.r)) * d.E * wb, s);
     if (e != cudaSuccess) return cuda_fail(e, "merge");
     if (gemv) {

@@ -543,6 +543,7 @@ struct MergeIn {
   const float *xm, *xl, *xz;   // prefix: slot sp B + b (n = SP), or slot c + b of schedule xsched, G xg
   const int32_t* xsched;
   int n, xg;
+  int most;                    // entries at most
 };
 
 __global__ void __launch_bounds__(128)
@@ -553,90 +554,97 @@ k_merge_shared(const WsHeader* __restrict__ hdr, const MergeIn in, float* __rest
   if (pf_bytes && threadIdx.x == 32) dev::l2_prefetch_share(pf, pf_bytes);
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
-  __shared__ float wt[2][kMaxSplits];
-  __shared__ int range[2][2];
+  // the partials that count, own splits first: where their z starts and their weight
+  extern __shared__ uint64_t merge_smem[];   // most entries: own splits G + the prefix's
+  const float** from = reinterpret_cast<const float**>(merge_smem);
+  float* wt = reinterpret_cast<float*>(merge_smem + in.most);
+  __shared__ int count;
   const int ch = blockIdx.x * 512 + 4 * threadIdx.x;
   const int h = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    const long long G = hdr->G, T = in.sched[B];
-    int c0[2] = {0, 0}, c1[2] = {-1, -1};
-    if (in.sched[b + 1] > in.sched[b]) {
-      c0[0] = int(dev::split_of_tile(in.sched[b], G, T));
-      c1[0] = int(dev::split_of_tile(in.sched[b + 1] - 1, G, T));
+    const int T = in.sched[B], t0 = in.sched[b], t1 = in.sched[b + 1], G = hdr->G;
+    const int XT = in.xsched ? in.xsched[B] : 0, x0 = in.xsched ? in.xsched[b] : 0, x1 = in.xsched ? in.xsched[b + 1] : 0;
+    int c0 = 0, n0 = 0, c1 = 0, n1 = in.n;   // first split and splits of the own rows, of the prefix
+    if (t1 > t0) {
+      c0 = int(dev::split_of_tile(t0, G, T));
+      n0 = int(dev::split_of_tile(t1 - 1, G, T)) - c0 + 1;
     }
-    const long long XG = in.xg, XT = in.xsched ? in.xsched[B] : 0;
     if (in.xsched) {
-      c0[1] = int(dev::split_of_tile(in.xsched[b], XG, XT));
-      c1[1] = int(dev::split_of_tile(in.xsched[b + 1] - 1, XG, XT));
-    } else {
-      c1[1] = in.n - 1;
+      c1 = int(dev::split_of_tile(x0, in.xg, XT));
+      n1 = int(dev::split_of_tile(x1 - 1, in.xg, XT)) - c1 + 1;
     }
-    // split c of source k: its place in the partials, or -1 when it is empty
-    auto place = [&](int k, int c) -> long long {
-      if (k == 0) return dev::split_begin(c, G, T) == dev::split_begin(c + 1, G, T) ? -1 : ((long long)c + b) * H + h;
-      if (!in.xsched) return ((long long)c * B + b) * H + h;
-      return dev::split_begin(c, XG, XT) == dev::split_begin(c + 1, XG, XT) ? -1 : ((long long)c + b) * H + h;
+    // entry e of the two lists: its slot, or -1 for an empty split
+    auto slot_of = [&](int e) -> long long {
+      if (e < n0) return dev::split_begin(c0 + e, G, T) == dev::split_begin(c0 + e + 1, G, T) ? -1 : (long long)(c0 + e) + b;
+      e -= n0;
+      if (!in.xsched) return (long long)e * B + b;
+      return dev::split_begin(c1 + e, in.xg, XT) == dev::split_begin(c1 + e + 1, in.xg, XT) ? -1 : (long long)(c1 + e) + b;
     };
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int c = c0[k] + lane; c <= c1[k]; c += 32) {
-        const long long at = place(k, c);
-        if (at >= 0) M = fmaxf(M, __ldcg((k ? in.xm : in.pm) + at));
-      }
+    const int n = n0 + n1;
+    // m and l of the first 32 entries in registers, loaded together; further ones (long runs of splits) again below
+    float m0 = -INFINITY, l0 = 0.f;
+    const long long s0 = lane < n ? slot_of(lane) : -1;
+    if (s0 >= 0) {
+      const size_t at = size_t(s0) * H + h;
+      m0 = __ldcg((lane < n0 ? in.pm : in.xm) + at);
+      l0 = __ldcg((lane < n0 ? in.pl : in.xl) + at);
+    }
+    float M = m0;
+    for (int e = lane + 32; e < n; e += 32) {
+      const long long s = slot_of(e);
+      if (s >= 0) M = fmaxf(M, __ldcg((e < n0 ? in.pm : in.xm) + size_t(s) * H + h));
+    }
     M = dev::warp_max(M);
-    float L = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int c = c0[k] + lane; c <= c1[k]; c += 32) {
-        const long long at = place(k, c);
-        float w = 0.f;
-        if (at >= 0) {
-          w = exp2f(__ldcg((k ? in.xm : in.pm) + at) - M);
-          L += w * __ldcg((k ? in.xl : in.pl) + at);
-        }
-        wt[k][c - c0[k]] = w;
-      }
+    const float w0 = s0 >= 0 ? exp2f(m0 - M) : 0.f;
+    float L = w0 * l0;
+    for (int e = lane + 32; e < n; e += 32) {
+      const long long s = slot_of(e);
+      if (s >= 0)
+        L += exp2f(__ldcg((e < n0 ? in.pm : in.xm) + size_t(s) * H + h) - M) *
+             __ldcg((e < n0 ? in.pl : in.xl) + size_t(s) * H + h);
+    }
     L = dev::warp_sum(L);
     const float invL = L > 0.f ? 1.f / L : 0.f;
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      for (int c = c0[k] + lane; c <= c1[k]; c += 32) wt[k][c - c0[k]] *= invL;
-      if (lane == 0) { range[k][0] = c0[k]; range[k][1] = c1[k]; }
+    int kept = 0;   // compacted in order: entries of weight 0 are left out
+    for (int e0 = 0; e0 < n; e0 += 32) {
+      const int e = e0 + lane;
+      const long long s = e0 == 0 ? s0 : e < n ? slot_of(e) : -1;
+      float w = 0.f;
+      if (s >= 0) w = (e0 == 0 ? w0 : exp2f(__ldcg((e < n0 ? in.pm : in.xm) + size_t(s) * H + h) - M)) * invL;
+      const unsigned on = __ballot_sync(0xffffffffu, w != 0.f);
+      if (w != 0.f) {
+        const int at = kept + __popc(on & ((1u << lane) - 1u));
+        from[at] = (e < n0 ? in.pz : in.xz) + (size_t(s) * H + h) * r;
+        wt[at] = w;
+      }
+      kept += __popc(on);
     }
-    if (lane == 0 && blockIdx.x == 0) {
-      ml[size_t(b) * H + h] = make_float2(M, invL);
-      if (cm) {   // one slot per sequence (2 b), merged already
-        cm[size_t(2 * b) * H + h] = 0.f;
-        cl[size_t(2 * b) * H + h] = 1.f;
+    if (lane == 0) {
+      count = kept;
+      if (blockIdx.x == 0) {
+        ml[size_t(b) * H + h] = make_float2(M, invL);
+        if (cm) {   // one slot per sequence (2 b), merged already
+          cm[size_t(2 * b) * H + h] = 0.f;
+          cl[size_t(2 * b) * H + h] = 1.f;
+        }
       }
     }
   }
   __syncthreads();
   if (ch >= r) return;
+  const int n = count;
   float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    const int c0 = range[k][0], c1 = range[k][1];
-    const bool rowwise = k == 1 && !in.xsched;
-    const float* base = (k ? in.xz : in.pz) + size_t(h) * r + ch;
-    for (int cb = c0; cb <= c1; cb += 8) {   // eight splits' loads in flight, added in split order
-      float4 v[8];
+  for (int e0 = 0; e0 < n; e0 += 8) {   // eight partials' loads in flight, added in order
+    float4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const size_t slot = rowwise ? size_t(cb + i) * B + b : size_t(cb + i) + b;
-        v[i] = cb + i <= c1 && wt[k][cb + i - c0] != 0.f
-                   ? __ldcg(reinterpret_cast<const float4*>(base + slot * H * r))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int i = 0; i < 8; ++i)
+      v[i] = e0 + i < n ? __ldcg(reinterpret_cast<const float4*>(from[e0 + i] + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = cb + i <= c1 ? wt[k][cb + i - c0] : 0.f;
-        z.x = fmaf(w, v[i].x, z.x); z.y = fmaf(w, v[i].y, z.y);
-        z.z = fmaf(w, v[i].z, z.z); z.w = fmaf(w, v[i].w, z.w);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float w = e0 + i < n ? wt[e0 + i] : 0.f;
+      z.x = fmaf(w, v[i].x, z.x); z.y = fmaf(w, v[i].y, z.y);
+      z.z = fmaf(w, v[i].z, z.z); z.w = fmaf(w, v[i].w, z.w);
     }
   }
   *reinterpret_cast<float4*>(zout + (size_t(cm ? 2 * b : b) * H + h) * r + ch) = z;
@@ -849,16 +857,17 @@ cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, ui
   return check_launch();
 }
 
-cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr,
+cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr, int G,
                                 const int32_t* sched, const float* pm, const float* pl, const float* pz, float* zm,
                                 bool slots, const void* next_weights, size_t next_bytes, cudaStream_t s) {
   const float* xm = reinterpret_cast<const float*>(ws + L.pm);
   const bool listed = L.plen > 0 && !L.fast;
+  const int most = G + (L.plen > 0 ? (L.fast ? L.SP : L.G) : 0);
   const MergeIn in{pm, pl, pz, sched, xm, reinterpret_cast<const float*>(ws + L.pl),
                    reinterpret_cast<const float*>(ws + L.pz),
-                   listed ? reinterpret_cast<const int32_t*>(ws + L.sched) : nullptr, L.plen > 0 ? L.SP : 0, L.G};
+                   listed ? reinterpret_cast<const int32_t*>(ws + L.sched) : nullptr, L.plen > 0 ? L.SP : 0, L.G, most};
   cudaError_t e = launch_pdl(k_merge_shared, dim3(unsigned((d.r + 511) / 512), unsigned(d.H), unsigned(d.batch)),
-                             dim3(128), 0, s, hdr, in, slots ? reinterpret_cast<float*>(ws + L.cz) : zm,
+                             dim3(128), size_t(most) * 12, s, hdr, in, slots ? reinterpret_cast<float*>(ws + L.cz) : zm,
                              slots ? reinterpret_cast<float*>(ws + L.cm) : nullptr,
                              slots ? reinterpret_cast<float*>(ws + L.cl) : nullptr, reinterpret_cast<float2*>(ws + L.ml),
                              d.batch, d.H, d.r, static_cast<const uint8_t*>(next_weights),

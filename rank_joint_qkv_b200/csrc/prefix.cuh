@@ -37,7 +37,7 @@ cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, ui
 int prefix_score_steps(const qsvd_dims& d);
 // Merge of the own splits' and the prefix's partials: zm [B][H][r], or (slots
 // != 0) one slot per sequence for launch_combine; ml {M, 1 / L} [B][H].
-cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr,
+cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr, int G,
                                 const int32_t* sched, const float* pm, const float* pl, const float* pz, float* zm,
                                 bool slots, const void* next_weights, size_t next_bytes, cudaStream_t s);
 

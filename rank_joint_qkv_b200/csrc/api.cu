@@ -444,7 +444,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
 
   if (phases & QSVD_PHASE_PROLOGUE) {
     int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets);
-    if ((e = launch_schedule(d, lengths, G, sched, hdr, kernel, tickets, W.NT, s)) != cudaSuccess)
+    if ((e = launch_schedule(d, lengths, G, sched, hdr, kernel, tickets, W.NT + 1, s)) != cudaSuccess)
       return cuda_fail(e, "schedule");
     if (x.on && ((px && !X.fast) || !combine_uses_gemv(d)) &&
         (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
@@ -501,7 +501,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     if (e != cudaSuccess) return cuda_fail(e, "split phase");
     if (px) {
       e = launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qt32,
-                        float(score_gain(prefix_score_steps(d)) / gain), sms, &hdr->status, s);
+                        float(score_gain(prefix_score_steps(d)) / gain), sms,
+                        reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);
       if (e != cudaSuccess) return cuda_fail(e, "prefix");
     }
   }

@@ -136,7 +136,7 @@ inline WsLayout ws_layout(const qsvd_dims& d, int G, bool keep_scores = false) {
   size_t o = 0;
   w.hdr = o;   o = align256(o + sizeof(WsHeader));
   w.sched = o; o = align256(o + (2 * B + 1) * 4);
-  w.tickets = o; o = align256(o + size_t(w.NT) * 4);
+  w.tickets = o; o = align256(o + size_t(w.NT + 1) * 4);   // and one counter (the shared prefix's score units)
   w.q = o;     o = align256(o + B * E * 4);
   w.qt32 = o;  o = align256(o + (H * r > E ? H * r : E) * B * 4);   // rotary mode: B x E query
   w.qt16 = o;  o = align256(o + 2 * B * H * r * 2);   // [B][2][H][r] for bf16 hi/lo

@@ -71,6 +71,7 @@ struct PxArgs {
   float* pl;      // split of its own (tiles == SP)
   float* pz;      // [SP B][H][r] (values: written)
   float gain;     // on the scores (see launch_prefix)
+  int32_t* counter;   // score units taken (single CTAs)
   int32_t* status;
 };
 
@@ -81,6 +82,10 @@ __device__ __forceinline__ int split_tile(int sp, int tiles, int SP) { return in
 // its shared memory and TMEM and half of the B tile (tcgen05 cta_group::2;
 // the first CTA issues): per 64 K of two A parts a CTA alone reads 64 KB from
 // L2, one of a pair 48 KB (one A part: 48 KB, and 32 KB).
+//
+// The scores of single CTAs are dealt out as CTAs become free (a counter): they
+// run beside the own rows' split kernel, whose CTAs hold their SMs for longer
+// than a unit takes, and a fixed share would wait behind them.
 //
 // AP: 16-bit parts of A in pass 0 (a second pass, for the lo part of an
 // expanded prefix, takes A's first part only).  CP: passes (parts of C).
@@ -98,6 +103,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   // is read here; this kernel's wait is at its end)
   constexpr int kSlot = px_slot<AP, PAIR>(), ns = px_slots<AP, PAIR>();
   constexpr int W = PAIR ? 2 : 1;            // CTAs, and row blocks, per unit
+  constexpr bool DYN = !VALUES && !PAIR;     // units by the counter
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -108,7 +114,10 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   uint64_t* afull = bars + 2 * kPxMaxSlots; // [2] accumulator complete
   uint64_t* aempty = afull + 2;             // [2] accumulator read by the epilogue
   uint64_t* drain = aempty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* uq_full = drain + 1;            // [4] DYN: a unit published by the producer ...
+  uint64_t* uq_empty = uq_full + 4;         // [4] ... and read by the MMA thread and the epilogue
+  volatile int* uq = reinterpret_cast<volatile int*>(uq_empty + 4);   // [4]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(uq_empty + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NB = VALUES ? (g.r + 255) / 256 : g.tiles;       // column blocks of the product
@@ -116,12 +125,11 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
   const int units = MU * NB * (VALUES ? g.SP : 1);
   const int walker = int(blockIdx.x) / W, walkers = int(gridDim.x) / W;
   const uint32_t rank = PAIR ? pair_rank() : 0u;
-  const int mine = units > walker ? (units - 1 - walker) / walkers + 1 : 0;
-  if (mine == 0) return;   // uniform across the CTA (and the pair); no launch has such CTAs
+  // units of this CTA (at most, when they are dealt out)
+  const int mine = DYN ? units : units > walker ? (units - 1 - walker) / walkers + 1 : 0;
   // unit u: row block(s) u % MU, so that the blocks in flight share their B
   // tiles in L2.  mb: this CTA's; the last pair's second may lie past MB (zeros)
-  auto unit = [&](int j, int* mb, int* n, int* sp, int* k0, int* k1) {
-    const int u = walker + j * walkers;
+  auto unit = [&](int u, int* mb, int* n, int* sp, int* k0, int* k1) {
     *mb = (u % MU) * W + int(rank);
     *n = (u / MU) % NB;
     *sp = (u / MU) / NB;
@@ -144,6 +152,10 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       mbar_init(saddr(&aempty[i]), W);
     }
     mbar_init(saddr(drain), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(saddr(&uq_full[i]), 1);
+      mbar_init(saddr(&uq_empty[i]), 2);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -171,8 +183,22 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     long long k = 0;
     bool ok = true;
     for (int j = 0; j < mine && ok; ++j) {
+      int u = walker + j * walkers;
+      if (DYN) {
+        if (j >= 4 && !__all_sync(0xffffffffu, mbar_wait(saddr(&uq_empty[j & 3]), uint32_t((j - 4) >> 2) & 1u))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          u = atomicAdd(g.counter, 1);
+          uq[j & 3] = u;
+          mbar_arrive(saddr(&uq_full[j & 3]));
+        }
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (u >= units) break;
+      }
       int mb, n, sp, k0, k1;
-      unit(j, &mb, &n, &sp, &k0, &k1);
+      unit(u, &mb, &n, &sp, &k0, &k1);
       for (int pass = 0; pass < CP && ok; ++pass) {
         const int parts = pass == 0 ? AP : 1;
         const uint32_t abytes = uint32_t(VALUES ? kPxA : g.nb * g.H * 128);
@@ -236,8 +262,15 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       Ring rg(ns);
       bool ok = true;
       for (int j = 0; j < mine && ok; ++j) {
+        int u = walker + j * walkers;
+        if (DYN) {
+          if (!mbar_wait(saddr(&uq_full[j & 3]), uint32_t(j >> 2) & 1u)) { ok = false; break; }
+          u = uq[j & 3];
+          mbar_arrive(saddr(&uq_empty[j & 3]));
+          if (u >= units) break;
+        }
         int mb, n, sp, k0, k1;
-        unit(j, &mb, &n, &sp, &k0, &k1);
+        unit(u, &mb, &n, &sp, &k0, &k1);
         const int ab = j & 1;
         if (j >= 2 && !mbar_wait(saddr(&aempty[ab]), uint32_t((j - 2) >> 1) & 1u)) { ok = false; break; }
         tc_fence_after();
@@ -320,8 +353,19 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
       return other;
     };
     for (int j = 0; j < mine; ++j) {
+      int u = walker + j * walkers;
+      bool ok = true;
+      if (DYN) {
+        ok = mbar_wait(saddr(&uq_full[j & 3]), uint32_t(j >> 2) & 1u);
+        u = ok ? uq[j & 3] : 0;
+      }
+      if (DYN && bar_or(!ok || u >= units, 1, kPxEpi)) {   // no unit is left (or the producer gave up)
+        if (!ok && t == 0 && half == 0) { *abort_flag = 1; atomicOr(g.status, QSVD_STATUS_TIMEOUT); }
+        break;
+      }
+      if (DYN && t == 0 && half == 0) mbar_arrive(saddr(&uq_empty[j & 3]));
       int mb, n, sp, k0, k1;
-      unit(j, &mb, &n, &sp, &k0, &k1);
+      unit(u, &mb, &n, &sp, &k0, &k1);
       const int ab = j & 1;
       const int fail = bar_or(!mbar_wait(saddr(&afull[ab]), uint32_t(j >> 1) & 1u), 1, kPxEpi);
       if (fail) {
@@ -671,7 +715,7 @@ cudaError_t gemm_p(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
   if (units > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int walkers = units < sms / W ? int(units) : sms / W;
   constexpr size_t smem = 1024 + size_t(px_slots<AP, PAIR>()) * px_slot<AP, PAIR>() + 8 * kPxStage +
-                          (2 * kPxMaxSlots + 5) * 8 + 16;
+                          (2 * kPxMaxSlots + 5 + 10) * 8 + 16;
   static_assert(px_slots<AP, PAIR>() <= kPxMaxSlots && smem <= kPxSmem, "ring fits");
   auto kern = k_prefix_gemm<BF16, AP, CP, PS, VALUES, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -707,7 +751,7 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
 // C parts: CP copies of [plen][r] 16-bit rows at `c`, one after another.
 template <bool BF16, int CP>
 cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* c, const void* qt16, float gain,
-                   int sms, int32_t* status, cudaStream_t s) {
+                   int sms, int32_t* counter, int32_t* status, cudaStream_t s) {
   constexpr int PS = BF16 ? 2 : 1;
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const cuuint64_t r = cuuint64_t(d.r), P = cuuint64_t(L.plen), rows = cuuint64_t(L.MB) * 128, ppad = cuuint64_t(L.ppad);
@@ -738,7 +782,7 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
   PxArgs g{d.batch, d.H, d.r, L.plen, L.nb, L.MB, L.tiles, L.ppad, L.SP, ws + L.p,
            reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pm),
            reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz),
-           gain, status};
+           gain, counter, status};
   cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
   if (e != cudaSuccess) return e;
   if (L.tiles != L.SP) {
@@ -817,7 +861,8 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
 }
 
 cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                          const void* scales, const void* qt16, const float* qt32, float gain, int sms, int32_t* status,
+                          const void* scales, const void* qt16, const float* qt32, float gain, int sms,
+                          int32_t* counter, int32_t* status,
                           cudaStream_t s) {
   if (!L.fast) {
     // the CUDA-core split kernel with the same rows for every sequence: no
@@ -828,9 +873,9 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
                                       reinterpret_cast<float*>(ws + L.pm), reinterpret_cast<float*>(ws + L.pl),
                                       reinterpret_cast<float*>(ws + L.pz), s);
   }
-  if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
-  if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, status, s);
-  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, status, s);
+  if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
+  if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
+  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, counter, status, s);
 }
 
 cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,

@@ -24,13 +24,15 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 
 // The prefix's partials (m, l, z per slot) from the absorbed query: qt16 its
 // 16-bit parts [B][2][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
-// the tensor cores' scores, for what their accumulation truncates.
+// the tensor cores' scores, for what their accumulation truncates.  counter:
+// one word, zero.
 // launch_prefix_expand goes before the own rows' split kernel and
 // launch_prefix directly behind it: the scores wait for nothing of it.
 cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
                                  const void* scales, cudaStream_t s);
 cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                          const void* scales, const void* qt16, const float* qt32, float gain, int sms, int32_t* status,
+                          const void* scales, const void* qt16, const float* qt32, float gain, int sms,
+                          int32_t* counter, int32_t* status,
                           cudaStream_t s);
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
 // Accumulations that a score of the tensor-core path takes.

@@ -214,14 +214,12 @@ __device__ __forceinline__ void sts128z(uint32_t a) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
 }
 // Zeros in rows [r0, r1) of a Z slot (two 64-channel boxes of 64 rows; whole
-// rows, so the swizzle has no bearing), by one warp.
+// rows, so the swizzle has no bearing), by one warp; the caller fences.
 __device__ __forceinline__ void zero_z_rows(uint32_t d, int r0, int r1, int lane) {
   for (int i = r0 * 8 + lane; i < r1 * 8; i += 32) {
     sts128z(d + uint32_t(i) * 16);
     sts128z(d + uint32_t(kZBoxBytes) + uint32_t(i) * 16);
   }
-  fence_proxy_async();   // generic-proxy stores -> visible to the tensor core
-  __syncwarp();
 }
 
 // ------------------------------------------------- quantised latent rows
@@ -936,16 +934,30 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
               rg.advance();
             }
         } else {
-          // the other lanes' ring positions: lane 0's
-          rg.slot = __shfl_sync(0xffffffffu, rg.slot, 0);
-          for (int u = 0; u < NI; ++u) {
-            if (SG && !sg_owns(u >> 1, ch, cpart, kind)) continue;
-            if (lane == 0 && ok) ok = mbar_wait(saddr(&zfull[rg.slot]), rg.phase);
-            const int left = nv - 64 * (u & 1), nk = min(4, max(0, (left + 15) >> 4));
-            if (nk > 0 && left < 16 * nk && __shfl_sync(0xffffffffu, int(ok), 0))
-              zero_z_rows(zring + uint32_t(rg.slot * kZSlotBytes), left, 16 * nk, lane);
-            if (lane == 0 && ok) issue(u, pb, first, nk);
-            rg.advance();
+          // in batches of half the ring: one proxy fence and one meeting of the
+          // lanes for several items (12 fences, one per item, took 16 us a
+          // tile at r 1536, and the ring's other half loads meanwhile)
+          rg.slot = __shfl_sync(0xffffffffu, rg.slot, 0);   // the other lanes' position: lane 0's
+          const int batch = (rg.n + 1) / 2;
+          for (int u = 0; u < NI;) {
+            const int u0 = u;
+            Ring ahead = rg;
+            for (int c = 0; u < NI && c < batch; ++u) {
+              if (SG && !sg_owns(u >> 1, ch, cpart, kind)) continue;
+              if (lane == 0 && ok) ok = mbar_wait(saddr(&zfull[ahead.slot]), ahead.phase);
+              const int left = nv - 64 * (u & 1), nk = min(4, max(0, (left + 15) >> 4));
+              if (nk > 0 && left < 16 * nk && __shfl_sync(0xffffffffu, int(ok), 0))
+                zero_z_rows(zring + uint32_t(ahead.slot * kZSlotBytes), left, 16 * nk, lane);
+              ahead.advance();
+              ++c;
+            }
+            fence_proxy_async();   // generic-proxy stores -> visible to the tensor core
+            __syncwarp();
+            for (int v = u0; v < u; ++v) {
+              if (SG && !sg_owns(v >> 1, ch, cpart, kind)) continue;
+              if (lane == 0 && ok) issue(v, pb, first, min(4, max(0, (nv - 64 * (v & 1) + 15) >> 4)));
+              rg.advance();
+            }
           }
         }
         if (lane == 0 && ok) {

@@ -22,8 +22,8 @@
 // src[j] >= j of the source, src increasing.  A CTA owns a column slice of a
 // sequence and walks the rows in chunks, the whole chunk read before any of
 // it is written: what chunk k writes, rows below its end, no later chunk
-// reads, since src[j] >= j.  Into other memory there is no order, and a CTA
-// copies whole rows.
+// reads, since src[j] >= j -- so the next chunk is already loading.  Into other
+// memory there is no order, and a CTA copies whole rows.
 #include "internal.cuh"
 
 namespace qsvd {
@@ -349,21 +349,51 @@ k_evict_move(const MoveArgs a, int ws) {
     const bool mine = v < a.vecs;
     s0 += size_t(v) * 16;
     d0 += size_t(v) * 16;
-    for (long long j0 = 0; j0 < m; j0 += chunk) {
-      const int last = int(min((long long)m, j0 + chunk)) - 1;
-      if (sb[last] == last) continue;   // src[j] >= j, increasing: the whole chunk stays (uniform)
-      uint4 x[kMvUnroll];
+    // the first chunk with a row that moves: src[j] >= j, increasing, so a
+    // chunk whose last row stays does so whole, and all before it
+    const int chunks = int(((long long)m + chunk - 1) / chunk);
+    int k0 = 0;
+    for (int hi = chunks; k0 < hi;) {   // uniform
+      const int mid = (k0 + hi) >> 1, last = int(min((long long)m, (long long)(mid + 1) * chunk)) - 1;
+      if (sb[last] == last) k0 = mid + 1; else hi = mid;
+    }
+    // The next chunk's rows load while this one's are stored (what this one
+    // stores no later chunk reads), their indices one chunk earlier still; the
+    // barrier puts every thread's loads of a chunk before any of its stores.
+    int at[kMvUnroll];
+    auto index = [&](int k) {
 #pragma unroll
       for (int i = 0; i < kMvUnroll; ++i) {
-        const long long j = j0 + i * rows + row;
-        if (mine && j <= last) x[i] = ld_cg(s0 + size_t(sb[j]) * rb);
+        const long long j = (long long)k * chunk + i * rows + row;
+        at[i] = j < m ? __ldg(sb + j) : -1;
       }
+    };
+    auto load = [&](uint4 (&x)[kMvUnroll]) {
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i)
+        if (mine && at[i] >= 0) x[i] = ld_cg(s0 + size_t(at[i]) * rb);
+    };
+    auto store = [&](int k, const uint4 (&x)[kMvUnroll]) {
+#pragma unroll
+      for (int i = 0; i < kMvUnroll; ++i) {
+        const long long j = (long long)k * chunk + i * rows + row;
+        if (mine && j < m) *reinterpret_cast<uint4*>(d0 + size_t(j) * rb) = x[i];
+      }
+    };
+    uint4 x0[kMvUnroll], x1[kMvUnroll];
+    index(k0);
+    load(x0);
+    index(k0 + 1);
+    for (int k = k0; k < chunks; k += 2) {
+      load(x1);        // chunk k + 1 (no row past the last chunk: its indices are -1)
+      index(k + 2);
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMvUnroll; ++i) {
-        const long long j = j0 + i * rows + row;
-        if (mine && j <= last) *reinterpret_cast<uint4*>(d0 + size_t(j) * rb) = x[i];
-      }
+      store(k, x0);
+      if (k + 1 >= chunks) break;
+      load(x0);
+      index(k + 3);
+      __syncthreads();
+      store(k + 1, x1);
     }
   } else {
     const unsigned long long total = (unsigned long long)m * a.vecs;
@@ -423,9 +453,8 @@ cudaError_t launch_evict(const qsvd_dims& d, const float* weights, const int32_t
   int ws = 0;
   long long walkers;
   if (in_place) {
-    // 128-byte slices, narrower ones where those are too few to fill the GPU (one sequence of 8192 rows of 1536
-    // fp16 channels: 24 slices of 128 bytes against 96 of 32)
-    for (ws = 3; ws > 1 && (long long)((a.vecs + (1 << ws) - 1) >> ws) * d.batch < 296; --ws) {}
+    // slices of 512 bytes, narrower ones where those are too few for the SMs, down to a sector of 32
+    for (ws = 5; ws > 1 && (long long)((a.vecs + (1 << ws) - 1) >> ws) * d.batch < 148; --ws) {}
     walkers = (a.vecs + (1 << ws) - 1) >> ws;
   } else {
     walkers = ((long long)budget * a.vecs + kMvThreads * kMvUnroll - 1) / (kMvThreads * kMvUnroll);

@@ -143,6 +143,14 @@ def _empty_bytes(n: int, device) -> torch.Tensor:
     return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
 
 
+def _scratch(n: int, device, stream) -> torch.Tensor:
+    """A workspace for one call: it outlives the call on ``stream`` even if the caller drops it at once."""
+    t = _empty_bytes(n, device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def qsvd_prepare_weights(dims: qsvd_dims, wd, wuq, wuk, wuv, h2_q=None, packed=None,
                          stream=None) -> torch.Tensor:
     """Lay out W^d, W^u_q, W^u_k, W^u_v (device tensors) into a packed buffer.
@@ -328,7 +336,7 @@ def qsvd_decode_attn_weights(dims: qsvd_dims, packed, qin, qin_is_latent, cache,
     summed over the heads, in ``weights`` (B x max_len float32; added to what
     is there with ``accumulate``).  Returns the workspace."""
     if workspace is None:
-        workspace = _empty_bytes(decode_weights_workspace_bytes(dims, num_splits), cache.device)
+        workspace = _scratch(decode_weights_workspace_bytes(dims, num_splits), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_decode_attn_weights(ctypes.byref(dims), _ptr(packed), _ptr(qin), int(bool(qin_is_latent)),
                                          _ptr(cache), _ptr(scales), _ptr(lengths), int(num_splits), _ptr(workspace),
@@ -354,7 +362,7 @@ def qsvd_decode_attn_shared(dims: qsvd_dims, packed, qin, qin_is_latent, prefix,
     optional B x max_len float32, the own rows' attention weights as in
     qsvd_decode_attn_weights.  Returns the workspace."""
     if workspace is None:
-        workspace = _empty_bytes(decode_shared_workspace_bytes(dims, prefix_len, num_splits), cache.device)
+        workspace = _scratch(decode_shared_workspace_bytes(dims, prefix_len, num_splits), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_decode_attn_shared(ctypes.byref(dims), _ptr(packed), _ptr(qin), int(bool(qin_is_latent)),
                                         _ptr(prefix), _ptr(prefix_scales), int(prefix_len), _ptr(cache), _ptr(scales),
@@ -388,7 +396,7 @@ def qsvd_evict_rows(dims: qsvd_dims, weights, lengths, budget, cache, scales=Non
         dst_weights = weights if dst_weights is None else dst_weights
         dst_lengths = lengths if dst_lengths is None else dst_lengths
     if workspace is None:
-        workspace = _empty_bytes(evict_workspace_bytes(dims, budget), cache.device)
+        workspace = _scratch(evict_workspace_bytes(dims, budget), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_evict_rows(ctypes.byref(dims), _ptr(weights), _ptr(lengths), int(budget), int(sink), int(recent),
                                 _ptr(cache), _ptr(scales), int(dims.max_len if dst_max_len is None else dst_max_len),

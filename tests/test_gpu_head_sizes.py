@@ -16,3 +16,16 @@ def test_decode_output(cuda_ok, d_h, cache, weight, bar):
     out = m.empty_out()
     q.qsvd_decode_attn(m.dims, m.packed, m.qin, True, m.cache, m.scales, m.lengths, out)
     assert rel_err(out, m.exact()[0]) <= bar
+
+
+@pytest.mark.parametrize("r", [512, 544, 1024, 4096, 4128])
+@pytest.mark.parametrize("batch", [1, 17, 50])
+@pytest.mark.parametrize("weight", ["f16", "bf16"])
+def test_decode_output_at_projection_splits(cuda_ok, r, batch, weight):
+    """One to nine k-splits of the projections' GEMV (512 rows each; up to eight in a cluster), and blocks of 16
+    sequences walked by one CTA."""
+    m = Layer(cache=weight, weight=weight, H=4, d_h=64, r=r, lens=tuple(1 + 7 * i % 40 for i in range(batch)),
+              kernel=q.QSVD_KERNEL_SIMT)
+    out = m.empty_out()
+    q.qsvd_decode_attn(m.dims, m.packed, m.qin, True, m.cache, m.scales, m.lengths, out)
+    assert rel_err(out, m.exact()[0]) <= 2e-3

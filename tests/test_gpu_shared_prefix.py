@@ -36,6 +36,9 @@ CASES = {
     "f16-pairs": dict(prefix=9300, lens=(3, 0, 130) * 6, H=32, r=128),   # 5 blocks of query rows in pairs, 37 tiles
     "bf16-pairs": dict(cache="bf16", weight="bf16", out="bf16", prefix=10001, lens=(1,) * 16, H=32, r=192),
     "i8-pairs": dict(cache="i8", prefix=9999, lens=(20,) * 16, H=32, r=256),
+    "f16-rank-4096": dict(prefix=130, lens=(3, 0, 40), H=4, r=4096),    # eight k-splits of the projections: one cluster
+    "f16-rank-4160": dict(prefix=130, lens=(3, 0) * 9, H=4, r=4160),    # nine: tickets; two blocks of sequences
+    "bf16-rank-4160": dict(cache="bf16", weight="bf16", prefix=70, lens=(3, 20), H=4, r=4160),
     # CUDA cores: fp32 rows, other ranks, by request, more heads than a block has rows
     "f32": dict(cache="f32", weight="f32", prefix=300, lens=(0, 140, 7), r=96),
     "f16-simt": dict(prefix=300, lens=(5, 0), kernel=S),

@@ -469,9 +469,9 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 
 // Per (query row, token split): m = the largest reference of the split's
 // tiles, l = their sums brought to it, and P of the tiles with a lower one
-// scaled to it.  A CTA has 32 rows: lane = row for the statistics (whole lines
-// of them), which each of its eight warps takes for itself; the tiles to
-// rescale are shared out over the warps, one row of one at a time.
+// scaled to it.  A CTA has 32 rows, lane = row (whole lines of statistics); the
+// split's tiles are shared out over its eight warps, a row's P to rescale taken
+// by the whole warp.  Bound by the latency of its loads.
 // grid (MB 4, SP), block 256.
 template <typename T16, int PS>
 __global__ void __launch_bounds__(256)
@@ -479,30 +479,28 @@ k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __
               float* __restrict__ pl, int B, int H, int nb, int MB, int tiles, int ppad, int SP) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
+  __shared__ float red[2][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int mb = int(blockIdx.x) >> 2, i0 = 32 * (int(blockIdx.x) & 3), sp = blockIdx.y;
   const int live = min(nb, B - mb * nb) * H;   // rows of the block that are queries
-  if (i0 >= live) return;
+  if (i0 >= live) return;   // uniform across the CTA
   const size_t rows = size_t(MB) * 128, row0 = size_t(mb) * 128 + i0;
   const bool mine = i0 + lane < live;
   const float* mr = mt + row0 + (mine ? lane : 0);
   const float* lr = lt + row0 + (mine ? lane : 0);
-  const int t0 = split_tile(sp, tiles, SP), t1 = split_tile(sp + 1, tiles, SP);
+  const int t0 = split_tile(sp, tiles, SP) + warp, t1 = split_tile(sp + 1, tiles, SP);
   float m = -INFINITY;
-#pragma unroll 8
-  for (int t = t0; t < t1; ++t) m = fmaxf(m, __ldcg(mr + size_t(t) * rows));
-  if (warp == 0) {
-    float l = 0.f;
-#pragma unroll 8
-    for (int t = t0; t < t1; ++t) l = fmaf(exp2f(__ldcg(mr + size_t(t) * rows) - m), __ldcg(lr + size_t(t) * rows), l);
-    if (mine) {
-      const size_t at = (size_t(sp) * B + size_t(mb) * nb) * H + i0 + lane;
-      pm[at] = m;
-      pl[at] = l;
-    }
-  }
-  for (int t = t0 + warp; t < t1; t += 8) {
+#pragma unroll 4
+  for (int t = t0; t < t1; t += 8) m = fmaxf(m, __ldcg(mr + size_t(t) * rows));
+  red[0][warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, red[0][w][lane]);
+  float l = 0.f;
+#pragma unroll 4
+  for (int t = t0; t < t1; t += 8) {
     const float f = exp2f(__ldcg(mr + size_t(t) * rows) - m);   // a power of two
+    l = fmaf(f, __ldcg(lr + size_t(t) * rows), l);
     unsigned lower = __ballot_sync(0xffffffffu, mine && f != 1.f);
     while (lower) {
       const int i = __ffs(lower) - 1;
@@ -518,6 +516,16 @@ k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __
         *v = x;
       }
     }
+  }
+  red[1][warp][lane] = l;
+  __syncthreads();
+  if (warp == 0 && mine) {
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += red[1][w][lane];
+    const size_t at = (size_t(sp) * B + size_t(mb) * nb) * H + i0 + lane;
+    pm[at] = m;
+    pl[at] = l;
   }
 }
 

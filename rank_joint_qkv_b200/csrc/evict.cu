@@ -14,9 +14,12 @@
 //                   dependent steps.  So a sequence gets a cluster of CTAs,
 //                   one per 4096 rows up to eight, whose threads hold their
 //                   keys in registers across the steps and add up the
-//                   histograms over distributed shared memory.
+//                   histograms over distributed shared memory (one CTA for
+//                   60,001 rows: 98 us; eight: 22 us).
 //   k_evict_move    the rows' bytes, scales and weights: bound by HBM, each
-//                   kept row read and written once
+//                   kept row read and written once (16 x 8192 rows of 3 KB to
+//                   half: 66 us, 6.1 TB/s, 0.93 of a copy's rate; in place, in
+//                   order, 4.6 TB/s)
 //
 // In place the move has an order to keep: row j of the result is row
 // src[j] >= j of the source, src increasing.  A CTA owns a column slice of a

@@ -71,7 +71,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the CTA's threads; *total: the sum.  red: 33 words.
+// Exclusive sum over the CTA's 1024 threads; *total: the sum.  red: 32 words
+// that the call before did not use (one barrier a call: every warp scans the
+// warps' sums for itself).
 __device__ __forceinline__ uint32_t cta_exclusive(uint32_t v, uint32_t* red, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
@@ -82,20 +84,15 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t v, uint32_t* red, uin
   }
   if (lane == 31) red[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t y = red[lane];
+  uint32_t y = red[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    red[lane] = y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
-  __syncthreads();
-  const uint32_t before = warp ? red[warp - 1] : 0u;
-  *total = red[31];
-  __syncthreads();   // red is reused by the next call
-  return before + x - v;
+  *total = __shfl_sync(0xffffffffu, y, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+  return (warp ? before : 0u) + x - v;
 }
 
 // grid B x CS in clusters of CS, block 1024.  CTA `rank` of a sequence's
@@ -107,7 +104,8 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   __shared__ __align__(8) uint32_t hist[3][kBins];
-  __shared__ uint32_t red[33];
+  __shared__ uint32_t red[2][32];
+  int turn = 0;   // of red's halves
   __shared__ uint32_t found[2];    // digit, count above it
   __shared__ uint32_t counts[2];   // this CTA's rows above the threshold (or kept anyway), and equal to it
   const int b = int(blockIdx.x) / CS, tid = threadIdx.x;
@@ -186,7 +184,7 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
       low = hist[pass][bin];
     }
     uint32_t total;
-    const uint32_t before = cta_exclusive(top + low, red, &total);
+    const uint32_t before = cta_exclusive(top + low, red[turn ^= 1], &total);
     if (before < K && K <= before + top + low) {   // one thread, the same in every CTA
       const bool upper = K <= before + top;
       found[0] = uint32_t(bin + (upper ? 1 : 0));
@@ -238,7 +236,7 @@ k_evict_select(const float* __restrict__ weights, const int32_t* lengths, int ma
     uint32_t above, equal;
     sort_out(&above, &equal);
     uint32_t all;   // 16 bits each: rows above, rows equal (a chunk has 8192)
-    const uint32_t before = cta_exclusive((uint32_t(__popc(above)) << 16) + uint32_t(__popc(equal)), red, &all);
+    const uint32_t before = cta_exclusive((uint32_t(__popc(above)) << 16) + uint32_t(__popc(equal)), red[turn ^= 1], &all);
     const unsigned left = K - min(K, eq);   // equal rows still to take at the chunk's start
     unsigned a = before >> 16, e = before & 0xFFFFu;
     for (uint32_t rest = above | equal; rest; rest &= rest - 1) {

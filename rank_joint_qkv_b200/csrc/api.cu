@@ -433,8 +433,10 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   float* pl = reinterpret_cast<float*>(Wb + W.pl);
   float* pz = reinterpret_cast<float*>(Wb + W.pz);
   float* opart = reinterpret_cast<float*>(Wb + W.opart);
-  const float* rope_tab = reinterpret_cast<const float*>(P + L.rope);
   const bool px = x.on && x.prefix_len > 0;   // prefix rows: on the tensor cores (X.fast) or the CUDA cores
+  // the own rows' positions start behind a prefix
+  const float* rope_tab = px && d.rope ? reinterpret_cast<const float*>(Wb + X.tab) : reinterpret_cast<const float*>(P + L.rope);
+  const float* own_tab = rope_tab + (px && d.rope ? size_t(x.prefix_len) * d.d_h : 0);
   const double gain = x.on ? split_score_gain(d, kernel) : 1.0;
   const float sl2 = float(double(score_scale_log2(d)) * gain);
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
@@ -446,9 +448,10 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     int32_t* tickets = reinterpret_cast<int32_t*>(Wb + W.tickets);
     if ((e = launch_schedule(d, lengths, G, sched, hdr, kernel, tickets, W.NT + 1, s)) != cudaSuccess)
       return cuda_fail(e, "schedule");
-    if (x.on && ((px && !X.fast) || !combine_uses_gemv(d)) &&
+    if (x.on && ((px && (!X.fast || d.rope)) || !combine_uses_gemv(d)) &&
         (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
       return cuda_fail(e, "prefix schedule");
+    if (px && d.rope && (e = launch_prefix_table(d, X, Wb, s)) != cudaSuccess) return cuda_fail(e, "rotary table");
     const bool third = x.weights != nullptr;   // see launch_absorb
     // q = c_new W^u_q (reduced into the workspace), or the query as given
     const float* qsrc = qin;
@@ -459,7 +462,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     }
     // rotary mode keeps the rotated query in the q section (qt32 is unused there)
     if (d.rope)
-      e = launch_rope_query(d, qsrc, sched, rope_tab, sl2, qt32, s);
+      e = launch_rope_query(d, qsrc, sched, rope_tab, sl2, qt32, s, px ? x.prefix_len : 0);
     else
       // only the copies the split kernels read: fp32 for CUDA cores, 16-bit hi/lo
       // for tensor cores; a quantised latent on the tensor cores takes the
@@ -481,14 +484,14 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     if (d.rope && kernel == QSVD_KERNEL_TCGEN05_CTA) {
       e = cudaSuccess;
       if (phases & QSVD_PHASE_SPLIT_SCORES)
-        e = launch_rope_scores(d, cache, P + L.wukT, qt32, rope_tab, sched, sms,
+        e = launch_rope_scores(d, cache, P + L.wukT, qt32, own_tab, sched, sms,
                                scores, &hdr->status, s);
       if (e == cudaSuccess && (phases & QSVD_PHASE_SPLIT_ACCUM))
         e = split_tc_scores_supported(d)
                 ? launch_split_tc_scores(d, scores, cache, sched, G, pm, pl, pz, &hdr->status, s)
                 : launch_split_simt_scores(d, scores, cache, scales, sched, G, pm, pl, pz, s);
     } else if (d.rope) {
-      e = launch_split_simt_rope(d, qt32, P + L.wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s,
+      e = launch_split_simt_rope(d, qt32, P + L.wuk, own_tab, cache, scales, sched, G, pm, pl, pz, s,
                                  keep);
     }
     else if (kernel == QSVD_KERNEL_TCGEN05_CLUSTER)
@@ -500,9 +503,11 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       e = launch_split_simt_absorbed(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
     if (e != cudaSuccess) return cuda_fail(e, "split phase");
     if (px) {
-      e = launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qt32,
-                        float(score_gain(prefix_score_steps(d)) / gain), sms,
-                        reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);
+      e = d.rope ? launch_prefix_rope(d, X, Wb, x.prefix, x.prefix_scales, P + L.wuk, P + L.wukT, qt32, sms,
+                                      &hdr->status, s)
+                 : launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qt32,
+                                 float(score_gain(prefix_score_steps(d)) / gain), sms,
+                                 reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);
       if (e != cudaSuccess) return cuda_fail(e, "prefix");
     }
   }
@@ -581,17 +586,17 @@ qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, c
   if (st != QSVD_OK) return st;
   const qsvd_dims& d = *dims;
   if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
-  if (d.rope)
-    return fail(QSVD_ERR_UNSUPPORTED, "a shared prefix needs absorbed mode (no rotary embedding)");
   if (prefix_len < 0 || (long long)d.batch * prefix_len > 0x7FFFFFFFLL)
     return fail(QSVD_ERR_INVALID_ARG, "prefix_len (%d) must be >= 0 and batch x prefix_len below 2^31", prefix_len);
+  if (d.rope && (long long)d.max_len + prefix_len > 0x7FFFFFFFLL)
+    return fail(QSVD_ERR_INVALID_ARG, "max_len + prefix_len must be below 2^31");
   if (workspace && prefix_len > 0) {
     if (!prefix || !aligned16(prefix)) return fail(QSVD_ERR_INVALID_ARG, "prefix must be given, 16-byte aligned");
     if (cache_is_int(d) && (!prefix_scales || !aligned2(prefix_scales)))
       return fail(QSVD_ERR_INVALID_ARG, "int caches need prefix_scales, 2-byte aligned");
   }
   if (weights && !aligned4(weights)) return fail(QSVD_ERR_INVALID_ARG, "weights must be 4-byte aligned");
-  if (split_simt_grid_heads(d) == 0 && (d.cache_dtype == QSVD_F32 || d.r % 64 || d.H > 128))
+  if (!d.rope && split_simt_grid_heads(d) == 0 && (d.cache_dtype == QSVD_F32 || d.r % 64 || d.H > 128))
     return fail(QSVD_ERR_UNSUPPORTED, "rank too large for the CUDA-core split kernel");
   DecodeExtra x;
   x.on = true;

@@ -219,7 +219,7 @@ cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, f
 cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s);
 cudaError_t launch_rope_query(const qsvd_dims& d, const float* q, const int32_t* sched,
                               const float* rope_tab, float scale_log2, float* qrot,
-                              cudaStream_t s);
+                              cudaStream_t s, int before = 0);
 
 // Split phase.  keep (absorbed mode and the CUDA-core rotary kernel): the
 // scores are also written there, [B][H][max_len] in the log2 domain, when it
@@ -236,6 +236,12 @@ bool rope_tc_supported(const qsvd_dims& d);
 cudaError_t launch_rope_scores(const qsvd_dims& d, const void* cache, const void* wukT,
                                const float* qrot, const float* rope_tab, const int32_t* sched,
                                int G, float* scores, int32_t* status, cudaStream_t s);
+// The same of a prefix of plen rows that all sequences share: each key is
+// rebuilt once and scored against every sequence's query; sched1: {0, tiles,
+// plen}, scores [B][H][stride].
+cudaError_t launch_rope_scores_shared(const qsvd_dims& d, const void* prefix, int plen, const void* wukT,
+                                      const float* qrot, const float* rope_tab, const int32_t* sched1, int G,
+                                      float* scores, int stride, int32_t* status, cudaStream_t s);
 bool split_tc_scores_supported(const qsvd_dims& d);
 int split_tc_scores_parts(const qsvd_dims& d);   // CTAs sharing one split's channels
 cudaError_t launch_split_tc_scores(const qsvd_dims& d, const float* scores, const void* cache,

@@ -49,6 +49,7 @@
 
 #include "internal.cuh"
 #include "prefix.cuh"
+#include "wsvd.cuh"
 #include "tc_common.cuh"
 
 namespace qsvd {
@@ -537,6 +538,51 @@ k_prefix_norm(T16* __restrict__ p, const float* __restrict__ mt, const float* __
   }
 }
 
+// Rotary mode: what the scores' epilogue does, from scores in memory
+// [B][H][ppad].  Warp = (row, tile of 256 tokens), lane = 8 tokens.
+// Bound by the scores read and P written, 6 B H P bytes (fp16), from L2.
+// grid ceil(B H tiles / 8), block 256.
+template <typename T16, int PS>
+__global__ void __launch_bounds__(256)
+k_prefix_probs(const float* __restrict__ scores, T16* __restrict__ p, float* __restrict__ mt, float* __restrict__ lt,
+               int B, int H, int nb, int MB, int plen, int tiles, int ppad, bool own) {
+  dev::pdl_wait();   // see launch_pdl
+  dev::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (u >= (long long)B * H * tiles) return;
+  const int tile = int(u % tiles), bh = int(u / tiles), b = bh / H, h = bh % H;
+  const size_t rows = size_t(MB) * 128, row = size_t(b / nb) * 128 + (b % nb) * H + h;
+  const int t0 = tile * kPxTile + 8 * lane;   // padded to ppad: loads stay inside the row
+  float v[8];
+  const float4* src = reinterpret_cast<const float4*>(scores + size_t(bh) * ppad + t0);
+  *reinterpret_cast<float4*>(v) = __ldcg(src);
+  *reinterpret_cast<float4*>(v + 4) = __ldcg(src + 1);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = t0 + e < plen ? fmaxf(mx, v[e]) : mx;
+  const float ref = kRefStep * floorf(dev::warp_max(mx) / kRefStep);
+  float sum = 0.f;
+  uint4 hi, lo;
+  T16* hv = reinterpret_cast<T16*>(&hi);
+  T16* lv = reinterpret_cast<T16*>(&lo);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = t0 + e < plen ? exp2f(v[e] - ref) : 0.f;
+    sum += x;
+    hv[e] = dev::from_f<T16>(x);
+    if (PS == 2) lv[e] = dev::from_f<T16>(x - dev::to_f(hv[e]));
+  }
+  *reinterpret_cast<uint4*>(p + row * ppad + t0) = hi;
+  if (PS == 2) *reinterpret_cast<uint4*>(p + (rows + row) * ppad + t0) = lo;
+  sum = dev::warp_sum(sum);
+  if (lane == 0) {
+    const size_t at = own ? (size_t(tile) * B + b) * H + h : size_t(tile) * rows + row;
+    mt[at] = ref;
+    lt[at] = sum;
+  }
+}
+
 // Quantised prefix -> fp16 hi and lo parts of code x scale, [2][P][r].
 // Thread = one 16-byte vector of codes.
 template <qsvd_dtype CT>
@@ -572,7 +618,8 @@ k_prefix_expand(const uint8_t* __restrict__ codes, const __half* __restrict__ sc
 }
 
 // Schedules that need no lengths: the prefix as B sequences of plen rows
-// (CUDA cores), and one tile per sequence for the combine of merged slots.
+// (CUDA cores), as one sequence (behind it: rotary scores), and one tile per
+// sequence for the combine of merged slots.
 __global__ void __launch_bounds__(256)
 k_prefix_schedule(int32_t* __restrict__ sched, int32_t* __restrict__ csched, WsHeader* __restrict__ hdr, int B,
                   int plen) {
@@ -588,6 +635,9 @@ k_prefix_schedule(int32_t* __restrict__ sched, int32_t* __restrict__ csched, WsH
     }
   }
   if (threadIdx.x == 0) {
+    sched[2 * B + 1] = 0;
+    sched[2 * B + 2] = nt;
+    sched[2 * B + 3] = plen;
     hdr->status = 0;
     hdr->G = B;
     hdr->tile = kTile;
@@ -765,14 +815,15 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
 }
 
 // C parts: CP copies of [plen][r] 16-bit rows at `c`, one after another.
+// given: the scores are in memory already (rotary mode).
 template <bool BF16, int CP>
 cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* c, const void* qt16, float gain,
-                   int sms, int32_t* counter, int32_t* status, cudaStream_t s) {
+                   int sms, int32_t* counter, int32_t* status, cudaStream_t s, const float* given = nullptr) {
   constexpr int PS = BF16 ? 2 : 1;
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const cuuint64_t r = cuuint64_t(d.r), P = cuuint64_t(L.plen), rows = cuuint64_t(L.MB) * 128, ppad = cuuint64_t(L.ppad);
   CUtensorMap tq, tp, tbs[2], tbv[2];
-  {
+  if (!given) {
     // query parts [B][2][H][r] as {channel, head, part, sequence}: one box is a block's rows of one part
     const cuuint64_t dims[4] = {r, cuuint64_t(d.H), 2, cuuint64_t(d.batch)};
     const cuuint64_t strides[3] = {r * 2, cuuint64_t(d.H) * r * 2, 2 * cuuint64_t(d.H) * r * 2};
@@ -799,7 +850,17 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
            reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pm),
            reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz),
            gain, counter, status};
-  cudaError_t e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
+  cudaError_t e;
+  if (given) {
+    const bool own = L.tiles == L.SP;   // as in the scores' epilogue
+    const long long warps = (long long)d.batch * d.H * L.tiles;
+    e = launch_pdl(k_prefix_probs<T16, PS>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, given,
+                   reinterpret_cast<T16*>(ws + L.p), own ? g.pm : g.mt, own ? g.pl : g.lt, d.batch, d.H, L.nb, L.MB,
+                   L.plen, L.tiles, L.ppad, own);
+    if (e == cudaSuccess) { note_launch(); e = check_launch(); }
+  } else {
+    e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
+  }
   if (e != cudaSuccess) return e;
   if (L.tiles != L.SP) {
     e = launch_pdl(k_prefix_norm<T16, PS>, dim3(unsigned(4 * L.MB), unsigned(L.SP)), dim3(256), 0, s,
@@ -818,11 +879,12 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
   PrefixLayout L{};
   const bool q = cache_is_int(d);
   L.plen = plen;
-  L.fast = d.kernel != QSVD_KERNEL_SIMT && d.cache_dtype != QSVD_F32 && d.r % 64 == 0 && d.H <= 128;
+  L.fast = d.kernel != QSVD_KERNEL_SIMT && d.H <= 128 &&
+           (d.rope ? rope_tc_supported(d) : d.cache_dtype != QSVD_F32 && d.r % 64 == 0);
   const size_t B = size_t(d.batch), H = size_t(d.H), r = size_t(d.r), P = size_t(plen);
   size_t o = base;
   L.ml = o; o = align256(o + B * H * 8);
-  L.sched = o; o = align256(o + (2 * B + 1) * 4);
+  L.sched = o; o = align256(o + (2 * B + 4) * 4);
   L.csched = o; o = align256(o + (2 * B + 1) * 4);
   L.hdr = o; o = align256(o + sizeof(WsHeader));
   if (!combine_uses_gemv(d)) {   // merged slots for the CUDA-core combine
@@ -831,6 +893,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     L.cz = o; o = align256(o + 2 * B * H * r * 4);
   }
   if (plen == 0) { L.total = o; return L; }
+  if (d.rope) { L.tab = o; o = align256(o + (P + size_t(d.max_len)) * d.d_h * 4); }
   if (L.fast) {
     L.tiles = (plen + kPxTile - 1) / kPxTile;
     L.nb = 128 / d.H;
@@ -860,6 +923,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     L.p = o; o = align256(o + (d.cache_dtype == QSVD_BF16 ? 2 : 1) * rows * L.ppad * 2);
     L.mt = o; o = align256(o + size_t(L.tiles) * rows * 4);
     L.lt = o; o = align256(o + size_t(L.tiles) * rows * 4);
+    if (d.rope) { L.scores = o; o = align256(o + B * H * L.ppad * 4); }
   } else {
     const long long t = (long long)d.batch * ((plen + kTile - 1) / kTile);
     const int hb = split_simt_grid_heads(d);
@@ -892,6 +956,29 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
   if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
   if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
   return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, counter, status, s);
+}
+
+cudaError_t launch_prefix_table(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s) {
+  return launch_rope_table(reinterpret_cast<float*>(ws + L.tab), L.plen + d.max_len, d.d_h, d.rope_base, s, true);
+}
+
+cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                               const void* scales, const void* wuk, const void* wukT, const float* qrot, int sms,
+                               int32_t* status, cudaStream_t s) {
+  const float* tab = reinterpret_cast<const float*>(ws + L.tab);
+  const int32_t* sched = reinterpret_cast<const int32_t*>(ws + L.sched);
+  if (!L.fast) {
+    qsvd_dims v = d;   // as in launch_prefix
+    v.max_len = 0;
+    return launch_split_simt_rope(v, qrot, wuk, tab, prefix, scales, sched, L.G, reinterpret_cast<float*>(ws + L.pm),
+                                  reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz), s);
+  }
+  float* scores = reinterpret_cast<float*>(ws + L.scores);
+  const cudaError_t e = launch_rope_scores_shared(d, prefix, L.plen, wukT, qrot, tab, sched + 2 * d.batch + 1, sms, scores,
+                                                  L.ppad, status, s);
+  if (e != cudaSuccess) return e;
+  return d.cache_dtype == QSVD_BF16 ? fast_t<true, 1>(d, L, ws, prefix, nullptr, 1.f, sms, nullptr, status, s, scores)
+                                    : fast_t<false, 1>(d, L, ws, prefix, nullptr, 1.f, sms, nullptr, status, s, scores);
 }
 
 cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,

@@ -11,14 +11,14 @@ constexpr int kPxTile = 256;   // tokens per score tile
 // Sections behind the decode's own workspace.
 struct PrefixLayout {
   bool pair;        // fast: CTA pairs
-  bool fast;        // tensor cores; else the CUDA-core split kernel on B views of the prefix
+  bool fast;        // tensor cores; else the CUDA-core split kernels on B views of the prefix
   int plen, tiles;  // prefix rows, score tiles
   int nb, MB;       // sequences per block of 128 query rows, blocks
   int ppad;         // tokens per row of P (tiles x 256)
   int SP;           // token splits of the value product
   int G;            // CUDA cores: split CTAs
   int slots;        // partials (fast: SP x B; CUDA cores: G + B)
-  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, total;
+  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, tab, scores, total;
 };
 PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 
@@ -34,6 +34,13 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
                           const void* scales, const void* qt16, const float* qt32, float gain, int sms,
                           int32_t* counter, int32_t* status,
                           cudaStream_t s);
+// Rotary mode: the table of all positions, prefix then own rows (tab, built
+// per call: the packed one ends at max_len), and the partials from the rotated
+// query qrot [B][H][d_h].
+cudaError_t launch_prefix_table(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
+cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
+                               const void* scales, const void* wuk, const void* wukT, const float* qrot, int sms,
+                               int32_t* status, cudaStream_t s);
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
 // Accumulations that a score of the tensor-core path takes.
 int prefix_score_steps(const qsvd_dims& d);

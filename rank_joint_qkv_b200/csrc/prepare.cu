@@ -80,8 +80,11 @@ __global__ void k_transpose(const WT* __restrict__ src, WT* __restrict__ dst, in
 }
 
 // tab[pos][i] = {cos, sin}(pos * base^(-2i/d_h)), angles in float64.
+// (launched with programmatic serialisation it runs beside its predecessor
+// and lets its successor start: see launch_pdl)
 __global__ void k_rope_table(float* __restrict__ tab, int max_len, int half, double log_base,
                              int d_h) {
+  dev::pdl_trigger();
   const size_t n = size_t(max_len) * half;
   for (size_t idx = size_t(blockIdx.x) * blockDim.x + threadIdx.x; idx < n;
        idx += size_t(gridDim.x) * blockDim.x) {
@@ -92,6 +95,7 @@ __global__ void k_rope_table(float* __restrict__ tab, int max_len, int half, dou
     tab[idx * 2 + 0] = float(c);
     tab[idx * 2 + 1] = float(s);
   }
+  dev::pdl_wait();
 }
 
 // Per-head fold of the value up-projection into the output projection (WSVD
@@ -345,11 +349,17 @@ cudaError_t launch_per_head_fold(const qsvd_dims& d, const void* bv, const void*
   }
 }
 
-cudaError_t launch_rope_table(float* tab, int max_len, int d_h, float base, cudaStream_t s) {
+cudaError_t launch_rope_table(float* tab, int max_len, int d_h, float base, cudaStream_t s, bool beside) {
   const int half = d_h / 2;
   const size_t n = size_t(max_len) * half;
   const unsigned blocks = unsigned(std::min<size_t>((n + 255) / 256, 4096));
-  k_rope_table<<<blocks, 256, 0, s>>>(tab, max_len, half, std::log(double(base)), d_h);
+  if (beside) {
+    const cudaError_t e =
+        launch_pdl(k_rope_table, dim3(blocks), dim3(256), 0, s, tab, max_len, half, std::log(double(base)), d_h);
+    if (e != cudaSuccess) return e;
+  } else {
+    k_rope_table<<<blocks, 256, 0, s>>>(tab, max_len, half, std::log(double(base)), d_h);
+  }
   note_launch();
   return check_launch();
 }

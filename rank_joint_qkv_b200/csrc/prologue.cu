@@ -347,18 +347,19 @@ k_quant_query(const float* __restrict__ qt, int8_t* __restrict__ qp, float* __re
 }
 
 // ---------------------------------------------------------------------------
-// Rotary query: q_h <- scale * R(len_b - 1) q_h, pairs (i, i + d_h/2).
+// Rotary query: q_h <- scale * R(before + len_b - 1) q_h, pairs (i, i + d_h/2),
+// with `before` rows of a shared prefix ahead of the sequence's own.
 // grid (B), block 256.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 k_rope_query(const float* __restrict__ q, const int32_t* __restrict__ sched,
-             const float* __restrict__ tab, float scale, float* __restrict__ qrot, int B,
+             const float* __restrict__ tab, int before, float scale, float* __restrict__ qrot, int B,
              int H, int d_h, int E) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   const int b = blockIdx.x;
   const int n = sched[B + 1 + b];
-  const int pos = n > 0 ? n - 1 : 0;
+  const int pos = max(before + n - 1, 0);
   const int half = d_h / 2;
   for (int i = threadIdx.x; i < H * half; i += blockDim.x) {
     const int h = i / half, k = i % half;
@@ -545,10 +546,10 @@ cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, 
 
 cudaError_t launch_rope_query(const qsvd_dims& d, const float* q, const int32_t* sched,
                               const float* rope_tab, float scale, float* qrot,
-                              cudaStream_t s) {
+                              cudaStream_t s, int before) {
   {
     const cudaError_t le = launch_pdl(k_rope_query, dim3(d.batch), dim3(256), 0, s,
-                                     q, sched, rope_tab, scale, qrot, d.batch, d.H, d.d_h, d.E);
+                                     q, sched, rope_tab, before, scale, qrot, d.batch, d.H, d.d_h, d.E);
     if (le != cudaSuccess) return le;
   }
   note_launch();

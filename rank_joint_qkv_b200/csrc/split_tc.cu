@@ -1265,12 +1265,17 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
 constexpr int kRopeSlotBytes = kBoxBytes + 256 * 128;   // latent box + 256 rows of W^u_k^T
 constexpr int kRopeTabPitch = 65;                        // floats per token row (bank-conflict free)
 
-template <bool BF16>
+// SHARED: the rows are a prefix of all sequences (one tile range, B = 1 for it),
+// and every rebuilt key, held in registers, is dotted with the nq sequences'
+// queries: the rebuild, 2 r d_h flops a key, is done once for the batch, and
+// the dots (nq d_h fma a key on CUDA cores) stay under the next pair's MMAs up
+// to about 32 sequences at r 1536.
+template <bool BF16, bool SHARED>
 __global__ void __launch_bounds__(192, 1)
 k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_w,
               const float* __restrict__ qrot, const float* __restrict__ rope_tab,
               const int32_t* __restrict__ sched, float* __restrict__ scores, int32_t* __restrict__ status,
-              int B, int H, int E, int r, int max_len, int G, int ns) {
+              int B, int H, int E, int r, int max_len, int G, int ns, int nq) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
@@ -1431,6 +1436,36 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
           if (h >= H) break;
           const float* qh = qb + h * 128;
           const uint32_t ta = tmem + lane_off + uint32_t(kb * 256 + hh * 128);
+          if constexpr (SHARED) {
+            float key[128];   // rotated: element j, then 64 + j
+#pragma unroll
+            for (int i0 = 0; i0 < 64; i0 += 16) {
+              float klo[16], khi[16];
+              tmem_ld16(ta + uint32_t(i0), klo);
+              tmem_ld16(ta + uint32_t(64 + i0), khi);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float c = tc[i0 + e], sn = ts[i0 + e];
+                key[i0 + e] = fmaf(klo[e], c, -khi[e] * sn);
+                key[64 + i0 + e] = fmaf(khi[e], c, klo[e] * sn);
+              }
+            }
+            for (int b1 = 0; b1 < nq; ++b1) {   // the query's loads are one address for the warp
+              const float4* q4 = reinterpret_cast<const float4*>(qrot + size_t(b1) * E + h * 128);
+              float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+              for (int v = 0; v < 32; ++v) {
+                const float4 x = __ldg(q4 + v);
+                s0 = fmaf(x.x, key[4 * v], s0);
+                s1 = fmaf(x.y, key[4 * v + 1], s1);
+                s2 = fmaf(x.z, key[4 * v + 2], s2);
+                s3 = fmaf(x.w, key[4 * v + 3], s3);
+              }
+              if (t < nv) scores[(size_t(b1) * H + h) * max_len + t0 + t] = (s0 + s1) + (s2 + s3);
+            }
+            continue;
+          }
           float s = 0.f;
 #pragma unroll 1
           for (int i0 = 0; i0 < 64; i0 += 16) {
@@ -1621,16 +1656,17 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   return check_launch();
 }
 
-template <bool BF16>
-cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, const void* wukT, const float* qrot,
-                          const float* rope_tab, const int32_t* sched, int G, float* scores,
+// rows: of the latent in all; SHARED: scores of stride `stride` per (sequence, head).
+template <bool BF16, bool SHARED>
+cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, size_t rows, const void* wukT, const float* qrot,
+                          const float* rope_tab, const int32_t* sched, int G, float* scores, int stride,
                           int32_t* status, cudaStream_t s) {
   TensorMapEncode enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap tc, tw;
   {
-    const cuuint64_t dims[2] = {cuuint64_t(d.r), cuuint64_t(d.batch) * d.max_len};
+    const cuuint64_t dims[2] = {cuuint64_t(d.r), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(d.r) * 2};
     const cuuint32_t box[2] = {64, 128};
     const cuuint32_t es[2] = {1, 1};
@@ -1653,12 +1689,12 @@ cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, const void* wuk
   constexpr int ns = 3;
   const size_t smem = 1024 + size_t(ns) * kRopeSlotBytes + 2 * 128 * kRopeTabPitch * 4 +
                       (2 * kMaxSlots + 5) * 8 + 16;
-  auto kern = k_rope_scores<BF16>;
+  auto kern = k_rope_scores<BF16, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   {
     const cudaError_t le = launch_pdl(kern, dim3(G), dim3(192), smem, s,
-                                     tc, tw, qrot, rope_tab, sched, scores, status, d.batch, d.H, d.E, d.r, d.max_len, G, ns);
+                                     tc, tw, qrot, rope_tab, sched, scores, status, SHARED ? 1 : d.batch, d.H, d.E, d.r, SHARED ? stride : d.max_len, G, ns, d.batch);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -1755,8 +1791,16 @@ cudaError_t launch_rope_scores(const qsvd_dims& d, const void* cache, const void
                                const float* qrot, const float* rope_tab, const int32_t* sched,
                                int G, float* scores, int32_t* status, cudaStream_t s) {
   return d.cache_dtype == QSVD_BF16
-             ? rope_scores_t<true>(d, cache, wukT, qrot, rope_tab, sched, G, scores, status, s)
-             : rope_scores_t<false>(d, cache, wukT, qrot, rope_tab, sched, G, scores, status, s);
+             ? rope_scores_t<true, false>(d, cache, size_t(d.batch) * d.max_len, wukT, qrot, rope_tab, sched, G, scores, 0, status, s)
+             : rope_scores_t<false, false>(d, cache, size_t(d.batch) * d.max_len, wukT, qrot, rope_tab, sched, G, scores, 0, status, s);
+}
+
+cudaError_t launch_rope_scores_shared(const qsvd_dims& d, const void* prefix, int plen, const void* wukT,
+                                      const float* qrot, const float* rope_tab, const int32_t* sched1, int G,
+                                      float* scores, int stride, int32_t* status, cudaStream_t s) {
+  return d.cache_dtype == QSVD_BF16
+             ? rope_scores_t<true, true>(d, prefix, size_t(plen), wukT, qrot, rope_tab, sched1, G, scores, stride, status, s)
+             : rope_scores_t<false, true>(d, prefix, size_t(plen), wukT, qrot, rope_tab, sched1, G, scores, stride, status, s);
 }
 
 }  // namespace qsvd

@@ -46,7 +46,7 @@ bool wsvd_rope_supported(const qsvd_dims& d);
 cudaError_t launch_wsvd_rope_front(const qsvd_dims& d, const void* bk, const float* q, const void* ck,
                                    const int32_t* lengths, float sl2, void* workspace, const WsvdLayout& W,
                                    int token_major, cudaStream_t s);
-cudaError_t launch_rope_table(float* tab, int max_len, int d_h, float base, cudaStream_t s);
+cudaError_t launch_rope_table(float* tab, int max_len, int d_h, float base, cudaStream_t s, bool beside = false);
 
 // Three kernels: absorb (qt = sl2 B_{Kh} q_h), split (per 256-token chunk:
 // exact chunk softmax, partial m, l, z), combine (merge the chunks,

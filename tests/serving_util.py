@@ -92,12 +92,12 @@ class Layer:
             qa = (self.qin[b].to(f64).abs() @ wq.abs()).view(H, d_h)
             worst = max(worst, float(torch.einsum("thd,hd->th", ka, qa).max()) * tau * u)
             if self.rope:
-                ang = torch.arange(n, device=DEV, dtype=f64)[:, None] * \
+                ang = torch.arange(P + n, device=DEV, dtype=f64)[:, None] * \
                     torch.pow(10000.0, -2.0 * torch.arange(d_h // 2, device=DEV, dtype=f64) / d_h)
                 cos, sin = ang.cos()[:, None], ang.sin()[:, None]
                 turn = lambda x, cs, sn: torch.cat([x[..., :d_h // 2] * cs - x[..., d_h // 2:] * sn,  # noqa: E731
                                                     x[..., d_h // 2:] * cs + x[..., :d_h // 2] * sn], -1)
-                qb, k = turn(qb, cos[n - 1], sin[n - 1]), turn(k, cos, sin)
+                qb, k = turn(qb, cos[P + n - 1], sin[P + n - 1]), turn(k, cos, sin)
             p = torch.softmax(torch.einsum("thd,hd->th", k, qb) * tau, 0)
             out[b] = torch.einsum("th,thd->hd", p, v).reshape(-1)
             self.spread[b] = torch.einsum("th,thd->hd", p, v.abs()).reshape(-1)

@@ -45,6 +45,20 @@ CASES = {
     "f16-rank-96": dict(prefix=129, lens=(5, 0), r=96),
     "i8-simt": dict(cache="i8", prefix=129, lens=(70, 2), r=96, group=32, kernel=S),
     "f16-130-heads": dict(prefix=70, lens=(5, 9), H=130, d_h=64, r=64),
+    # rotary: positions run through the prefix and on into the own rows, past the packed table's end
+    "rope-1": dict(prefix=1, lens=(5, 0, 130), d_h=128, rope=True),
+    "rope-127": dict(prefix=127, lens=(0, 0, 0), d_h=128, rope=True),
+    "rope-129": dict(prefix=129, lens=(1,), H=3, d_h=128, r=64, rope=True),      # an odd head: half a pair
+    "rope-256": dict(prefix=256, lens=(64,) * 33, H=4, d_h=128, r=128, rope=True),
+    "rope-1500": dict(prefix=1500, lens=(40, 0, 300, 1, 2), H=32, d_h=128, r=1536, rope=True),
+    "rope-no-prefix": dict(prefix=0, lens=(5, 0, 130), d_h=128, rope=True),
+    "rope-bf16": dict(cache="bf16", weight="bf16", out="bf16", prefix=2000, lens=(0, 33, 200), H=20, d_h=128, r=512, rope=True),
+    "rope-pairs": dict(prefix=9300, lens=(3, 0, 130) * 6, H=32, d_h=128, r=128, rope=True),
+    "rope-130-heads": dict(prefix=70, lens=(5, 9), H=130, d_h=128, r=64, rope=True),   # the prefix on the CUDA cores
+    "rope-f32": dict(cache="f32", weight="f32", prefix=140, lens=(0, 30, 7), H=2, r=96, rope=True),
+    "rope-i8": dict(cache="i8", prefix=129, lens=(70, 2), H=2, d_h=128, r=128, rope=True),
+    "rope-d-64": dict(prefix=150, lens=(5, 0), rope=True),
+    "rope-simt": dict(prefix=130, lens=(5, 0), H=2, d_h=128, r=128, rope=True, kernel=S),
     # the combine without the tensor-core GEMV (d_h % 64 != 0)
     "f16-d-24": dict(prefix=300, lens=(5, 0, 40), H=8, d_h=24, r=128),
     "f32-d-24": dict(cache="f32", weight="f32", prefix=3, lens=(0, 2), H=8, d_h=24, r=64),
@@ -116,10 +130,11 @@ def test_tile_references_that_differ(cuda_ok, cache, rise):
     close_weights(w, want_w, 3 * bound, m.lens)
 
 
-def test_same_as_a_decode_over_the_whole_rows(cuda_ok):
+@pytest.mark.parametrize("form", [dict(H=8, r=256), dict(H=4, d_h=128, r=256, rope=True)], ids=["absorbed", "rope"])
+def test_same_as_a_decode_over_the_whole_rows(cuda_ok, form):
     """The prefix copied in front of every sequence's rows gives the plain decode's output."""
-    m = Layer(prefix=600, lens=(40, 0, 333), H=8, r=256)
-    whole = Layer(lens=[600 + n for n in m.lens], H=8, r=256)
+    m = Layer(prefix=600, lens=(40, 0, 333), **form)
+    whole = Layer(lens=[600 + n for n in m.lens], **form)
     for b, n in enumerate(m.lens):
         whole.cache[b, :600] = m.prefix
         whole.cache[b, 600:600 + n] = m.cache[b, :n]
@@ -143,9 +158,9 @@ def test_output_projection(cuda_ok, proj):
 
 
 def test_rows_behind_the_length_have_no_bearing(cuda_ok):
-    for kernel in (q.QSVD_KERNEL_AUTO, S):
-        clean = run(Layer(prefix=100, lens=(10, 0, 129), kernel=kernel))
-        dirty = run(Layer(prefix=100, lens=(10, 0, 129), kernel=kernel, past=float("nan")))
+    for form in (dict(), dict(kernel=S), dict(d_h=128, rope=True)):
+        clean = run(Layer(prefix=100, lens=(10, 0, 129), **form))
+        dirty = run(Layer(prefix=100, lens=(10, 0, 129), past=float("nan"), **form))
         assert torch.equal(clean, dirty)
 
 

@@ -125,7 +125,7 @@ def shared_call(d, plen=100, splits=4, prefix=OK, prefix_scales=None, workspace=
 def test_shared_refusals():
     d = dims()
     bad = q.QSVD_ERR_INVALID_ARG
-    refused(shared_call(dims(rope=True)), q.QSVD_ERR_UNSUPPORTED, "absorbed mode")
+    refused(shared_call(dims(rope=True, batch=1), plen=0x7FFFFFFF), bad, "max_len + prefix_len")
     refused(shared_call(d, plen=-1), bad, "prefix_len")
     refused(shared_call(d, plen=1 << 30), bad, "below 2^31")
     refused(shared_call(d, prefix=None), bad, "prefix must be given")

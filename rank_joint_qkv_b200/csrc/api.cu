@@ -462,7 +462,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     }
     // rotary mode keeps the rotated query in the q section (qt32 is unused there)
     if (d.rope)
-      e = launch_rope_query(d, qsrc, sched, rope_tab, sl2, qt32, s, px ? x.prefix_len : 0);
+      e = launch_rope_query(d, qsrc, sched, rope_tab, sl2, qt32, s, px ? x.prefix_len : 0,
+                            px && X.fast ? reinterpret_cast<uint32_t*>(Wb + X.qpack) : nullptr);
     else
       // only the copies the split kernels read: fp32 for CUDA cores, 16-bit hi/lo
       // for tensor cores; a quantised latent on the tensor cores takes the

@@ -217,9 +217,16 @@ cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, f
 // Quantised latent on the tensor cores: qt32 [B][H][r] -> three int8 parts
 // qp [B][3][H][r] and one power-of-two scale qs [B][H] per (sequence, head).
 cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s);
+// before: rows ahead of the sequence's own.  pack (d_h 128): also written
+// there are the query's two fp16 parts, scaled by dev::f16_scale, as B
+// fragments of m16n8k16: per (sequence, head) kRopePackWords words, of which
+// lane c of a query's four takes the vectors of four words 4 v + c, v < 8, word
+// 16 part + 2 (k step of 16) + (elements 2 c, 2 c + 1 or 2 c + 8, 2 c + 9) of
+// them; and the scale's inverse at kRopePackScale.
+constexpr int kRopePackWords = 132, kRopePackScale = 128;
 cudaError_t launch_rope_query(const qsvd_dims& d, const float* q, const int32_t* sched,
                               const float* rope_tab, float scale_log2, float* qrot,
-                              cudaStream_t s, int before = 0);
+                              cudaStream_t s, int before = 0, uint32_t* pack = nullptr);
 
 // Split phase.  keep (absorbed mode and the CUDA-core rotary kernel): the
 // scores are also written there, [B][H][max_len] in the log2 domain, when it
@@ -240,7 +247,7 @@ cudaError_t launch_rope_scores(const qsvd_dims& d, const void* cache, const void
 // rebuilt once and scored against every sequence's query; sched1: {0, tiles,
 // plen}, scores [B][H][stride].
 cudaError_t launch_rope_scores_shared(const qsvd_dims& d, const void* prefix, int plen, const void* wukT,
-                                      const float* qrot, const float* rope_tab, const int32_t* sched1, int G,
+                                      const uint32_t* qpack, const float* rope_tab, const int32_t* sched1, int G,
                                       float* scores, int stride, int32_t* status, cudaStream_t s);
 bool split_tc_scores_supported(const qsvd_dims& d);
 int split_tc_scores_parts(const qsvd_dims& d);   // CTAs sharing one split's channels
@@ -391,6 +398,25 @@ __device__ __forceinline__ void pdl_trigger() {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The fp16 parts of two numbers, packed (a low); a and b become the rest.
+__device__ __forceinline__ uint32_t f16_part(float& a, float& b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  a -= __low2float(v);
+  b -= __high2float(v);
+  uint32_t bits;
+  memcpy(&bits, &v, 4);
+  return bits;
+}
+
+// A power of two that brings `most` (>= 0) into [2^14, 2^15), or as far up as it
+// goes, and its inverse: two fp16 parts of what it scales then err by 2^-23 of
+// the element or 2^-39 of `most`.
+__device__ __forceinline__ float f16_scale(float most, float* inverse) {
+  const int field = min(268 - int(__float_as_uint(most) >> 23), 253);   // 127 + 14 - (exponent field - 127)
+  *inverse = __uint_as_float(uint32_t(254 - field) << 23);
+  return __uint_as_float(uint32_t(field) << 23);
+}
 
 template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }

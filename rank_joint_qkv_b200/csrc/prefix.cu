@@ -924,6 +924,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     L.mt = o; o = align256(o + size_t(L.tiles) * rows * 4);
     L.lt = o; o = align256(o + size_t(L.tiles) * rows * 4);
     if (d.rope) { L.scores = o; o = align256(o + B * H * L.ppad * 4); }
+    if (d.rope) { L.qpack = o; o = align256(o + B * H * kRopePackWords * 4); }
   } else {
     const long long t = (long long)d.batch * ((plen + kTile - 1) / kTile);
     const int hb = split_simt_grid_heads(d);
@@ -974,7 +975,7 @@ cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_
                                   reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz), s);
   }
   float* scores = reinterpret_cast<float*>(ws + L.scores);
-  const cudaError_t e = launch_rope_scores_shared(d, prefix, L.plen, wukT, qrot, tab, sched + 2 * d.batch + 1, sms, scores,
+  const cudaError_t e = launch_rope_scores_shared(d, prefix, L.plen, wukT, reinterpret_cast<const uint32_t*>(ws + L.qpack), tab, sched + 2 * d.batch + 1, sms, scores,
                                                   L.ppad, status, s);
   if (e != cudaSuccess) return e;
   return d.cache_dtype == QSVD_BF16 ? fast_t<true, 1>(d, L, ws, prefix, nullptr, 1.f, sms, nullptr, status, s, scores)

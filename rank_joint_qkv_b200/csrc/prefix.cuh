@@ -18,7 +18,7 @@ struct PrefixLayout {
   int SP;           // token splits of the value product
   int G;            // CUDA cores: split CTAs
   int slots;        // partials (fast: SP x B; CUDA cores: G + B)
-  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, tab, scores, total;
+  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, tab, scores, qpack, total;
 };
 PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 

@@ -348,21 +348,23 @@ k_quant_query(const float* __restrict__ qt, int8_t* __restrict__ qp, float* __re
 
 // ---------------------------------------------------------------------------
 // Rotary query: q_h <- scale * R(before + len_b - 1) q_h, pairs (i, i + d_h/2),
-// with `before` rows of a shared prefix ahead of the sequence's own.
-// grid (B), block 256.
+// with `before` rows of a shared prefix ahead of the sequence's own; packed
+// too where pack is given (see launch_rope_query).
+// grid (B, ceil(H / 4)), block 256.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 k_rope_query(const float* __restrict__ q, const int32_t* __restrict__ sched,
-             const float* __restrict__ tab, int before, float scale, float* __restrict__ qrot, int B,
-             int H, int d_h, int E) {
+             const float* __restrict__ tab, int before, float scale, float* __restrict__ qrot,
+             uint32_t* __restrict__ pack, int B, int H, int d_h, int E) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   const int b = blockIdx.x;
   const int n = sched[B + 1 + b];
   const int pos = max(before + n - 1, 0);
   const int half = d_h / 2;
-  for (int i = threadIdx.x; i < H * half; i += blockDim.x) {
-    const int h = i / half, k = i % half;
+  const int h0 = 4 * blockIdx.y, hn = min(4, H - h0);
+  for (int i = threadIdx.x; i < hn * half; i += blockDim.x) {
+    const int h = h0 + i / half, k = i % half;
     const int e0 = h * d_h + k, e1 = e0 + half;
     const float a = q[size_t(b) * E + e0];
     const float c = q[size_t(b) * E + e1];
@@ -371,6 +373,27 @@ k_rope_query(const float* __restrict__ q, const int32_t* __restrict__ sched,
     qrot[size_t(b) * E + e0] = (a * cs - c * sn) * scale;
     qrot[size_t(b) * E + e1] = (c * cs + a * sn) * scale;
   }
+  if (!pack) return;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= hn) return;   // a warp a head, four elements a lane
+  const float2* src = reinterpret_cast<const float2*>(qrot + size_t(b) * E + (h0 + warp) * 128);
+  float2 v[2] = {src[lane], src[lane + 32]};
+  const float most = dev::warp_max(fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[1].x), fabsf(v[1].y))));
+  float inverse;
+  const float f = dev::f16_scale(most, &inverse);
+  uint32_t* dst = pack + (size_t(b) * H + h0 + warp) * kRopePackWords;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int p = lane + 32 * j;   // elements 2 p, 2 p + 1
+    float x = v[j].x * f, y = v[j].y * f;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int word = 16 * part + 2 * (p >> 3) + ((p >> 2) & 1);
+      dst[((word >> 2) * 4 + (p & 3)) * 4 + (word & 3)] = dev::f16_part(x, y);
+    }
+  }
+  if (lane == 0) dst[kRopePackScale] = __float_as_uint(inverse);
 }
 
 // ---------------------------------------------------------------------------
@@ -546,10 +569,10 @@ cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, 
 
 cudaError_t launch_rope_query(const qsvd_dims& d, const float* q, const int32_t* sched,
                               const float* rope_tab, float scale, float* qrot,
-                              cudaStream_t s, int before) {
+                              cudaStream_t s, int before, uint32_t* pack) {
   {
-    const cudaError_t le = launch_pdl(k_rope_query, dim3(d.batch), dim3(256), 0, s,
-                                     q, sched, rope_tab, before, scale, qrot, d.batch, d.H, d.d_h, d.E);
+    const cudaError_t le = launch_pdl(k_rope_query, dim3(d.batch, unsigned((d.H + 3) / 4)), dim3(256), 0, s,
+                                     q, sched, rope_tab, before, scale, qrot, pack, d.batch, d.H, d.d_h, d.E);
     if (le != cudaSuccess) return le;
   }
   note_launch();

@@ -1263,17 +1263,118 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
 // dot products.  Every wait is bounded as in k_split_tc.
 // ---------------------------------------------------------------------------
 constexpr int kRopeSlotBytes = kBoxBytes + 256 * 128;   // latent box + 256 rows of W^u_k^T
+template <bool SHARED> constexpr int kRopeThreads = SHARED ? 320 : 192;   // producer, MMA, 8 or 4 scoring warps
 constexpr int kRopeTabPitch = 65;                        // floats per token row (bank-conflict free)
+constexpr int kRopePairPitch = 144;                      // SHARED: (cos, sin) pairs, conflict-free as fragments
+
+// fp16 m16n8k16, d += a b.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 TMEM lanes x 64 float32 columns as eight m16n8 accumulator fragments:
+// v[4 i ..] = (row g, column 8 i + 2 c), (g, + 1), (g + 8, 8 i + 2 c), (g + 8,
+// + 1) with g = lane / 4, c = lane % 4.
+__device__ __forceinline__ void tmem_ld_frag64(uint32_t ta, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(ta));
+}
+
+// One warp: the keys of 16 tokens (TMEM lanes of ta, 128 columns) rotated and
+// scored against nq queries (qp + b E2: packed, see launch_rope_query); token
+// i's scores to out[b stride + i], i < live.  tab: the tokens' rows of (cos,
+// sin) pairs.
+// The products are fp16 MMAs on two parts of both operands (hi hi, hi lo, lo
+// hi), each key and each query scaled by a power of two (dev::f16_scale), so
+// that they stand for 22 bits of the row's largest element whatever float32's
+// range holds.  The keys come straight from TMEM in fragment order, and the
+// queries are packed in it: a block of eight queries is 8 loads and 24 MMAs.
+// What bounds it are these MMAs, which take the tensor cores' time from the
+// keys' own.  At B 16, 8192 rows, 32 heads, r 1536 103 us (B 1: 92);
+// three bf16 parts, 48 MMAs, took 115 (99), two tf32 parts, 48 of half the
+// length, 131 (108), and fma on CUDA cores, a key per thread, 186.
+__device__ __forceinline__ void score_keys(uint32_t ta, const float* tab, const uint32_t* __restrict__ qp, int E2, int nq,
+                                           float* __restrict__ out, size_t stride, int live, int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t kp[2][32];   // part, [2 i + (row g, g + 8)] of fragment i: 8 of the low half of the columns, 8 of the high
+  float unscale[2];
+  {
+    float k[64];
+    tmem_ld_frag64(ta, k);
+    tmem_ld_frag64(ta + 64, k + 32);
+    tmem_wait_ld();
+    float mx[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float4 w = *reinterpret_cast<const float4*>(tab + (g + 4 * (i & 2)) * kRopePairPitch + 16 * (i >> 2) + 4 * c);
+      const float l0 = k[i], l1 = k[i + 1], h0 = k[32 + i], h1 = k[33 + i];
+      k[i] = fmaf(l0, w.x, -h0 * w.y);
+      k[i + 1] = fmaf(l1, w.z, -h1 * w.w);
+      k[32 + i] = fmaf(h0, w.x, l0 * w.y);
+      k[33 + i] = fmaf(h1, w.z, l1 * w.w);
+      float& x = mx[(i >> 1) & 1];
+      x = fmaxf(fmaxf(fmaxf(x, fabsf(k[i])), fmaxf(fabsf(k[i + 1]), fabsf(k[32 + i]))), fabsf(k[33 + i]));
+    }
+    float scale[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {   // a row is four lanes'
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 1));
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 2));
+      scale[j] = dev::f16_scale(mx[j], &unscale[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+      const float f = scale[(i >> 1) & 1];
+      float x = k[i] * f, y = k[i + 1] * f;
+      kp[0][i / 2] = dev::f16_part(x, y);
+      kp[1][i / 2] = dev::f16_part(x, y);
+    }
+  }
+#pragma unroll 1
+  for (int n0 = 0; n0 < nq; n0 += 8) {
+    uint32_t x[32];   // [part][k step][2]
+    const uint4* src = reinterpret_cast<const uint4*>(qp + size_t(min(n0 + g, nq - 1)) * E2) + c;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) *reinterpret_cast<uint4*>(x + 4 * v) = __ldg(src + 4 * v);
+    float qs[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      qs[j] = __uint_as_float(__ldg(qp + size_t(min(n0 + 2 * c + j, nq - 1)) * E2 + kRopePackScale));
+    float d[2][3][4] = {};   // of each half of the columns: hi hi, hi lo, lo hi
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int st = 4 * half + s;
+        mma_f16(d[half][0], &kp[0][4 * st], x[2 * st], x[2 * st + 1]);
+        mma_f16(d[half][1], &kp[0][4 * st], x[16 + 2 * st], x[17 + 2 * st]);
+        mma_f16(d[half][2], &kp[1][4 * st], x[2 * st], x[2 * st + 1]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = n0 + 2 * c + (e & 1), i = g + 8 * (e >> 1);
+      if (n < nq && i < live)
+        out[size_t(n) * stride + i] = ((d[0][0][e] + d[1][0][e]) + ((d[0][1][e] + d[1][1][e]) + (d[0][2][e] + d[1][2][e]))) *
+                                      unscale[e >> 1] * qs[e & 1];
+    }
+  }
+}
 
 // SHARED: the rows are a prefix of all sequences (one tile range, B = 1 for it),
-// and every rebuilt key, held in registers, is dotted with the nq sequences'
-// queries: the rebuild, 2 r d_h flops a key, is done once for the batch, and
-// the dots (nq d_h fma a key on CUDA cores) stay under the next pair's MMAs up
-// to about 32 sequences at r 1536.
+// and every rebuilt key is scored against the nq sequences' queries: the
+// rebuild, 2 r d_h flops a key, is done once for the batch.
 template <bool BF16, bool SHARED>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kRopeThreads<SHARED>, 1)
 k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_w,
-              const float* __restrict__ qrot, const float* __restrict__ rope_tab,
+              const float* __restrict__ qrot, const uint32_t* __restrict__ qpack, const float* __restrict__ rope_tab,
               const int32_t* __restrict__ sched, float* __restrict__ scores, int32_t* __restrict__ status,
               int B, int H, int E, int r, int max_len, int G, int ns, int nq) {
   dev::pdl_wait();   // see launch_pdl
@@ -1284,7 +1385,7 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
   uint8_t* ring = base;
   float* tab_c = reinterpret_cast<float*>(ring + size_t(ns) * kRopeSlotBytes);   // [128][65] cos
   float* tab_s = tab_c + 128 * kRopeTabPitch;                                       // [128][65] sin
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tab_s + 128 * kRopeTabPitch);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tab_c + 128 * (SHARED ? kRopePairPitch : 2 * kRopeTabPitch));
   uint64_t* full = bars;                  // [kMaxSlots]
   uint64_t* empty = bars + kMaxSlots;     // [kMaxSlots]
   uint64_t* kfull = bars + 2 * kMaxSlots; // [2]
@@ -1405,7 +1506,9 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
     __syncwarp();
   } else {
     // ------------------------------------------------ rotation and scores
+    constexpr int kScoring = kRopeThreads<SHARED> - 64;
     const int q = warp & 3;
+    const int m = SHARED ? 16 * ((warp - 2) >> 2) : 0;   // SHARED: 16 of the quarter's rows to a warp
     const int t = 32 * q + lane;              // token row in the tile == TMEM lane
     const uint32_t lane_off = uint32_t(32 * q) << 16;
     float* tc = tab_c + t * kRopeTabPitch;    // this token's cos / sin row (private)
@@ -1415,7 +1518,17 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
     long long pc = 0;
     for (int i = 0; i < n; ++i) {
       const int nv = it.nvalid(), b = it.b, t0 = it.t0();
-      if (t < nv) {   // the row of position t0 + t: 64 (cos, sin) pairs
+      if constexpr (SHARED) {   // a row an instruction
+        const int row0 = 32 * q + m;
+        float4 x[16];   // all in flight (rows past the prefix repeat its last)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[i] = __ldg(reinterpret_cast<const float4*>(rope_tab + size_t(t0 + min(row0 + i, nv - 1)) * 128) + lane);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float4*>(tab_c + (row0 + i) * kRopePairPitch + 4 * lane) = x[i];
+        __syncwarp();   // read by all lanes
+      } else if (t < nv) {   // the row of position t0 + t: 64 (cos, sin) pairs
         const float4* src = reinterpret_cast<const float4*>(rope_tab + size_t(t0 + t) * 128);
 #pragma unroll 8
         for (int v = 0; v < 32; ++v) {
@@ -1427,7 +1540,7 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
       int fail = 0;
       for (int p = pair_lo(i); p < pair_hi(i); ++p, ++pc) {
         const int kb = int(pc & 1);
-        fail = group_or(!mbar_wait(saddr(&kfull[kb]), uint32_t(pc >> 1) & 1u));   // uniform
+        fail = bar_or(!mbar_wait(saddr(&kfull[kb]), uint32_t(pc >> 1) & 1u), 1, kScoring);   // uniform
         if (fail) break;
         tc_fence_after();
 #pragma unroll 1
@@ -1437,33 +1550,9 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
           const float* qh = qb + h * 128;
           const uint32_t ta = tmem + lane_off + uint32_t(kb * 256 + hh * 128);
           if constexpr (SHARED) {
-            float key[128];   // rotated: element j, then 64 + j
-#pragma unroll
-            for (int i0 = 0; i0 < 64; i0 += 16) {
-              float klo[16], khi[16];
-              tmem_ld16(ta + uint32_t(i0), klo);
-              tmem_ld16(ta + uint32_t(64 + i0), khi);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float c = tc[i0 + e], sn = ts[i0 + e];
-                key[i0 + e] = fmaf(klo[e], c, -khi[e] * sn);
-                key[64 + i0 + e] = fmaf(khi[e], c, klo[e] * sn);
-              }
-            }
-            for (int b1 = 0; b1 < nq; ++b1) {   // the query's loads are one address for the warp
-              const float4* q4 = reinterpret_cast<const float4*>(qrot + size_t(b1) * E + h * 128);
-              float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-              for (int v = 0; v < 32; ++v) {
-                const float4 x = __ldg(q4 + v);
-                s0 = fmaf(x.x, key[4 * v], s0);
-                s1 = fmaf(x.y, key[4 * v + 1], s1);
-                s2 = fmaf(x.z, key[4 * v + 2], s2);
-                s3 = fmaf(x.w, key[4 * v + 3], s3);
-              }
-              if (t < nv) scores[(size_t(b1) * H + h) * max_len + t0 + t] = (s0 + s1) + (s2 + s3);
-            }
+            const int row = 32 * q + m;
+            score_keys(ta + (uint32_t(m) << 16), tab_c + row * kRopePairPitch, qpack + size_t(h) * kRopePackWords, H * kRopePackWords, nq,
+                       scores + size_t(h) * max_len + t0 + row, size_t(H) * max_len, nv - row, lane);
             continue;
           }
           float s = 0.f;
@@ -1484,15 +1573,15 @@ k_rope_scores(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ 
           if (t < nv) scores[(size_t(b) * H + h) * max_len + t0 + t] = s;
         }
         tc_fence_before();
-        group_sync();
-        if (t == 0) mbar_arrive(saddr(&kempty[kb]));
+        bar_sync(1, kScoring);
+        if (t == 0 && m == 0) mbar_arrive(saddr(&kempty[kb]));
       }
       if (fail) {
-        if (t == 0) { *abort_flag = 1; atomicOr(status, QSVD_STATUS_TIMEOUT); }
+        if (t == 0 && m == 0) { *abort_flag = 1; atomicOr(status, QSVD_STATUS_TIMEOUT); }
         break;
       }
       it.next();
-      if (group_or(*abort_flag)) break;
+      if (bar_or(*abort_flag, 1, kScoring)) break;
     }
   }
   tc_fence_before();
@@ -1656,9 +1745,9 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
   return check_launch();
 }
 
-// rows: of the latent in all; SHARED: scores of stride `stride` per (sequence, head).
+// rows: of the latent in all; q: the rotated query, SHARED: its packed parts; SHARED: scores of stride `stride` per (sequence, head).
 template <bool BF16, bool SHARED>
-cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, size_t rows, const void* wukT, const float* qrot,
+cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, size_t rows, const void* wukT, const void* q,
                           const float* rope_tab, const int32_t* sched, int G, float* scores, int stride,
                           int32_t* status, cudaStream_t s) {
   TensorMapEncode enc = tensor_map_encoder();
@@ -1687,14 +1776,15 @@ cudaError_t rope_scores_t(const qsvd_dims& d, const void* cache, size_t rows, co
       return cudaErrorInvalidValue;
   }
   constexpr int ns = 3;
-  const size_t smem = 1024 + size_t(ns) * kRopeSlotBytes + 2 * 128 * kRopeTabPitch * 4 +
+  const size_t smem = 1024 + size_t(ns) * kRopeSlotBytes + 128 * (SHARED ? kRopePairPitch : 2 * kRopeTabPitch) * 4 +
                       (2 * kMaxSlots + 5) * 8 + 16;
   auto kern = k_rope_scores<BF16, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   {
-    const cudaError_t le = launch_pdl(kern, dim3(G), dim3(192), smem, s,
-                                     tc, tw, qrot, rope_tab, sched, scores, status, SHARED ? 1 : d.batch, d.H, d.E, d.r, SHARED ? stride : d.max_len, G, ns, d.batch);
+    const cudaError_t le = launch_pdl(kern, dim3(G), dim3(kRopeThreads<SHARED>), smem, s,
+                                     tc, tw, SHARED ? nullptr : static_cast<const float*>(q), SHARED ? static_cast<const uint32_t*>(q) : nullptr,
+                                     rope_tab, sched, scores, status, SHARED ? 1 : d.batch, d.H, d.E, d.r, SHARED ? stride : d.max_len, G, ns, d.batch);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -1796,11 +1886,11 @@ cudaError_t launch_rope_scores(const qsvd_dims& d, const void* cache, const void
 }
 
 cudaError_t launch_rope_scores_shared(const qsvd_dims& d, const void* prefix, int plen, const void* wukT,
-                                      const float* qrot, const float* rope_tab, const int32_t* sched1, int G,
+                                      const uint32_t* qpack, const float* rope_tab, const int32_t* sched1, int G,
                                       float* scores, int stride, int32_t* status, cudaStream_t s) {
   return d.cache_dtype == QSVD_BF16
-             ? rope_scores_t<true, true>(d, prefix, size_t(plen), wukT, qrot, rope_tab, sched1, G, scores, stride, status, s)
-             : rope_scores_t<false, true>(d, prefix, size_t(plen), wukT, qrot, rope_tab, sched1, G, scores, stride, status, s);
+             ? rope_scores_t<true, true>(d, prefix, size_t(plen), wukT, qpack, rope_tab, sched1, G, scores, stride, status, s)
+             : rope_scores_t<false, true>(d, prefix, size_t(plen), wukT, qpack, rope_tab, sched1, G, scores, stride, status, s);
 }
 
 }  // namespace qsvd

@@ -130,6 +130,23 @@ def test_tile_references_that_differ(cuda_ok, cache, rise):
     close_weights(w, want_w, 3 * bound, m.lens)
 
 
+@pytest.mark.parametrize("cache", ["f16", "bf16"])
+def test_rotary_rows_of_very_different_size(cuda_ok, cache):
+    """Zero rows, rows 2^-12 and 8 times the usual (scores up to eight times the peak), a zero query, one 64 times the usual
+    (one row takes all the weight)."""
+    m = Layer(cache=cache, weight=cache, prefix=700, lens=(30, 0, 5), H=4, d_h=128, r=256, peak=0.5, rope=True)
+    size = torch.tensor([0.0, 2.0 ** -12, 1.0, 8.0], device=DEV).repeat(175)[:, None]
+    m.prefix = (m.prefix.float() * size).to(TORCH[cache])
+    m.prefix_values = m.prefix.double()
+    m.qin[0] = 0
+    m.qin[2] *= 64
+    want, want_w, bound = m.exact()
+    w = torch.zeros(m.B, m.max_len, device=DEV)
+    out = run(m, weights=w)
+    close_out(m, out, want)
+    close_weights(w, want_w, 3 * bound, m.lens)
+
+
 @pytest.mark.parametrize("form", [dict(H=8, r=256), dict(H=4, d_h=128, r=256, rope=True)], ids=["absorbed", "rope"])
 def test_same_as_a_decode_over_the_whole_rows(cuda_ok, form):
     """The prefix copied in front of every sequence's rows gives the plain decode's output."""

@@ -147,7 +147,10 @@ def test_rotary_rows_of_very_different_size(cuda_ok, cache):
     close_weights(w, want_w, 3 * bound, m.lens)
 
 
-@pytest.mark.parametrize("form", [dict(H=8, r=256), dict(H=4, d_h=128, r=256, rope=True)], ids=["absorbed", "rope"])
+FORMS = [dict(H=8, r=256), dict(H=4, d_h=128, r=256, rope=True)]
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["absorbed", "rope"])
 def test_same_as_a_decode_over_the_whole_rows(cuda_ok, form):
     """The prefix copied in front of every sequence's rows gives the plain decode's output."""
     m = Layer(prefix=600, lens=(40, 0, 333), **form)
@@ -191,9 +194,10 @@ def test_a_strided_view_of_a_longer_prefix(cuda_ok):
     assert torch.equal(run(m), out)
 
 
-def test_graph_replay_on_a_side_stream(cuda_ok):
+@pytest.mark.parametrize("form", FORMS, ids=["absorbed", "rope"])
+def test_graph_replay_on_a_side_stream(cuda_ok, form):
     """Two graphs with workspaces of their own, replayed in turn with new queries and lengths."""
-    m = Layer(prefix=700, lens=(40, 3, 200), H=8, r=256)
+    m = Layer(prefix=700, lens=(40, 3, 200), **form)
     side, graphs = torch.cuda.Stream(), []
     for _ in range(2):
         out, w = m.empty_out(), torch.zeros(m.B, m.max_len, device=DEV)
@@ -271,9 +275,10 @@ def test_empty_everything_gives_zero_rows(cuda_ok):
     assert bool((run(m)[0] == 0).all())
 
 
-def test_two_calls_at_once(cuda_ok):
+@pytest.mark.parametrize("form", FORMS, ids=["absorbed", "rope"])
+def test_two_calls_at_once(cuda_ok, form):
     """Two batches on two streams with workspaces of their own, over one prefix, many times over."""
-    a, b = (Layer(prefix=1200, lens=lens, H=8, r=256, seed=5) for lens in ((300, 0, 77), (10, 900, 128)))
+    a, b = (Layer(prefix=1200, lens=lens, max_len=1000, seed=5, **form) for lens in ((300, 0, 77), (10, 900, 128)))
     b.prefix, b.prefix_values, b.packed = a.prefix, a.prefix_values, a.packed
     b.wuq, b.wuk, b.wuv = a.wuq, a.wuk, a.wuv
     want = [run(m) for m in (a, b)]
@@ -291,9 +296,25 @@ def test_two_calls_at_once(cuda_ok):
             assert torch.equal(x, w)
 
 
-def test_the_query_as_given(cuda_ok):
+@pytest.mark.parametrize("form", FORMS, ids=["absorbed", "rope"])
+def test_one_workspace_for_prefixes_that_grow_and_shrink(cuda_ok, form):
+    """Calls in a row without a wait between them, each laying its workspace out for its own prefix."""
+    layers = [Layer(prefix=p, lens=(30, 0, 129), **form) for p in (900, 40, 0, 513)]
+    outs = [m.empty_out() for m in layers]
+    ws = torch.empty(max(q.decode_shared_workspace_bytes(m.dims, 900) for m in layers), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for m, out in zip(layers, outs):
+        q.qsvd_decode_attn_shared(m.dims, m.packed, m.qin, True, m.prefix, None, m.prefix_values.shape[0], m.cache, None,
+                                  m.lengths, out, workspace=ws)
+    torch.cuda.synchronize()
+    for m, out in zip(layers, outs):
+        close_out(m, out, m.exact()[0])
+
+
+@pytest.mark.parametrize("form", [dict(H=8), dict(d_h=128, rope=True)], ids=["absorbed", "rope"])
+def test_the_query_as_given(cuda_ok, form):
     """qin as the B x E query itself instead of the token's latent."""
-    m = Layer(prefix=300, lens=(20, 0, 129), H=8)
+    m = Layer(prefix=300, lens=(20, 0, 129), **form)
     query = m.qin.double() @ m.wuq.double()
     out = m.empty_out()
     q.qsvd_decode_attn_shared(m.dims, m.packed, query.float().contiguous(), False, m.prefix, None, 300, m.cache, None,

@@ -507,7 +507,10 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
  * of tensor-core products over all B H query rows.  Serving decode; the pages
  * have no counterpart.
  *   dims           as in qsvd_decode_attn; max_len is the capacity of the own
- *                  caches.  Absorbed mode only (dims->rope: UNSUPPORTED).
+ *                  caches.  With dims->rope the prefix's rows are at positions
+ *                  0 .. prefix_len - 1, the own rows and the query behind them;
+ *                  the table of all of them is built in the workspace by every
+ *                  call, and max_len + prefix_len must be below 2^31.
  *   prefix, prefix_scales  device, prefix_len rows (and group scales) as in
  *                  qsvd_append_latent's cache, 16-byte (2-byte) aligned; not
  *                  read when prefix_len is 0.
@@ -525,7 +528,8 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
  *                  dims->out_proj).
  * The prefix runs on the tensor cores for F16, BF16, I8 and I4 caches with
  * r % 64 == 0, H <= 128 and dims->kernel other than SIMT, and on the CUDA cores
- * otherwise.  A quantised prefix is expanded to fp16 parts in the workspace,
+ * otherwise; with dims->rope for cache and weights both F16 or both BF16 with
+ * d_h == 128 besides.  A quantised prefix is expanded to fp16 parts in the workspace,
  * so code x scale and the absorbed query must lie within fp16's range.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  */

@@ -360,7 +360,8 @@ def qsvd_decode_attn_shared(dims: qsvd_dims, packed, qin, qin_is_latent, prefix,
     """Decode step of a batch over ``prefix_len`` shared latent rows
     (``prefix``, ``prefix_scales``) and each sequence's own rows.  ``weights``:
     optional B x max_len float32, the own rows' attention weights as in
-    qsvd_decode_attn_weights.  Returns the workspace."""
+    qsvd_decode_attn_weights.  In rotary mode the own rows' positions follow
+    the prefix's.  Returns the workspace."""
     if workspace is None:
         workspace = _scratch(decode_shared_workspace_bytes(dims, prefix_len, num_splits), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())

@@ -1,4 +1,5 @@
 // C-ABI layer: argument validation, layouts, phase dispatch.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cmath>
@@ -156,17 +157,28 @@ static float score_scale_log2(const qsvd_dims& d) {
 }
 
 // The tensor cores add into their float32 accumulator by truncation: each of
-// a score's `steps` accumulations loses half a unit in the last place on
+// a sum's `steps` accumulations loses half a unit in the last place on
 // average, 0.5 x 2^-23 of a mantissa that averages 1 / 0.72, while the partial
-// sum is on average 0.7 to 0.8 of the final one -- about 2^-25 of the score a
-// step.  Scores come out short by that factor (measured: 2.7e-6 at r 1536,
-// where 96 x 2^-25 = 2.9e-6), a slightly higher softmax temperature that 16-bit
-// outputs do not show but float32 attention weights do (1e-5 of a weight);
-// the query is scaled up by it where weights are asked for.
-static double score_gain(double steps) { return 1.0 + steps / 33554432.0; }
+// sum is on average 0.6 to 0.8 of the final one -- about 0.9 x 2^-25 of the sum a
+// step on tcgen05 and 0.7 x 2^-25 in the projections' chains of mma.sync.
+// Scores come out short by the sum of these, a slightly higher softmax
+// temperature that 16-bit outputs do not show but float32 attention weights do;
+// the query is scaled up by it where weights are asked for.  Measured as the
+// slope of the weights' log error over their log, one head, 2500 and 3000 rows:
+// without it -3.3e-6 at fp16, r 1536 (96 steps, and 16 of each projection);
+// with the scores' steps alone at 2^-25, -2e-7 to -7e-7 (int8 rows, whose sums
+// are exact: -7e-7, the projections' share).
+static double score_gain(double steps) { return 1.0 + 0.9 * steps / 33554432.0; }
 static double split_score_gain(const qsvd_dims& d, int kernel) {
   if (kernel == QSVD_KERNEL_SIMT || cache_is_int(d)) return 1.0;   // quantised: integer sums, exact
   return score_gain(kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) / 16.0 : d.r / 16.0);
+}
+static double projection_gain(const qsvd_dims& d, int qin_is_latent) {
+  if (d.weight_dtype == QSVD_F32) return 1.0;   // CUDA cores, rounded sums
+  double steps = 0.0;   // of 16, on two parts of the activation (a third one of bf16's adds next to nothing)
+  if (qin_is_latent) steps += (std::min(32, (d.r + 15) / 16) + 3) / 4;   // 512 rows over four warps
+  if (!d.rope && d.d_h % 64 == 0 && d.d_h <= 256) steps += d.d_h / 16;
+  return 1.0 + 0.7 * 2 * steps / 33554432.0;
 }
 
 }  // namespace qsvd
@@ -438,7 +450,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   const float* rope_tab = px && d.rope ? reinterpret_cast<const float*>(Wb + X.tab) : reinterpret_cast<const float*>(P + L.rope);
   const float* own_tab = rope_tab + (px && d.rope ? size_t(x.prefix_len) * d.d_h : 0);
   const double gain = x.on ? split_score_gain(d, kernel) : 1.0;
-  const float sl2 = float(double(score_scale_log2(d)) * gain);
+  const float sl2 = float(double(score_scale_log2(d)) * gain *
+                          (x.on ? projection_gain(d, qin_is_latent) : 1.0));
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
   void* px16 = cache_is_int(d) ? static_cast<void*>(Wb + X.qt16) : qt16;   // the prefix's 16-bit query parts

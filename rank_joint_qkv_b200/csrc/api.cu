@@ -454,6 +454,14 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
                           (x.on ? projection_gain(d, qin_is_latent) : 1.0));
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
+  const bool third = x.weights != nullptr;   // see launch_absorb
+  // parts of the absorbed query: a third one of bf16's where float32 weights
+  // are asked for (two carry 16 bits: weights off by 2e-6 to 6e-6 of
+  // themselves, with three by 1e-6 or so).  What it costs, r 1536, 32 heads:
+  // nothing on the own rows (B 16, 8192 of them: 178 and 179 us), on a prefix
+  // half of the scores' products again (B 16, 8192 + 512 rows: 116 -> 138 us;
+  // B 64, 16,384 + 512: 424 -> 484).
+  const int qparts = third && d.cache_dtype == QSVD_BF16 && kernel != QSVD_KERNEL_TCGEN05_CLUSTER ? 3 : 2;
   void* px16 = cache_is_int(d) ? static_cast<void*>(Wb + X.qt16) : qt16;   // the prefix's 16-bit query parts
   cudaError_t e;
 
@@ -465,7 +473,6 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
         (e = launch_prefix_schedule(d, X, Wb, s)) != cudaSuccess)
       return cuda_fail(e, "prefix schedule");
     if (px && d.rope && (e = launch_prefix_table(d, X, Wb, s)) != cudaSuccess) return cuda_fail(e, "rotary table");
-    const bool third = x.weights != nullptr;   // see launch_absorb
     // q = c_new W^u_q (reduced into the workspace), or the query as given
     const float* qsrc = qin;
     if (qin_is_latent) {
@@ -486,7 +493,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       const bool codes = kernel != QSVD_KERNEL_SIMT && cache_is_int(d);
       const bool need32 = kernel == QSVD_KERNEL_SIMT || codes || (px && !X.fast);
       void* parts = (kernel != QSVD_KERNEL_SIMT && !codes) || (px && X.fast) ? (px && cache_is_int(d) ? px16 : qt16) : nullptr;
-      e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s, third);
+      e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s, third, qparts);
       if (e == cudaSuccess && codes)
         e = launch_quant_query(d, qt32, static_cast<int8_t*>(qt16), quant_query_scales(d, qt16), s);
     }
@@ -519,8 +526,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
     if (px) {
       e = d.rope ? launch_prefix_rope(d, X, Wb, x.prefix, x.prefix_scales, P + L.wuk, P + L.wukT, qt32, sms,
                                       &hdr->status, s)
-                 : launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qt32,
-                                 float(score_gain(prefix_score_steps(d)) / gain), sms,
+                 : launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qparts, qt32,
+                                 float(score_gain(prefix_score_steps(d, qparts)) / gain), sms,
                                  reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);
       if (e != cudaSuccess) return cuda_fail(e, "prefix");
     }

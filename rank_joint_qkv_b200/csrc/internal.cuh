@@ -139,7 +139,8 @@ inline WsLayout ws_layout(const qsvd_dims& d, int G, bool keep_scores = false) {
   w.tickets = o; o = align256(o + size_t(w.NT + 1) * 4);   // and one counter (the shared prefix's score units)
   w.q = o;     o = align256(o + B * E * 4);
   w.qt32 = o;  o = align256(o + (H * r > E ? H * r : E) * B * 4);   // rotary mode: B x E query
-  w.qt16 = o;  o = align256(o + 2 * B * H * r * 2);   // [B][2][H][r] for bf16 hi/lo
+  // [B][2][H][r] parts; three of bf16's where weights may be asked for
+  w.qt16 = o;  o = align256(o + (keep_scores && d.cache_dtype == QSVD_BF16 ? 3 : 2) * B * H * r * 2);
   w.qpart = o; o = align256(o + size_t(w.KS) * B * E * 4);
   w.pm = o;    o = align256(o + size_t(w.P) * H * 4);
   w.pl = o;    o = align256(o + size_t(w.P) * H * 4);
@@ -213,7 +214,7 @@ cudaError_t launch_q_partial(const qsvd_dims& d, const float* qin, const void* w
 // qt32 (fp32, for the CUDA-core split) and qt16 ([B][2][H][r] hi/lo, for the
 // tensor cores) are each written only when non-null.
 cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, float scale_log2,
-                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third = false);
+                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third = false, int qparts = 2);
 // Quantised latent on the tensor cores: qt32 [B][H][r] -> three int8 parts
 // qp [B][3][H][r] and one power-of-two scale qs [B][H] per (sequence, head).
 cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s);

@@ -27,8 +27,9 @@
 // bound, lies in the middle of 256 scores' usual maxima); where it does, the
 // factor is a power of two and the only loss is a fp16 subnormal's.
 //
-// Precision as in the split kernels: the query as two 16-bit parts (both
-// products accumulate in float32), P as two for bf16; a quantised prefix is
+// Precision as in the split kernels: the query as two 16-bit parts (three of
+// bf16's where weights are asked for; the products accumulate in float32), P as
+// two for bf16; a quantised prefix is
 // expanded to the fp16 hi and lo parts of code x scale (18 bits: exact), each
 // a pass of both products, so that the scores are as good as the integer ones
 // of the sequences' own rows.
@@ -817,16 +818,16 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensor
 // C parts: CP copies of [plen][r] 16-bit rows at `c`, one after another.
 // given: the scores are in memory already (rotary mode).
 template <bool BF16, int CP>
-cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* c, const void* qt16, float gain,
-                   int sms, int32_t* counter, int32_t* status, cudaStream_t s, const float* given = nullptr) {
+cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* c, const void* qt16, int qparts,
+                   float gain, int sms, int32_t* counter, int32_t* status, cudaStream_t s, const float* given = nullptr) {
   constexpr int PS = BF16 ? 2 : 1;
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const cuuint64_t r = cuuint64_t(d.r), P = cuuint64_t(L.plen), rows = cuuint64_t(L.MB) * 128, ppad = cuuint64_t(L.ppad);
   CUtensorMap tq, tp, tbs[2], tbv[2];
   if (!given) {
-    // query parts [B][2][H][r] as {channel, head, part, sequence}: one box is a block's rows of one part
-    const cuuint64_t dims[4] = {r, cuuint64_t(d.H), 2, cuuint64_t(d.batch)};
-    const cuuint64_t strides[3] = {r * 2, cuuint64_t(d.H) * r * 2, 2 * cuuint64_t(d.H) * r * 2};
+    // query parts [B][qparts][H][r] as {channel, head, part, sequence}: one box is a block's rows of one part
+    const cuuint64_t dims[4] = {r, cuuint64_t(d.H), cuuint64_t(qparts), cuuint64_t(d.batch)};
+    const cuuint64_t strides[3] = {r * 2, cuuint64_t(d.H) * r * 2, cuuint64_t(qparts) * cuuint64_t(d.H) * r * 2};
     const cuuint32_t box[4] = {64, cuuint32_t(d.H), 1, cuuint32_t(L.nb)};
     if (!encode(&tq, BF16, 4, qt16, dims, strides, box)) return cudaErrorInvalidValue;
   }
@@ -859,7 +860,10 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
                    L.plen, L.tiles, L.ppad, own);
     if (e == cudaSuccess) { note_launch(); e = check_launch(); }
   } else {
-    e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
+    bool done = false;
+    if constexpr (BF16)   // (only bf16 comes in three parts)
+      if ((done = qparts == 3)) e = gemm_t<BF16, 3, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
+    if (!done) e = gemm_t<BF16, 2, CP, PS, false>(tq, tbs[0], tbs[1], g, L.pair, sms, s);
   }
   if (e != cudaSuccess) return e;
   if (L.tiles != L.SP) {
@@ -942,7 +946,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
 }
 
 cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                          const void* scales, const void* qt16, const float* qt32, float gain, int sms,
+                          const void* scales, const void* qt16, int qparts, const float* qt32, float gain, int sms,
                           int32_t* counter, int32_t* status,
                           cudaStream_t s) {
   if (!L.fast) {
@@ -954,9 +958,9 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
                                       reinterpret_cast<float*>(ws + L.pm), reinterpret_cast<float*>(ws + L.pl),
                                       reinterpret_cast<float*>(ws + L.pz), s);
   }
-  if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
-  if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, gain, sms, counter, status, s);
-  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, gain, sms, counter, status, s);
+  if (d.cache_dtype == QSVD_BF16) return fast_t<true, 1>(d, L, ws, prefix, qt16, qparts, gain, sms, counter, status, s);
+  if (d.cache_dtype == QSVD_F16) return fast_t<false, 1>(d, L, ws, prefix, qt16, qparts, gain, sms, counter, status, s);
+  return fast_t<false, 2>(d, L, ws, ws + L.cparts, qt16, qparts, gain, sms, counter, status, s);
 }
 
 cudaError_t launch_prefix_table(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s) {
@@ -978,8 +982,8 @@ cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_
   const cudaError_t e = launch_rope_scores_shared(d, prefix, L.plen, wukT, reinterpret_cast<const uint32_t*>(ws + L.qpack), tab, sched + 2 * d.batch + 1, sms, scores,
                                                   L.ppad, status, s);
   if (e != cudaSuccess) return e;
-  return d.cache_dtype == QSVD_BF16 ? fast_t<true, 1>(d, L, ws, prefix, nullptr, 1.f, sms, nullptr, status, s, scores)
-                                    : fast_t<false, 1>(d, L, ws, prefix, nullptr, 1.f, sms, nullptr, status, s, scores);
+  return d.cache_dtype == QSVD_BF16 ? fast_t<true, 1>(d, L, ws, prefix, nullptr, 2, 1.f, sms, nullptr, status, s, scores)
+                                    : fast_t<false, 1>(d, L, ws, prefix, nullptr, 2, 1.f, sms, nullptr, status, s, scores);
 }
 
 cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
@@ -995,7 +999,7 @@ cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint
   return check_launch();
 }
 
-int prefix_score_steps(const qsvd_dims& d) { return d.r / 16 * (cache_is_int(d) ? 3 : 2); }
+int prefix_score_steps(const qsvd_dims& d, int qparts) { return d.r / 16 * (cache_is_int(d) ? 3 : qparts); }
 
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s) {
   cudaError_t e = launch_pdl(k_prefix_schedule, dim3(1), dim3(256), 0, s, reinterpret_cast<int32_t*>(ws + L.sched),

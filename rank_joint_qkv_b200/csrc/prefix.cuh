@@ -23,7 +23,7 @@ struct PrefixLayout {
 PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 
 // The prefix's partials (m, l, z per slot) from the absorbed query: qt16 its
-// 16-bit parts [B][2][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
+// 16-bit parts [B][qparts][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
 // the tensor cores' scores, for what their accumulation truncates.  counter:
 // one word, zero.
 // launch_prefix_expand goes before the own rows' split kernel and
@@ -31,7 +31,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
                                  const void* scales, cudaStream_t s);
 cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                          const void* scales, const void* qt16, const float* qt32, float gain, int sms,
+                          const void* scales, const void* qt16, int qparts, const float* qt32, float gain, int sms,
                           int32_t* counter, int32_t* status,
                           cudaStream_t s);
 // Rotary mode: the table of all positions, prefix then own rows (tab, built
@@ -43,7 +43,7 @@ cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_
                                int32_t* status, cudaStream_t s);
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
 // Accumulations that a score of the tensor-core path takes.
-int prefix_score_steps(const qsvd_dims& d);
+int prefix_score_steps(const qsvd_dims& d, int qparts);
 // Merge of the own splits' and the prefix's partials: zm [B][H][r], or (slots
 // != 0) one slot per sequence for launch_combine; ml {M, 1 / L} [B][H].
 cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr, int G,

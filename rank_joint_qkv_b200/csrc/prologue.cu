@@ -26,7 +26,7 @@ using dev::to_f;
 template <typename WT, typename QT16>
 __global__ void __launch_bounds__(128)
 k_absorb(const float* __restrict__ q, const WT* __restrict__ W, float scale,
-         float* __restrict__ qt32, QT16* __restrict__ qt16, int B, int H, int d_h, int r,
+         float* __restrict__ qt32, QT16* __restrict__ qt16, int qparts, int B, int H, int d_h, int r,
          int E) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
@@ -99,13 +99,15 @@ k_absorb(const float* __restrict__ q, const WT* __restrict__ W, float scale,
           const size_t o = (size_t(b) * H + h) * r + j;
           if (qt32) qt32[o] = v;
           if (qt16) {
-            // 16-bit copy for the tensor cores, [B][2][H][r]: the rounded value
+            // 16-bit copy for the tensor cores, [B][qparts][H][r]: the rounded value
             // and its rounding residual (hi + lo carries ~2x the mantissa bits;
-            // one 16-bit part alone perturbs peaked softmaxes by ~1e-2)
-            const QT16 hi = dev::from_f<QT16>(v);
-            const size_t o2 = ((size_t(b) * 2) * H + h) * r + j;
+            // one 16-bit part alone perturbs peaked softmaxes by ~1e-2), and
+            // of three parts what these leave
+            const QT16 hi = dev::from_f<QT16>(v), lo = dev::from_f<QT16>(v - dev::to_f(hi));
+            const size_t o2 = ((size_t(b) * qparts) * H + h) * r + j;
             qt16[o2] = hi;
-            qt16[o2 + size_t(H) * r] = dev::from_f<QT16>(v - dev::to_f(hi));
+            qt16[o2 + size_t(H) * r] = lo;
+            if (qparts == 3) qt16[o2 + 2 * size_t(H) * r] = dev::from_f<QT16>(v - dev::to_f(hi) - dev::to_f(lo));
           }
         }
       }
@@ -127,7 +129,7 @@ k_absorb(const float* __restrict__ q, const WT* __restrict__ W, float scale,
 template <typename WT, typename QT16, bool THIRD>
 __global__ void __launch_bounds__(128)
 k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__ q, float scale,
-             float* __restrict__ qt32, QT16* __restrict__ qt16, int B, int H, int d_h, int r, int E,
+             float* __restrict__ qt32, QT16* __restrict__ qt16, int qparts, int B, int H, int d_h, int r, int E,
              int32_t* status) {
   using namespace gemv_mma;
   constexpr bool BF16 = std::is_same<WT, __nv_bfloat16>::value;
@@ -289,14 +291,19 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
         const size_t o = (size_t(b) * H + h) * r + j0 + jl;
         if (qt32) *reinterpret_cast<float2*>(qt32 + o) = make_float2(v0, v1);
         if (!qt16) continue;
-        // 16-bit copy for the tensor cores, [B][2][H][r]: the rounded value
-        // and its rounding residual
+        // 16-bit copy for the tensor cores, [B][qparts][H][r]: the rounded value,
+        // its rounding residual and, of three parts, what these leave
         const QT16 h0 = dev::from_f<QT16>(v0), h1 = dev::from_f<QT16>(v1);
         const QT16 l0 = dev::from_f<QT16>(v0 - dev::to_f(h0)), l1 = dev::from_f<QT16>(v1 - dev::to_f(h1));
-        const size_t o2 = ((size_t(b) * 2) * H + h) * r + j0 + jl;
+        const size_t o2 = ((size_t(b) * qparts) * H + h) * r + j0 + jl;
         QT16 hv[2] = {h0, h1}, lv[2] = {l0, l1};
         *reinterpret_cast<uint32_t*>(qt16 + o2) = *reinterpret_cast<const uint32_t*>(hv);
         *reinterpret_cast<uint32_t*>(qt16 + o2 + size_t(H) * r) = *reinterpret_cast<const uint32_t*>(lv);
+        if (qparts == 3) {
+          const QT16 rv[2] = {dev::from_f<QT16>(v0 - dev::to_f(h0) - dev::to_f(l0)),
+                              dev::from_f<QT16>(v1 - dev::to_f(h1) - dev::to_f(l1))};
+          *reinterpret_cast<uint32_t*>(qt16 + o2 + 2 * size_t(H) * r) = *reinterpret_cast<const uint32_t*>(rv);
+        }
       }
     }
     __syncthreads();   // xs is restaged for the next 16 sequences
@@ -465,7 +472,7 @@ cudaError_t q_partial_t(const qsvd_dims& d, const float* qin, const void* wuq, f
 
 template <typename WT, typename QT16>
 cudaError_t absorb_t(const qsvd_dims& d, const float* q, const void* wuk, float scale,
-                     float* qt32, void* qt16, int32_t* status, bool third, cudaStream_t s) {
+                     float* qt32, void* qt16, int qparts, int32_t* status, bool third, cudaStream_t s) {
   if constexpr (sizeof(WT) == 2) {
     if (d.d_h % 64 == 0 && d.d_h <= 256) {
       TensorMapEncode enc = tensor_map_encoder();
@@ -490,7 +497,7 @@ cudaError_t absorb_t(const qsvd_dims& d, const float* q, const void* wuk, float 
       dim3 grid(d.H, (d.r + 127) / 128);
       {
         const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(128), smem, s,
-                                         tm, q, scale, qt32, static_cast<QT16*>(qt16), d.batch, d.H, d.d_h, d.r, d.E, status);
+                                         tm, q, scale, qt32, static_cast<QT16*>(qt16), qparts, d.batch, d.H, d.d_h, d.r, d.E, status);
         if (le != cudaSuccess) return le;
       }
       note_launch();
@@ -504,7 +511,7 @@ cudaError_t absorb_t(const qsvd_dims& d, const float* q, const void* wuk, float 
   dim3 grid(d.H, (d.r + 127) / 128);
   {
     const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(128), smem, s,
-                                     q, static_cast<const WT*>(wuk), scale, qt32, static_cast<QT16*>(qt16), d.batch, d.H, d.d_h, d.r, d.E);
+                                     q, static_cast<const WT*>(wuk), scale, qt32, static_cast<QT16*>(qt16), qparts, d.batch, d.H, d.d_h, d.r, d.E);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -542,18 +549,18 @@ cudaError_t launch_q_partial(const qsvd_dims& d, const float* qin, const void* w
 }
 
 cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, float scale,
-                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third) {
+                          float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third, int qparts) {
   const bool bf = d.cache_dtype == QSVD_BF16;
   switch (d.weight_dtype) {
     case QSVD_F32:
-      return bf ? absorb_t<float, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
-                : absorb_t<float, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
+      return bf ? absorb_t<float, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s)
+                : absorb_t<float, __half>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s);
     case QSVD_F16:
-      return bf ? absorb_t<__half, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
-                : absorb_t<__half, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
+      return bf ? absorb_t<__half, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s)
+                : absorb_t<__half, __half>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s);
     case QSVD_BF16:
-      return bf ? absorb_t<__nv_bfloat16, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, status, third, s)
-                : absorb_t<__nv_bfloat16, __half>(d, q, wuk, scale, qt32, qt16, status, third, s);
+      return bf ? absorb_t<__nv_bfloat16, __nv_bfloat16>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s)
+                : absorb_t<__nv_bfloat16, __half>(d, q, wuk, scale, qt32, qt16, qparts, status, third, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -700,7 +700,7 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
   const Smem s = carve<NP, QS, PS, SG, QB>(base, ns, nz, nraw, r);
   // S accumulator columns per buffer: hi and lo query parts (16-bit), or the
   // three int8 query parts' int32 sums of one group (quantised)
-  constexpr int SW = QB ? 3 * NP : QS * NP;
+  constexpr int SW = QB ? 3 * NP : 2 * NP;   // (a third 16-bit part adds to the second's columns)
   constexpr int WG = softmax_groups<NP, QB>(), HW = NP / WG;   // softmax groups, heads per group
   const int ZC0 = SG ? 0 : (QB ? nsg : 2) * SW;   // first Z column
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -863,6 +863,8 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
             const uint64_t a = sa + uint64_t((kk * 32) >> 4);
             const uint64_t bd = sa + uint64_t((kBoxBytes + kk * 32) >> 4);
             tc_mma(d, a, bd, id_s, (first | kk) != 0);
+            if constexpr (QS == 3)
+              tc_mma(d + NP, a, bd + uint64_t((2 * NP * 128) >> 4), idesc_f16(128, NP, BF16, false, false), true);
           }
           tc_commit(saddr(&s.s_empty[rg.slot]));
           rg.advance();
@@ -1078,7 +1080,7 @@ k_split_tc(const __grid_constant__ CUtensorMap tm_cs, const __grid_constant__ CU
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < HW / 16; ++c) tmem_ld16(tmem + lane_off + uint32_t(pb * SW + hb + 16 * c), sv + 16 * c);
-        if (QS == 2) {   // S = C (q_hi + q_lo)
+        {   // S = C (q_hi + q_lo [+ q_rest])
           float lo[HW];
 #pragma unroll
           for (int c = 0; c < HW / 16; ++c)
@@ -1621,7 +1623,9 @@ cudaError_t launch_t(const qsvd_dims& d, const void* cache, const void* scales, 
                      float* pz, int32_t* status, cudaStream_t s, int ch = 1, const float* qsh = nullptr) {
   TensorMapEncode enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  constexpr int QS = 2;              // absorbed query as hi + lo 16-bit parts
+  // absorbed query as hi + lo 16-bit parts; where bf16 rows' scores are kept,
+  // for float32 weights, three parts (16 bits of the query would show there)
+  constexpr int QS = BF16 && KEEP ? 3 : 2;
   constexpr int PS = BF16 ? 2 : 1;   // P as hi + lo parts for bf16 (8-bit mantissa)
   const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t rows = cuuint64_t(d.batch) * d.max_len;

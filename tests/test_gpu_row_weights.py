@@ -18,6 +18,12 @@ CASES = {
     "f16-tc": dict(cache="f16", H=4, d_h=64, r=256, lens=(0, 1, 127, 128, 129, 700), kernel=T),
     "f16-tc-20-heads": dict(cache="f16", H=20, d_h=64, r=384, lens=(300, 64), kernel=T),
     "bf16-tc": dict(cache="bf16", weight="bf16", out="bf16", H=32, d_h=128, r=512, lens=(1000, 3), kernel=T),
+    # three parts of the absorbed query: both head paddings, all of TMEM, both absorption kernels, two parts by cluster
+    "bf16-7b": dict(cache="bf16", weight="bf16", out="bf16", H=32, d_h=128, r=1536, lens=(300, 0, 128, 1), kernel=T),
+    "bf16-12-heads": dict(cache="bf16", weight="f16", H=12, d_h=64, r=640, lens=(129, 20), kernel=T),
+    "bf16-f32-weights": dict(cache="bf16", weight="f32", H=4, d_h=64, r=128, lens=(0, 140), kernel=T),
+    "bf16-d-24": dict(cache="bf16", weight="bf16", H=8, d_h=24, r=256, lens=(130, 3), kernel=T),
+    "bf16-cluster": dict(cache="bf16", weight="bf16", H=8, d_h=64, r=512, lens=(0, 257, 40), kernel=C),
     "f16-cluster": dict(cache="f16", H=8, d_h=64, r=512, lens=(0, 257, 40), kernel=C),
     "i8-tc": dict(cache="i8", H=4, d_h=64, r=256, lens=(0, 1, 129, 500), kernel=T),
     "i8-tc-32-heads": dict(cache="i8", weight="bf16", out="bf16", H=32, d_h=64, r=256, lens=(200, 77), kernel=T),
@@ -114,3 +120,52 @@ def test_clamped_length_is_flagged(cuda_ok):
     ws = q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, lengths, out, w)
     assert q.status_word(ws) == q.QSVD_STATUS_LEN_CLAMPED
     assert bool((out[0] == 0).all()) and bool((w[0] == 0).all()) and bool((w[1] > 0).all())
+
+
+@pytest.mark.parametrize("prefix", [0, 1])
+def test_bf16_rows_see_more_of_the_query_than_two_parts(cuda_ok, prefix):
+    """Rows V c_j - U c_k whose two large terms nearly cancel, for queries with 24 significant bits.  With u = 2^-23 a term's
+    product of query and weight comes from three parts (three truncations) and one scaling (u / 2), and enters the score's
+    sum with one more truncation: 4.5 u of each term.  The gain on the query moves a score by less than 2^-19 of itself;
+    2^-20 for the exponential, the sums and the float32 weights.  Two parts would miss up to 2^-18 of each term."""
+    B, n, r, d_h = 8, 64, 256, 64
+    g = torch.Generator()
+    g.manual_seed(3)
+    bf = lambda x: x.bfloat16().double()  # noqa: E731
+    a = bf(1 + torch.rand(r, generator=g))
+    rows = torch.zeros(n, r, dtype=torch.float64)
+    pairs = []
+    for t in range(1, n):   # U is what bf16 has next to V a_j / a_k
+        j, k = 2 * t, 2 * t + 1
+        for _ in range(1000):
+            v = float(bf(256 + 256 * torch.rand(1, generator=g)))
+            u = float(bf(torch.tensor(v * float(a[j] / a[k]))))
+            if abs(v * a[j] - u * a[k]) < 4:
+                break
+        rows[t, j], rows[t, k] = v, -u
+        pairs.append((j, k))
+    query = (1 + torch.rand(B, generator=g)).float()
+    dims = q.make_dims(d_h, 1, d_h, r, B, n, cache="bf16", weight="bf16", kernel=T)
+    wuk = torch.zeros(r, d_h, dtype=torch.float64)
+    wuk[:, 0] = a
+    z = torch.zeros(r, d_h, device=DEV, dtype=torch.bfloat16)
+    packed = q.qsvd_prepare_weights(dims, z.t().contiguous(), z, wuk.bfloat16().to(DEV), z)
+    qin = torch.zeros(B, d_h)
+    qin[:, 0] = query
+    cache = rows.bfloat16()[None].repeat(B, 1, 1).contiguous().to(DEV)
+    lengths = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    w, out = torch.zeros(B, n, device=DEV), torch.zeros(B, d_h, device=DEV)
+    zero = torch.zeros(1, r, device=DEV, dtype=torch.bfloat16)
+    q.qsvd_decode_attn_shared(dims, packed, qin.to(DEV), False, zero if prefix else None, None, prefix, cache, None, lengths,
+                              out, weights=w, accumulate=False)
+    scores = query.double()[:, None] * (rows @ a)[None] / d_h ** 0.5
+    terms = query.double()[:, None] * (rows.abs() @ a)[None] / d_h ** 0.5
+    lim = 4.5 * 2.0 ** -23 * terms + 2.0 ** -19 * scores.abs() + 2.0 ** -20
+    got = w.double().cpu()
+    off = (got[:, 1:] / got[:, :1]).log() - scores[:, 1:]
+    assert float((off.abs() / lim[:, 1:]).max()) <= 1.0
+    # by arithmetic: with two parts of the absorbed query some of these rows would be further off than that
+    qt = query.double()[:, None] * a[None] * (1.4426950408889634 / d_h ** 0.5)
+    two = bf(qt) + bf(qt - bf(qt))
+    miss = ((two - qt) @ rows.t()) * 0.6931471805599453
+    assert float((miss[:, 1:].abs() / lim[:, 1:]).max()) > 1.5

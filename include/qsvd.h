@@ -480,12 +480,13 @@ qsvd_status qsvd_prepare_per_head_fold(const qsvd_dims* dims, const void* bv, co
  * they were.  Summed over steps (accumulate != 0) it is what decides which
  * rows qsvd_evict_rows keeps.  The output is that of qsvd_decode_attn, up to
  * a few 1e-6 of the scores (the query is scaled up by what the tensor cores'
- * truncating accumulation takes off them).
+ * truncating accumulation takes off them; bf16 rows and bf16 weights take it
+ * in three bf16 parts instead of two).
  * Serving decode; the pages have no counterpart.
  *   weights    device, B x max_len float32, 4-byte aligned.
  *   workspace  as in qsvd_decode_attn, with room for the step's scores
- *              (B x H x max_len float32 more in absorbed mode); query its size
- *              with this call.
+ *              (in absorbed mode B x H x max_len float32 more, and for bf16
+ *              rows B x H x r 16-bit); query its size with this call.
  * Every other argument, limit, status bit and error as in qsvd_decode_attn
  * (all phases).  The weights are sums of float32 terms in head order: the
  * same inputs and num_splits give the same bits.

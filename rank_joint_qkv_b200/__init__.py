@@ -139,15 +139,24 @@ def qsvd_testing_set_score_wait_ns(ns: int) -> None:
     _check(_lib.qsvd_testing_set_score_wait_ns(int(ns)), "qsvd_testing_set_score_wait_ns")
 
 
-def _empty_bytes(n: int, device) -> torch.Tensor:
-    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
-
-
 def _scratch(n: int, device, stream) -> torch.Tensor:
-    """A workspace for one call: it outlives the call on ``stream`` even if the caller drops it at once."""
-    t = _empty_bytes(n, device)
-    if stream is not None:
-        t.record_stream(stream)
+    """Device bytes for a call on ``stream`` (None: the current one).
+
+    They come from that stream's own pool: a block of another stream's may
+    still be in use there, and one that went back to another stream's while
+    the call runs could be handed out again.  The tensor goes to the caller,
+    so it is kept from reuse until the stream current here is done with it
+    too."""
+    n = max(int(n), 256)
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # any holder of a cudaStream_t
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+    if here != stream:
+        t.record_stream(here)
     return t
 
 
@@ -160,7 +169,7 @@ def qsvd_prepare_weights(dims: qsvd_dims, wd, wuq, wuk, wuv, h2_q=None, packed=N
     _check(_lib.qsvd_prepare_weights(ctypes.byref(dims), None, None, None, None, None, None,
                                      ctypes.byref(n), None), "qsvd_prepare_weights(size)")
     if packed is None:
-        packed = _empty_bytes(n.value, wd.device)
+        packed = _scratch(n.value, wd.device, stream)
     n = ctypes.c_size_t(packed.numel() * packed.element_size())
     hq = None
     if h2_q is not None:
@@ -199,7 +208,7 @@ def append_workspace_bytes(dims: qsvd_dims) -> int:
 def qsvd_append_latent(dims: qsvd_dims, packed, x, pos, cache, scales=None, c_out=None,
                        status=None, workspace=None, stream=None):
     if workspace is None:
-        workspace = _empty_bytes(append_workspace_bytes(dims), x.device)
+        workspace = _scratch(append_workspace_bytes(dims), x.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_append_latent(ctypes.byref(dims), _ptr(packed), _ptr(x), _ptr(pos),
                                    _ptr(cache), _ptr(scales), _ptr(c_out), _ptr(status),
@@ -233,7 +242,8 @@ def qsvd_sq_diff_sum(y, yq, out, stream=None) -> None:
 def qsvd_prepare_per_head_fold(dims: qsvd_dims, bv, wo, f=None, stream=None) -> torch.Tensor:
     """F = [B_{Vh} W_{O,h}]_h (H r x E) in the weight type; returns F."""
     if f is None:
-        f = torch.empty((dims.H * dims.r, dims.E), dtype=wo.dtype, device=wo.device)
+        f = _scratch(dims.H * dims.r * dims.E * wo.element_size(), wo.device, stream)
+        f = f[:dims.H * dims.r * dims.E * wo.element_size()].view(wo.dtype).view(dims.H * dims.r, dims.E)
     _check(_lib.qsvd_prepare_per_head_fold(ctypes.byref(dims), _ptr(bv), _ptr(wo), _ptr(f), _stream(stream)),
            "qsvd_prepare_per_head_fold")
     return f
@@ -251,7 +261,7 @@ def qsvd_prefill_attention(dims: qsvd_dims, packed, cache, lengths, out, status,
     """Causal attention over the prompts' latent rows (cache rows b * max_len
     + t, t < lengths[b]); out is B x max_len x E.  Returns the workspace."""
     if workspace is None:
-        workspace = _empty_bytes(prefill_attention_workspace_bytes(dims), cache.device)
+        workspace = _scratch(prefill_attention_workspace_bytes(dims), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_prefill_attention(ctypes.byref(dims), _ptr(packed), _ptr(cache), _ptr(lengths),
                                        _ptr(workspace), ctypes.byref(n), _ptr(out), _ptr(status),
@@ -281,7 +291,7 @@ def decode_workspace_bytes(dims: qsvd_dims, num_splits: int = 0) -> int:
 def qsvd_decode_attn(dims: qsvd_dims, packed, qin, qin_is_latent, cache, scales, lengths,
                      out, num_splits=0, workspace=None, phases=0, stream=None):
     if workspace is None:
-        workspace = _empty_bytes(decode_workspace_bytes(dims, num_splits), cache.device)
+        workspace = _scratch(decode_workspace_bytes(dims, num_splits), cache.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_decode_attn(ctypes.byref(dims), _ptr(packed), _ptr(qin),
                                  int(bool(qin_is_latent)), _ptr(cache), _ptr(scales),
@@ -306,7 +316,7 @@ def qsvd_decode_attn_per_head(dims: qsvd_dims, bk, bv, q, ck, cv, lengths, out, 
     H x r x d_h; q: B x E float32.  Returns the workspace (its first int32
     is the status word)."""
     if workspace is None:
-        workspace = _empty_bytes(per_head_workspace_bytes(dims), q.device)
+        workspace = _scratch(per_head_workspace_bytes(dims), q.device, stream)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
     _check(_lib.qsvd_decode_attn_per_head(ctypes.byref(dims), _ptr(bk), _ptr(bv), _ptr(q), _ptr(ck),
                                           _ptr(cv), _ptr(lengths), int(layout), _ptr(workspace), ctypes.byref(n),

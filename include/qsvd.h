@@ -531,7 +531,9 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
  * r % 64 == 0, H <= 128 and dims->kernel other than SIMT, and on the CUDA cores
  * otherwise; with dims->rope for cache and weights both F16 or both BF16 with
  * d_h == 128 besides.  A quantised prefix is expanded to fp16 parts in the workspace,
- * so code x scale and the absorbed query must lie within fp16's range.
+ * so code x scale must lie within fp16's range; the absorbed query is scaled
+ * per (sequence, head) and may have any size.  F16 rows take it unscaled, as in
+ * qsvd_decode_attn: past 65,504 it is infinite, below 2^-14 it loses bits.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  */
 qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, const float* qin,

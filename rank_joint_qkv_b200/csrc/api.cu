@@ -488,14 +488,16 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       // only the copies the split kernels read: fp32 for CUDA cores, 16-bit hi/lo
       // for tensor cores; a quantised latent on the tensor cores takes the
       // absorbed query as three int8 parts and one scale per (sequence, head),
-      // both written into the 16-bit parts' section from the fp32 copy
+      // both written into the 16-bit parts' section from the fp32 copy; a
+      // quantised prefix takes two scaled fp16 parts of it
     {
-      const bool codes = kernel != QSVD_KERNEL_SIMT && cache_is_int(d);
+      const bool codes = kernel != QSVD_KERNEL_SIMT && cache_is_int(d), pcodes = px && X.fast && cache_is_int(d);
       const bool need32 = kernel == QSVD_KERNEL_SIMT || codes || (px && !X.fast);
-      void* parts = (kernel != QSVD_KERNEL_SIMT && !codes) || (px && X.fast) ? (px && cache_is_int(d) ? px16 : qt16) : nullptr;
+      void* parts = !cache_is_int(d) && (kernel != QSVD_KERNEL_SIMT || (px && X.fast)) ? qt16 : nullptr;
       e = launch_absorb(d, qsrc, P + L.wuk, sl2, need32 ? qt32 : nullptr, parts, &hdr->status, s, third, qparts);
-      if (e == cudaSuccess && codes)
-        e = launch_quant_query(d, qt32, static_cast<int8_t*>(qt16), quant_query_scales(d, qt16), s);
+      if (e == cudaSuccess && (codes || pcodes))
+        e = launch_quant_query(d, qt32, codes ? static_cast<int8_t*>(qt16) : nullptr, quant_query_scales(d, qt16),
+                               pcodes ? px16 : nullptr, reinterpret_cast<float*>(Wb + X.qinv), s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "query prologue");
   }

@@ -217,7 +217,10 @@ cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, f
                           float* qt32, void* qt16, int32_t* status, cudaStream_t s, bool third = false, int qparts = 2);
 // Quantised latent on the tensor cores: qt32 [B][H][r] -> three int8 parts
 // qp [B][3][H][r] and one power-of-two scale qs [B][H] per (sequence, head).
-cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s);
+// And, for a quantised shared prefix, two scaled fp16 parts pp [B][2][H][r] with
+// the scales' inverses pinv [B][H].  Either pair may be null.
+cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, void* pp, float* pinv,
+                               cudaStream_t s);
 // before: rows ahead of the sequence's own.  pack (d_h 128): also written
 // there are the query's two fp16 parts, scaled by dev::f16_scale, as B
 // fragments of m16n8k16: per (sequence, head) kRopePackWords words, of which

@@ -30,9 +30,14 @@
 // Precision as in the split kernels: the query as two 16-bit parts (three of
 // bf16's where weights are asked for; the products accumulate in float32), P as
 // two for bf16; a quantised prefix is
-// expanded to the fp16 hi and lo parts of code x scale (18 bits: exact), each
-// a pass of both products, so that the scores are as good as the integer ones
-// of the sequences' own rows.
+// expanded to the fp16 hi and lo parts of code x scale (18 bits: exact up to
+// 65,504), each a pass of both products, and its query parts are scaled by a
+// power of two per (sequence, head) (k_quant_query), so that the scores are as
+// good as the integer ones of the sequences' own rows whatever the query's size.
+// One fp16 part of P (each weight within 2^-11) under an unrounded sum is what
+// outputs of fp16 and quantised rows mostly differ by from 32-bit ones; a second
+// part would double the values' product (17 of 101 us at B 16, P 8192, 74 of
+// 400 at B 64, P 16384).
 //
 // Measured at B 64, H 32, r 1536 over 16,384 fp16 rows (206 and 103 GFLOP with
 // the query's two parts counted): scores 137 us, 1.50 PFLOP/s, values 74 us,
@@ -81,6 +86,7 @@ struct PxArgs {
   float* pl;      // split of its own (tiles == SP)
   float* pz;      // [SP B][H][r] (values: written)
   float gain;     // on the scores (see launch_prefix)
+  const float* qinv;   // [B][H] and the inverse of the query's scale (null: not scaled)
   int32_t* counter;   // score units taken (single CTAs)
   int32_t* status;
 };
@@ -415,7 +421,8 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
           for (int e = 0; e < 32; ++e) mx = c + e < nv ? fmaxf(mx, v[e]) : mx;
         }
         mx = fmaxf(mx, exchange(mx));
-        const float ref = kRefStep * floorf(mx * g.gain / kRefStep);
+        const float gain = g.qinv && t < live_rows ? g.gain * __ldcg(g.qinv + size_t(mb) * g.nb * g.H + t) : g.gain;
+        const float ref = kRefStep * floorf(mx * gain / kRefStep);
         float sum = 0.f;
         uint8_t* prow = reinterpret_cast<uint8_t*>(static_cast<T16*>(g.p) + (size_t(mb) * 128 + 32 * q) * g.ppad + size_t(n) * kPxTile);
         constexpr int kStep = PS == 2 ? 32 : 64;   // tokens staged at a time: hi parts, and lo parts beside them
@@ -434,7 +441,7 @@ k_prefix_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
               T16* lv = reinterpret_cast<T16*>(&lo);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float p = c + 32 * e32 + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], g.gain, -ref)) : 0.f;
+                const float p = c + 32 * e32 + 8 * e8 + e < nv ? exp2f(fmaf(v[8 * e8 + e], gain, -ref)) : 0.f;
                 sum += p;
                 hv[e] = dev::from_f<T16>(p);
                 if (PS == 2) lv[e] = dev::from_f<T16>(p - dev::to_f(hv[e]));
@@ -850,7 +857,7 @@ cudaError_t fast_t(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const
   PxArgs g{d.batch, d.H, d.r, L.plen, L.nb, L.MB, L.tiles, L.ppad, L.SP, ws + L.p,
            reinterpret_cast<float*>(ws + L.mt), reinterpret_cast<float*>(ws + L.lt), reinterpret_cast<float*>(ws + L.pm),
            reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz),
-           gain, counter, status};
+           gain, cache_is_int(d) ? reinterpret_cast<const float*>(ws + L.qinv) : nullptr, counter, status};
   cudaError_t e;
   if (given) {
     const bool own = L.tiles == L.SP;   // as in the scores' epilogue
@@ -922,6 +929,7 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
       }
     L.slots = L.SP * d.batch;
     if (q) { L.qt16 = o; o = align256(o + 2 * B * H * r * 2); }   // beside the int8 parts
+    if (q) { L.qinv = o; o = align256(o + B * H * 4); }
     if (q) { L.cparts = o; o = align256(o + 2 * P * r * 2); }
     const size_t rows = size_t(L.MB) * 128;
     L.p = o; o = align256(o + (d.cache_dtype == QSVD_BF16 ? 2 : 1) * rows * L.ppad * 2);

@@ -18,12 +18,13 @@ struct PrefixLayout {
   int SP;           // token splits of the value product
   int G;            // CUDA cores: split CTAs
   int slots;        // partials (fast: SP x B; CUDA cores: G + B)
-  size_t qt16, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, tab, scores, qpack, total;
+  size_t qt16, qinv, cparts, p, mt, lt, pm, pl, pz, ml, sched, hdr, cm, cl, cz, csched, tab, scores, qpack, total;
 };
 PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base);
 
 // The prefix's partials (m, l, z per slot) from the absorbed query: qt16 its
-// 16-bit parts [B][qparts][H][r] (fast), qt32 [B][H][r] (CUDA cores).  gain: on
+// 16-bit parts [B][qparts][H][r] (fast; of a quantised prefix scaled per
+// (sequence, head), the scales' inverses at L.qinv), qt32 [B][H][r] (CUDA cores).  gain: on
 // the tensor cores' scores, for what their accumulation truncates.  counter:
 // one word, zero.
 // launch_prefix_expand goes before the own rows' split kernel and

@@ -317,10 +317,16 @@ k_absorb_mma(const __grid_constant__ CUtensorMap tm_w, const float* __restrict__
 // Q0 = rint(qt / s) (|Q0| <= 127), Q1 = rint(128 (qt - s Q0) / s), Q2 likewise
 // (|Q1|, |Q2| <= 64; remainder <= s / 32768): the integer MMAs of the split
 // kernel take the parts, the softmax applies s once per head.  qp [B][3][H][r]
-// int8, qs [B][H].  grid (H, B), block 128.
+// int8, qs [B][H].
+// For a shared prefix, whose rows are expanded to fp16: also two fp16 parts pp
+// [B][2][H][r] of the row scaled by dev::f16_scale, and the scale's inverse
+// pinv [B][H] -- unscaled, an element past 65,504 would be infinite and one
+// below 2^-14 would lose its second part's bits.
+// Either output may be null.  grid (H, B), block 128.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(128)
-k_quant_query(const float* __restrict__ qt, int8_t* __restrict__ qp, float* __restrict__ qs, int H, int r) {
+k_quant_query(const float* __restrict__ qt, int8_t* __restrict__ qp, float* __restrict__ qs, __half* __restrict__ pp,
+              float* __restrict__ pinv, int H, int r) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   __shared__ float red[4];
@@ -332,6 +338,20 @@ k_quant_query(const float* __restrict__ qt, int8_t* __restrict__ qp, float* __re
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if (pp) {
+    float inverse;
+    const float ps = dev::f16_scale(m, &inverse);
+    if (threadIdx.x == 0) pinv[size_t(b) * H + h] = inverse;
+    __half* hi = pp + ((size_t(b) * 2 + 0) * H + h) * r;
+    __half* lo = hi + size_t(H) * r;
+    for (int j = threadIdx.x; j < r; j += 128) {
+      const float v = row[j] * ps;   // exact: a power of two
+      const __half top = __float2half_rn(v);
+      hi[j] = top;
+      lo[j] = __float2half_rn(v - __half2float(top));
+    }
+  }
+  if (!qp) return;
   // the smallest power of two >= m / 127 (1 for an all-zero query)
   const float f = m / 127.f;
   const float sq = f > 0.f ? __uint_as_float((__float_as_uint(f) + 0x007FFFFFu) & 0xFF800000u) : 1.f;
@@ -565,9 +585,11 @@ cudaError_t launch_absorb(const qsvd_dims& d, const float* q, const void* wuk, f
   }
 }
 
-cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, cudaStream_t s) {
+cudaError_t launch_quant_query(const qsvd_dims& d, const float* qt, int8_t* qp, float* qs, void* pp, float* pinv,
+                               cudaStream_t s) {
   {
-    const cudaError_t le = launch_pdl(k_quant_query, dim3(d.H, d.batch), dim3(128), 0, s, qt, qp, qs, d.H, d.r);
+    const cudaError_t le = launch_pdl(k_quant_query, dim3(d.H, d.batch), dim3(128), 0, s, qt, qp, qs,
+                                      static_cast<__half*>(pp), pinv, d.H, d.r);
     if (le != cudaSuccess) return le;
   }
   note_launch();

@@ -339,3 +339,54 @@ def test_on_the_other_current_stream(cuda_ok):
     side.synchronize()
     assert torch.equal(out, want)
     assert np.isfinite(out.float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** -17], ids=["large", "small"])
+@pytest.mark.parametrize("kernel", [q.QSVD_KERNEL_AUTO, S], ids=["tc", "simt"])
+@pytest.mark.parametrize("cache", ["i8", "i4"])
+def test_a_quantised_prefix_takes_a_query_of_any_size(cuda_ok, cache, kernel, size):
+    """One prefix row c and one own row of zeros: the own row's weight is 1 / (1 + e^s), which gives the prefix's score s
+    back.  The absorbed query qt is q a tau, past fp16's range or within its last subnormals, and c the other way round.
+    With T = sum_j |qt_j c_j|: qt_j from three parts and a scaling is off by 4.5 x 2^-23, as two fp16 parts of a scaled row
+    by another 2^-22; 3 x 16 accumulations of 16 products, each cut off below 2^-22 of T; 2^-19 of s for the gain.  The
+    weight in float32, its exponentials and sum: 2^-20 of w, an error of s of 2^-20 / (1 - w)."""
+    B, r, d_h, qmax = 8, 256, 64, 7
+    g = torch.Generator()
+    g.manual_seed(11)
+    a = (1 + torch.rand(r, generator=g)).bfloat16().double() * size
+    codes = torch.randint(-qmax, qmax + 1, (1, r), generator=g)
+    tau = d_h ** -0.5
+    # a scale that brings T to about 16, a multiple of fp16's smallest number
+    sc = torch.tensor(16.0 / float((1.5 * tau * a.abs() * codes[0].abs()).sum()), dtype=torch.float64).half().clamp(min=2.0 ** -24)
+    values = codes.double() * sc.double()
+    assert float(values.abs().max()) < 65504
+    query = (1 + torch.rand(B, generator=g)).float()
+    dims = q.make_dims(d_h, 1, d_h, r, B, 1, cache=cache, weight="bf16", kernel=kernel)
+    wuk, wuv = torch.zeros(r, d_h, dtype=torch.float64), torch.zeros(r, d_h, dtype=torch.float64)
+    wuk[:, 0] = a
+    wuv[:, 1] = torch.randn(r, generator=g, dtype=torch.float64).bfloat16().double()
+    z = torch.zeros(r, d_h, device=DEV, dtype=torch.bfloat16)
+    packed = q.qsvd_prepare_weights(dims, z.t().contiguous(), z, wuk.bfloat16().to(DEV), wuv.bfloat16().to(DEV))
+    qin = torch.zeros(B, d_h)
+    qin[:, 0] = query
+    stored = codes if cache == "i8" else (codes[:, 0::2] & 0xF) | ((codes[:, 1::2] & 0xF) << 4)
+    prefix = stored.to(torch.int8 if cache == "i8" else torch.uint8).contiguous().to(DEV)
+    scales = sc.expand(1, r // 128).contiguous().to(DEV)
+    own = torch.zeros(B, 1, prefix.shape[1], dtype=prefix.dtype, device=DEV)
+    own_scales = torch.ones(B, 1, r // 128, dtype=torch.float16, device=DEV)
+    w, out = torch.zeros(B, 1, device=DEV), torch.zeros(B, d_h, device=DEV)
+    ws = q.qsvd_decode_attn_shared(dims, packed, qin.to(DEV), False, prefix, scales, 1, own, own_scales,
+                                   torch.ones(B, dtype=torch.int32, device=DEV), out, weights=w, accumulate=False)
+    torch.cuda.synchronize()
+    assert q.status_word(ws) == 0
+    qt = query.double()[:, None] * a[None] * tau
+    s, terms = qt @ values[0], qt.abs() @ values[0].abs()
+    assert 4 < float(terms.min()) and float(s.abs().max()) < 8   # neither score far from the own row's
+    w = w[:, 0].double().cpu()
+    p = torch.sigmoid(s)
+    lim = (6.5 * 2.0 ** -23 + 48 * 2.0 ** -22) * terms + 2.0 ** -19 * s.abs() + 2.0 ** -20 / p
+    assert float((((1 - w) / w).log() - s).abs().div(lim).max()) <= 1.0
+    # the value: p within its score's error and one fp16 rounding, c W in two 16-bit parts of the merged latent
+    want = p * (values[0] @ wuv[:, 1])
+    bar = (lim + 2.0 ** -11) * want.abs() + 2.0 ** -14 * (p * (values[0].abs() @ wuv[:, 1].abs()))
+    assert bool(((out[:, 1].double().cpu() - want).abs() <= bar).all())

@@ -112,15 +112,18 @@ __device__ __forceinline__ void cluster_sync_all() {
 //   ring   NT tile slots, each the CTA's RC channels of one 128-token tile:
 //          RC / 64 boxes of [128 rows][64 channels], 128-byte swizzle
 //   qbuf   the CTA's query slice: per 64-channel box [part][NP rows][64],
-//          QS = 2 parts (rounded 16-bit query + its rounding residual)
-//   xbuf   two exchange buffers of the S partial, [NP / 4][128 tokens][4]
-//          floats (16-byte vectors: conflict-free for token-per-thread)
+//          QS = 2 parts (rounded 16-bit query + its rounding residual), or 3
+//          (and what these leave) for bf16 rows whose scores are kept
+//   xbuf   XB = 2 exchange buffers of the S partial, [NP / 4][128 tokens][4]
+//          floats (16-byte vectors: conflict-free for token-per-thread); one
+//          where a third query part leaves no room for two beside two tiles
 //   pbuf   two P^T buffers, PS parts each, [half][NP rows][64 tokens]
-template <int NP, int RC>
+template <int NP, int RC, int QS>
 struct ClSizes {
   static constexpr int NBX = RC / 64;                  // boxes per tile slot
   static constexpr int kSlot = NBX * kClBox;
-  static constexpr int kQBox = 2 * NP * 128;           // QS = 2
+  static constexpr int kQBox = QS * NP * 128;
+  static constexpr int XB = QS == 3 && NP == 32 && RC == 256 ? 1 : 2;
   static constexpr int kQBuf = NBX * kQBox;
   static constexpr int kXBuf = NP * 128 * 4;
   static constexpr int kPPart = 2 * NP * 128;
@@ -129,7 +132,7 @@ struct ClSizes {
 struct ClSmem {
   uint8_t* ring;
   uint8_t* qbuf;
-  uint8_t* xbuf;       // [2]
+  uint8_t* xbuf;       // [XB]
   uint8_t* pbuf;       // [2][PS]
   uint64_t* t_full;    // [kClMaxSlots]
   uint64_t* t_empty;   // [kClMaxSlots]
@@ -150,14 +153,14 @@ struct ClSmem {
 };
 constexpr int kClMaxSlots = 4;
 
-template <int NP, int RC, int PS>
+template <int NP, int RC, int PS, int QS>
 __device__ ClSmem cl_carve(uint8_t* base, int nt) {
-  using Z = ClSizes<NP, RC>;
+  using Z = ClSizes<NP, RC, QS>;
   ClSmem s;
   s.ring = base;
   s.qbuf = s.ring + size_t(nt) * Z::kSlot;
   s.xbuf = s.qbuf + Z::kQBuf;
-  s.pbuf = s.xbuf + 2 * Z::kXBuf;
+  s.pbuf = s.xbuf + Z::XB * Z::kXBuf;
   uint8_t* m = s.pbuf + 2 * PS * Z::kPPart;
   uint64_t* bars = reinterpret_cast<uint64_t*>(m);
   s.t_full = bars;
@@ -203,22 +206,22 @@ __device__ __forceinline__ void cl_ragged(uint8_t* d, const uint8_t* src, size_t
 
 // ------------------------------------------------------------------ kernel
 
-template <int NP, bool BF16, int RC>
+template <int NP, bool BF16, int RC, int QS>
 __global__ void __launch_bounds__(kThreadsCl, 1)
 k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q,
            const uint8_t* __restrict__ cache, const int32_t* __restrict__ sched,
            float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
            int32_t* __restrict__ status, int B, int H, int r, int max_len, int G, int nt,
            float* __restrict__ keep) {
-  constexpr int QS = 2, PS = BF16 ? 2 : 1;
-  constexpr int SW = QS * NP;                 // S accumulator columns per buffer
+  constexpr int PS = BF16 ? 2 : 1;
+  constexpr int SW = 2 * NP;                  // S accumulator columns per buffer (a third part adds to the second's)
   constexpr int ZC0 = 2 * SW;                 // first Z column
-  using Z = ClSizes<NP, RC>;
+  using Z = ClSizes<NP, RC, QS>;
   constexpr int NBX = Z::NBX, NCH = RC / 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const ClSmem s = cl_carve<NP, RC, PS>(base, nt);
+  const ClSmem s = cl_carve<NP, RC, PS, QS>(base, nt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int CS = r / RC;                      // CTAs per cluster
   const uint32_t rank = cluster_rank();
@@ -345,6 +348,8 @@ k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUt
             const uint64_t a = da0 + uint64_t((rg.slot * Z::kSlot + u * kClBox + kk * 32) >> 4);
             const uint64_t bq = qd0 + uint64_t((u * Z::kQBox + kk * 32) >> 4);
             tc_mma(d, a, bq, id_s, (u | kk) != 0);
+            if constexpr (QS == 3)
+              tc_mma(d + NP, a, bq + uint64_t((2 * NP * 128) >> 4), idesc_f16(128, NP, BF16, false, false), true);
           }
         }
         tc_commit(saddr(&s.acc_full[i & 1]));
@@ -410,9 +415,10 @@ k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUt
     it.init(sched, B, tb, te);
     for (int i = 0; i < n; ++i) {
       const int pb = i & 1;
+      const int xi = i % Z::XB, xn = i / Z::XB;   // exchange buffer and how often it was used before
       const bool first = it.first(tb), last = it.last();
       const int nv = it.nvalid();
-      // this CTA's S partial, S_k = C_k (q_hi + q_lo)_k, out of TMEM
+      // this CTA's S partial, S_k = C_k (q_hi + q_lo [+ q_rest])_k, out of TMEM
       int fail = !mbar_wait(saddr(&s.acc_full[pb]), uint32_t(i >> 1) & 1u);
       if (group_or(fail)) { if (t == 0) cl_abort(s, status); break; }
       tc_fence_after();
@@ -429,20 +435,20 @@ k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUt
         for (int h = 0; h < NP; ++h) sv[h] += lo[h];
       }
       tc_fence_before();
-      // exchange buffer pb is free once every CTA has read what tile i - 2 left in it
-      if (i >= 2) {
-        fail = !mbar_wait_cluster(saddr(&s.x_empty[pb]), uint32_t((i - 2) >> 1) & 1u);
+      // exchange buffer xi is free once every CTA has read what tile i - XB left in it
+      if (xn > 0) {
+        fail = !mbar_wait_cluster(saddr(&s.x_empty[xi]), uint32_t(xn - 1) & 1u);
         if (group_or(fail)) { if (t == 0) cl_abort(s, status); break; }
       }
-      const uint32_t xb = xb0 + uint32_t(pb * Z::kXBuf);
+      const uint32_t xb = xb0 + uint32_t(xi * Z::kXBuf);
 #pragma unroll
       for (int h4 = 0; h4 < NP / 4; ++h4)
         st_shared_v4(xb + uint32_t((h4 * kTile + t) * 16),
                      make_float4(sv[4 * h4], sv[4 * h4 + 1], sv[4 * h4 + 2], sv[4 * h4 + 3]));
       fence_cluster();
       group_sync();
-      if (t < CS) mbar_arrive_remote(peer_addr(saddr(&s.x_full[pb]), uint32_t(t)));   // one peer per thread
-      fail = !mbar_wait_cluster(saddr(&s.x_full[pb]), uint32_t(i >> 1) & 1u);
+      if (t < CS) mbar_arrive_remote(peer_addr(saddr(&s.x_full[xi]), uint32_t(t)));   // one peer per thread
+      fail = !mbar_wait_cluster(saddr(&s.x_full[xi]), uint32_t(xn) & 1u);
       if (group_or(fail)) { if (t == 0) cl_abort(s, status); break; }
       // S = S_0 + ... + S_{CS-1} in rank order: every CTA holds the same bits
 #pragma unroll
@@ -460,7 +466,7 @@ k_split_cl(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUt
       }
       fence_cluster();
       group_sync();
-      if (t < CS) mbar_arrive_remote(peer_addr(saddr(&s.x_empty[pb]), uint32_t(t)));
+      if (t < CS) mbar_arrive_remote(peer_addr(saddr(&s.x_empty[xi]), uint32_t(t)));
 
       // online softmax, m and l per head in shared memory (thread t < NP owns head t)
       const bool valid = t < nv;
@@ -619,17 +625,18 @@ int cl_slice(int r) {
 }
 int cl_heads_padded(int H) { return H <= 16 ? 16 : (H <= 32 ? 32 : 0); }
 
-template <int NP, bool BF16, int RC>
+template <int NP, bool BF16, int RC, int QS>
 struct ClPlan {
   static constexpr int PS = BF16 ? 2 : 1;
-  using Z = ClSizes<NP, RC>;
+  using Z = ClSizes<NP, RC, QS>;
   static int slots() {
-    const int avail = kClSmemLimit - 1024 - kClMisc - Z::kQBuf - 2 * Z::kXBuf - 2 * PS * Z::kPPart;
+    constexpr int avail = kClSmemLimit - 1024 - kClMisc - Z::kQBuf - Z::XB * Z::kXBuf - 2 * PS * Z::kPPart;
+    static_assert(avail >= 2 * Z::kSlot, "two tiles");
     int nt = avail / Z::kSlot;
     return nt > kClMaxSlots ? kClMaxSlots : nt;
   }
   static size_t smem(int nt) {
-    return 1024 + size_t(nt) * Z::kSlot + Z::kQBuf + 2 * Z::kXBuf + 2 * PS * Z::kPPart + kClMisc;
+    return 1024 + size_t(nt) * Z::kSlot + Z::kQBuf + Z::XB * Z::kXBuf + 2 * PS * Z::kPPart + kClMisc;
   }
   // Launch configuration for G clusters of CS CTAs (attr must outlive cfg).
   static cudaError_t config(int CS, int G, cudaStream_t s, cudaLaunchConfig_t* cfg,
@@ -637,7 +644,7 @@ struct ClPlan {
     *nt = slots();
     if (*nt < 2) return cudaErrorInvalidConfiguration;
     const size_t sm = smem(*nt);
-    cudaError_t e = cudaFuncSetAttribute(k_split_cl<NP, BF16, RC>,
+    cudaError_t e = cudaFuncSetAttribute(k_split_cl<NP, BF16, RC, QS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
     if (e != cudaSuccess) return e;
     memset(cfg, 0, sizeof(*cfg));
@@ -659,7 +666,7 @@ struct ClPlan {
     cudaLaunchAttribute attr;
     int nt = 0, n = 0;
     if (config(CS, 1, nullptr, &cfg, &attr, &nt) != cudaSuccess) return 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_split_cl<NP, BF16, RC>, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_split_cl<NP, BF16, RC, QS>, &cfg) != cudaSuccess) return 0;
     return n;
   }
   static cudaError_t launch(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
@@ -667,7 +674,6 @@ struct ClPlan {
                             float* keep) {
     TensorMapEncode enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
-    constexpr int QS = 2;
     const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tc, tq;
     memset(&tc, 0, sizeof(tc));
@@ -702,7 +708,7 @@ struct ClPlan {
     int nt = 0;
     cudaError_t e = config(CS, G, s, &cfg, &attr, &nt);
     if (e != cudaSuccess) return e;
-    e = cudaLaunchKernelEx(&cfg, k_split_cl<NP, BF16, RC>, tc, tq, static_cast<const uint8_t*>(cache),
+    e = cudaLaunchKernelEx(&cfg, k_split_cl<NP, BF16, RC, QS>, tc, tq, static_cast<const uint8_t*>(cache),
                            sched, pm, pl, pz, status, d.batch, d.H, d.r, d.max_len, G, nt, keep);
     if (e != cudaSuccess) return e;
     note_launch();
@@ -723,14 +729,17 @@ auto cl_dispatch(const qsvd_dims& d, A&&... a) {
 }
 template <int NP, bool BF16, int RC>
 struct ClClusters {
-  static int run(const qsvd_dims& d) { return ClPlan<NP, BF16, RC>::clusters(d); }
+  static int run(const qsvd_dims& d) { return ClPlan<NP, BF16, RC, 2>::clusters(d); }
 };
 template <int NP, bool BF16, int RC>
 struct ClLaunch {
   static cudaError_t run(const qsvd_dims& d, const void* cache, const void* qt16, const int32_t* sched,
                          int G, float* pm, float* pl, float* pz, int32_t* status, cudaStream_t s,
-                            float* keep) {
-    return ClPlan<NP, BF16, RC>::launch(d, cache, qt16, sched, G, pm, pl, pz, status, s, keep);
+                         float* keep) {
+    // bf16 rows whose scores are kept, for float32 weights: three parts of the query
+    if constexpr (BF16)
+      if (keep) return ClPlan<NP, BF16, RC, 3>::launch(d, cache, qt16, sched, G, pm, pl, pz, status, s, keep);
+    return ClPlan<NP, BF16, RC, 2>::launch(d, cache, qt16, sched, G, pm, pl, pz, status, s, keep);
   }
 };
 

@@ -169,3 +169,51 @@ def test_bf16_rows_see_more_of_the_query_than_two_parts(cuda_ok, prefix):
     two = bf(qt) + bf(qt - bf(qt))
     miss = ((two - qt) @ rows.t()) * 0.6931471805599453
     assert float((miss[:, 1:].abs() / lim[:, 1:]).max()) > 1.5
+
+
+@pytest.mark.parametrize("kernel,H,r", [(T, 1, 256), (C, 1, 256), (C, 12, 512), (C, 20, 1024), (A, 32, 1792), (A, 32, 2048)])
+@pytest.mark.parametrize("n", [64, 700])
+def test_bf16_rows_see_more_of_the_query_on_every_kernel(cuda_ok, kernel, H, r, n):
+    """The rows of the test above, their two terms in any two channels and the heads alike, on the one-CTA kernel, on
+    clusters of two to eight CTAs, and where the latter is the library's own choice.  The same bounds, and H additions of the
+    heads' equal weights in each of the two weights compared."""
+    B, d_h = 4, 64
+    g = torch.Generator()
+    g.manual_seed(7)
+    bf = lambda x: x.bfloat16().double()  # noqa: E731
+    a = bf(1 + torch.rand(r, generator=g))
+    rows = torch.zeros(n, r, dtype=torch.float64)
+    for t in range(1, n):
+        for _ in range(1000):
+            j, k = torch.randperm(r, generator=g)[:2].tolist()
+            v = float(bf(256 + 256 * torch.rand(1, generator=g)))
+            u = float(bf(torch.tensor(v * float(a[j] / a[k]))))
+            if abs(v * a[j] - u * a[k]) < 4:
+                break
+        rows[t, j], rows[t, k] = v, -u
+    query = (1 + torch.rand(B, generator=g)).float()
+    E = H * d_h
+    dims = q.make_dims(E, H, d_h, r, B, n, cache="bf16", weight="bf16", kernel=kernel)
+    wuk = torch.zeros(r, E, dtype=torch.float64)
+    wuk[:, ::d_h] = a[:, None]
+    z = torch.zeros(r, E, device=DEV, dtype=torch.bfloat16)
+    packed = q.qsvd_prepare_weights(dims, z.t().contiguous(), z, wuk.bfloat16().to(DEV), z)
+    qin = torch.zeros(B, E)
+    qin[:, ::d_h] = query[:, None]
+    cache = rows.bfloat16()[None].repeat(B, 1, 1).contiguous().to(DEV)
+    lengths = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    w, out = torch.zeros(B, n, device=DEV), torch.zeros(B, E, device=DEV)
+    ws = q.qsvd_decode_attn_weights(dims, packed, qin.to(DEV), False, cache, None, lengths, out, w, accumulate=False)
+    torch.cuda.synchronize()
+    status, _, _, ran = ws[:16].view(torch.int32).tolist()
+    assert status == 0 and ran == (T if kernel == T else C)
+    scores = query.double()[:, None] * (rows @ a)[None] / d_h ** 0.5
+    terms = query.double()[:, None] * (rows.abs() @ a)[None] / d_h ** 0.5
+    lim = 4.5 * 2.0 ** -23 * terms + 2.0 ** -19 * scores.abs() + 2.0 ** -20 + 2 * H * 2.0 ** -24
+    got = w.double().cpu()
+    off = (got[:, 1:] / got[:, :1]).log() - scores[:, 1:]
+    assert float((off.abs() / lim[:, 1:]).max()) <= 1.0
+    qt = query.double()[:, None] * a[None] * (1.4426950408889634 / d_h ** 0.5)
+    two = bf(qt) + bf(qt - bf(qt))
+    miss = ((two - qt) @ rows.t()) * 0.6931471805599453
+    assert float((miss[:, 1:].abs() / lim[:, 1:]).max()) > 1.5

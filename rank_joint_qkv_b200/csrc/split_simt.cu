@@ -238,10 +238,10 @@ k_split_abs(const float* __restrict__ qt32, const uint8_t* __restrict__ cache,
 // ---------------------------------------------------------------------------
 // Rotary split kernel.  grid (G, H), block 256 = 8 warps.
 // Sub-tile of 16 tokens: warp w owns tokens 2w, 2w+1; lane g owns the
-// rotary pairs (i, i + d_h/2) with i in [g*NP, g*NP + NP), NP = d_h/64.
+// rotary pairs (i, i + d_h/2) with i in [g*NP, g*NP + NP), NP = d_h/64 (1 to 4).
 // smem: cs[16][r+1], wk[32][d_h], zs[r].
 // ---------------------------------------------------------------------------
-template <qsvd_dtype CT, typename WT>
+template <qsvd_dtype CT, typename WT, int NP>
 __global__ void __launch_bounds__(kThreads)
 k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
              const float* __restrict__ tab, const uint8_t* __restrict__ cache,
@@ -264,7 +264,6 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
   const int h = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = d_h / 2;
-  const int NP = half / 32;         // pairs per lane (1 or 2 for d_h 64/128)
   const int32_t* tstart = sched;
   const int32_t* lens = sched + B + 1;
   const long long T = tstart[B];
@@ -287,11 +286,12 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
     const uint8_t* seq_base = cache + size_t(b) * max_len * row_bytes;
     const __half* seq_scales = scales ? scales + size_t(b) * max_len * ngroups : nullptr;
     // this lane's query components (already rotated and scaled)
-    float qlo[2], qhi[2];
-    for (int k = 0; k < 2; ++k) {
+    float qlo[NP], qhi[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
       const int i = lane * NP + k;
-      qlo[k] = (k < NP) ? qrot[size_t(b) * E + h * d_h + i] : 0.f;
-      qhi[k] = (k < NP) ? qrot[size_t(b) * E + h * d_h + i + half] : 0.f;
+      qlo[k] = qrot[size_t(b) * E + h * d_h + i];
+      qhi[k] = qrot[size_t(b) * E + h * d_h + i + half];
     }
     __syncthreads();
     for (int j = threadIdx.x; j < r; j += kThreads) zs[j] = 0.f;
@@ -302,11 +302,11 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
       __syncthreads();
       stage_rows<CT>(cs, ldc, TS, seq_base, seq_scales, row_bytes, r, group, s0, nv);
       // keys of tokens 2w, 2w+1 at this lane's dims
-      float acc[2][2][2];  // [token][pair slot][lo/hi]
+      float acc[2][NP][2];  // [token][pair slot][lo/hi]
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) { acc[a][k][0] = 0.f; acc[a][k][1] = 0.f; }
+        for (int k = 0; k < NP; ++k) { acc[a][k][0] = 0.f; acc[a][k][1] = 0.f; }
       for (int j0 = 0; j0 < r; j0 += JC) {
         __syncthreads();
         for (int i = threadIdx.x; i < JC * d_h; i += kThreads) {
@@ -318,6 +318,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
         for (int jj = 0; jj < JC; ++jj) {
           const float c0 = cs[(2 * warp) * ldc + j0 + jj];
           const float c1 = cs[(2 * warp + 1) * ldc + j0 + jj];
+#pragma unroll
           for (int k = 0; k < NP; ++k) {
             const int i = lane * NP + k;
             const float wlo = wk[jj * d_h + i], whi = wk[jj * d_h + i + half];
@@ -335,6 +336,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
         const int pos = s0 + tt;
         float part = 0.f;
         if (tt < nv) {
+#pragma unroll
           for (int k = 0; k < NP; ++k) {
             const int i = lane * NP + k;
             const float cs_ = tab[(size_t(pos) * half + i) * 2 + 0];
@@ -436,12 +438,12 @@ cudaError_t abs_ct(const qsvd_dims& d, const float* qt32, const void* cache, con
   }
 }
 
-template <qsvd_dtype CT, typename WT>
-cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
+template <qsvd_dtype CT, typename WT, int NP>
+cudaError_t rope_np(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                    const void* cache, const void* scales, const int32_t* sched, int G,
                    float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
   const size_t smem = (size_t(16) * (d.r + 1) + size_t(32) * d.d_h + d.r) * 4;
-  auto kern = k_split_rope<CT, WT>;
+  auto kern = k_split_rope<CT, WT, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   dim3 grid(G, d.H);
@@ -452,6 +454,19 @@ cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const
   }
   note_launch();
   return check_launch();
+}
+
+template <qsvd_dtype CT, typename WT>
+cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
+                   const void* cache, const void* scales, const int32_t* sched, int G,
+                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
+  switch (d.d_h) {   // d_h / 64 pairs a lane
+    case 64: return rope_np<CT, WT, 1>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case 128: return rope_np<CT, WT, 2>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case 192: return rope_np<CT, WT, 3>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case 256: return rope_np<CT, WT, 4>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <qsvd_dtype CT>

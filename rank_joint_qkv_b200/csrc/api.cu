@@ -163,11 +163,17 @@ static float score_scale_log2(const qsvd_dims& d) {
 // step on tcgen05 and 0.7 x 2^-25 in the projections' chains of mma.sync.
 // Scores come out short by the sum of these, a slightly higher softmax
 // temperature that 16-bit outputs do not show but float32 attention weights do;
-// the query is scaled up by it where weights are asked for.  Measured as the
+// the serving calls scale the query up by it (decode over a shared prefix with
+// or without weights, so that both give the same output).  Measured as the
 // slope of the weights' log error over their log, one head, 2500 and 3000 rows:
 // without it -3.3e-6 at fp16, r 1536 (96 steps, and 16 of each projection);
 // with the scores' steps alone at 2^-25, -2e-7 to -7e-7 (int8 rows, whose sums
-// are exact: -7e-7, the projections' share).
+// are exact: -7e-7, the projections' share).  Fitted over 13 forms (every split
+// kernel, r 1472 to 2560, own rows and prefixes): -5e-7 to -8.6e-6 without the
+// gain, each within 4% of these formulas, or 2e-7 of them; -2e-7 to 4e-7 with it.
+// It is a mean over dense rows, whose sums keep growing: a score of few terms is cut off fewer times and comes out
+// too large by up to the gain (2.6e-6 of itself at r 1536), one whose first terms
+// make most of it is cut off by up to 1 / 0.7 of the mean.
 static double score_gain(double steps) { return 1.0 + 0.9 * steps / 33554432.0; }
 static double split_score_gain(const qsvd_dims& d, int kernel) {
   if (kernel == QSVD_KERNEL_SIMT || cache_is_int(d)) return 1.0;   // quantised: integer sums, exact
@@ -526,8 +532,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       e = launch_split_simt_absorbed(d, qt32, cache, scales, sched, G, pm, pl, pz, s, keep);
     if (e != cudaSuccess) return cuda_fail(e, "split phase");
     if (px) {
-      e = d.rope ? launch_prefix_rope(d, X, Wb, x.prefix, x.prefix_scales, P + L.wuk, P + L.wukT, qt32, sms,
-                                      &hdr->status, s)
+      e = d.rope ? launch_prefix_rope(d, X, Wb, x.prefix, x.prefix_scales, P + L.wuk, P + L.wukT, qt32,
+                                      float(1.0 / gain), sms, &hdr->status, s)
                  : launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qparts, qt32,
                                  float(score_gain(prefix_score_steps(d, qparts)) / gain), sms,
                                  reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);

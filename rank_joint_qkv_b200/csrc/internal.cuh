@@ -265,7 +265,8 @@ cudaError_t launch_split_simt_rope(const qsvd_dims& d, const float* qrot,
                                    const void* wuk, const float* rope_tab,
                                    const void* cache, const void* scales,
                                    const int32_t* sched, int G, float* pm,
-                                   float* pl, float* pz, cudaStream_t s, float* keep = nullptr);
+                                   float* pl, float* pz, cudaStream_t s, float* keep = nullptr,
+                                   float gain = 1.f);   // on the scores
 int split_simt_grid_heads(const qsvd_dims& d);   // head blocks per split
 bool split_tc_supported(const qsvd_dims& d);
 // Absorbed mode, the tile's channels spread over a thread-block cluster;

@@ -976,15 +976,16 @@ cudaError_t launch_prefix_table(const qsvd_dims& d, const PrefixLayout& L, uint8
 }
 
 cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                               const void* scales, const void* wuk, const void* wukT, const float* qrot, int sms,
-                               int32_t* status, cudaStream_t s) {
+                               const void* scales, const void* wuk, const void* wukT, const float* qrot,
+                               float simt_gain, int sms, int32_t* status, cudaStream_t s) {
   const float* tab = reinterpret_cast<const float*>(ws + L.tab);
   const int32_t* sched = reinterpret_cast<const int32_t*>(ws + L.sched);
   if (!L.fast) {
     qsvd_dims v = d;   // as in launch_prefix
     v.max_len = 0;
     return launch_split_simt_rope(v, qrot, wuk, tab, prefix, scales, sched, L.G, reinterpret_cast<float*>(ws + L.pm),
-                                  reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz), s);
+                                  reinterpret_cast<float*>(ws + L.pl), reinterpret_cast<float*>(ws + L.pz), s, nullptr,
+                                  simt_gain);
   }
   float* scores = reinterpret_cast<float*>(ws + L.scores);
   const cudaError_t e = launch_rope_scores_shared(d, prefix, L.plen, wukT, reinterpret_cast<const uint32_t*>(ws + L.qpack), tab, sched + 2 * d.batch + 1, sms, scores,

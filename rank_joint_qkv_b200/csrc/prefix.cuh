@@ -37,11 +37,12 @@ cudaError_t launch_prefix(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws
                           cudaStream_t s);
 // Rotary mode: the table of all positions, prefix then own rows (tab, built
 // per call: the packed one ends at max_len), and the partials from the rotated
-// query qrot [B][H][d_h].
+// query qrot [B][H][d_h].  simt_gain: on the scores of the CUDA cores, which
+// truncate nothing (the tensor cores' come about as the own rows' do).
 cudaError_t launch_prefix_table(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
 cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const void* prefix,
-                               const void* scales, const void* wuk, const void* wukT, const float* qrot, int sms,
-                               int32_t* status, cudaStream_t s);
+                               const void* scales, const void* wuk, const void* wukT, const float* qrot,
+                               float simt_gain, int sms, int32_t* status, cudaStream_t s);
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
 // Accumulations that a score of the tensor-core path takes.
 int prefix_score_steps(const qsvd_dims& d, int qparts);

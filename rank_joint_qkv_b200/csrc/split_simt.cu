@@ -239,7 +239,7 @@ k_split_abs(const float* __restrict__ qt32, const uint8_t* __restrict__ cache,
 // Rotary split kernel.  grid (G, H), block 256 = 8 warps.
 // Sub-tile of 16 tokens: warp w owns tokens 2w, 2w+1; lane g owns the
 // rotary pairs (i, i + d_h/2) with i in [g*NP, g*NP + NP), NP = d_h/64 (1 to 4).
-// smem: cs[16][r+1], wk[32][d_h], zs[r].
+// smem: cs[16][r+1], wk[32][d_h], zs[r].  gain: on the scores.
 // ---------------------------------------------------------------------------
 template <qsvd_dtype CT, typename WT, int NP>
 __global__ void __launch_bounds__(kThreads)
@@ -247,7 +247,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
              const float* __restrict__ tab, const uint8_t* __restrict__ cache,
              const __half* __restrict__ scales, const int32_t* __restrict__ sched,
              float* __restrict__ pm, float* __restrict__ pl, float* __restrict__ pz,
-             int B, int H, int d_h, int r, int E, int max_len, int group, int G, float* __restrict__ keep) {
+             int B, int H, int d_h, int r, int E, int max_len, int group, int G, float* __restrict__ keep, float gain) {
   dev::pdl_wait();   // see launch_pdl
   dev::pdl_trigger();
   constexpr int TS = 16;
@@ -353,7 +353,7 @@ k_split_rope(const float* __restrict__ qrot, const WT* __restrict__ wuk,
       }
       __syncthreads();
       if (warp == 0) {
-        const float s = lane < nv ? sc[lane & (TS - 1)] : -INFINITY;
+        const float s = lane < nv ? sc[lane & (TS - 1)] * gain : -INFINITY;
         if (keep && lane < nv) keep[(size_t(b) * H + h) * max_len + s0 + lane] = s;
         const float mx = dev::warp_max(lane < TS ? s : -INFINITY);
         const float m_old = m_s;
@@ -441,7 +441,7 @@ cudaError_t abs_ct(const qsvd_dims& d, const float* qt32, const void* cache, con
 template <qsvd_dtype CT, typename WT, int NP>
 cudaError_t rope_np(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                    const void* cache, const void* scales, const int32_t* sched, int G,
-                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
+                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep, float gain) {
   const size_t smem = (size_t(16) * (d.r + 1) + size_t(32) * d.d_h + d.r) * 4;
   auto kern = k_split_rope<CT, WT, NP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -449,7 +449,7 @@ cudaError_t rope_np(const qsvd_dims& d, const float* qrot, const void* wuk, cons
   dim3 grid(G, d.H);
   {
     const cudaError_t le = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s,
-                                     qrot, static_cast<const WT*>(wuk), tab, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.d_h, d.r, d.E, d.max_len, d.group, G, keep);
+                                     qrot, static_cast<const WT*>(wuk), tab, static_cast<const uint8_t*>(cache), static_cast<const __half*>(scales), sched, pm, pl, pz, d.batch, d.H, d.d_h, d.r, d.E, d.max_len, d.group, G, keep, gain);
     if (le != cudaSuccess) return le;
   }
   note_launch();
@@ -459,12 +459,12 @@ cudaError_t rope_np(const qsvd_dims& d, const float* qrot, const void* wuk, cons
 template <qsvd_dtype CT, typename WT>
 cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                    const void* cache, const void* scales, const int32_t* sched, int G,
-                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
+                   float* pm, float* pl, float* pz, cudaStream_t s, float* keep, float gain) {
   switch (d.d_h) {   // d_h / 64 pairs a lane
-    case 64: return rope_np<CT, WT, 1>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case 128: return rope_np<CT, WT, 2>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case 192: return rope_np<CT, WT, 3>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case 256: return rope_np<CT, WT, 4>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case 64: return rope_np<CT, WT, 1>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case 128: return rope_np<CT, WT, 2>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case 192: return rope_np<CT, WT, 3>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case 256: return rope_np<CT, WT, 4>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -472,11 +472,11 @@ cudaError_t rope_t(const qsvd_dims& d, const float* qrot, const void* wuk, const
 template <qsvd_dtype CT>
 cudaError_t rope_ct(const qsvd_dims& d, const float* qrot, const void* wuk, const float* tab,
                     const void* cache, const void* scales, const int32_t* sched, int G,
-                    float* pm, float* pl, float* pz, cudaStream_t s, float* keep) {
+                    float* pm, float* pl, float* pz, cudaStream_t s, float* keep, float gain) {
   switch (d.weight_dtype) {
-    case QSVD_F32: return rope_t<CT, float>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_F16: return rope_t<CT, __half>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_BF16: return rope_t<CT, __nv_bfloat16>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_F32: return rope_t<CT, float>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_F16: return rope_t<CT, __half>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_BF16: return rope_t<CT, __nv_bfloat16>(d, qrot, wuk, tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -515,13 +515,13 @@ cudaError_t launch_split_simt_scores(const qsvd_dims& d, const float* scores, co
 cudaError_t launch_split_simt_rope(const qsvd_dims& d, const float* qrot, const void* wuk,
                                    const float* rope_tab, const void* cache, const void* scales,
                                    const int32_t* sched, int G, float* pm, float* pl, float* pz,
-                                   cudaStream_t s, float* keep) {
+                                   cudaStream_t s, float* keep, float gain) {
   switch (d.cache_dtype) {
-    case QSVD_F32: return rope_ct<QSVD_F32>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_F16: return rope_ct<QSVD_F16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_BF16: return rope_ct<QSVD_BF16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_I8: return rope_ct<QSVD_I8>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
-    case QSVD_I4: return rope_ct<QSVD_I4>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep);
+    case QSVD_F32: return rope_ct<QSVD_F32>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_F16: return rope_ct<QSVD_F16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_BF16: return rope_ct<QSVD_BF16>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_I8: return rope_ct<QSVD_I8>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
+    case QSVD_I4: return rope_ct<QSVD_I4>(d, qrot, wuk, rope_tab, cache, scales, sched, G, pm, pl, pz, s, keep, gain);
   }
   return cudaErrorInvalidValue;
 }

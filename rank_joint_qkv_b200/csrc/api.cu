@@ -96,7 +96,7 @@ static qsvd_status validate(const qsvd_dims* d) {
   return QSVD_OK;
 }
 
-static int device_sms() {
+int device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;

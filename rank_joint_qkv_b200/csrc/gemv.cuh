@@ -243,14 +243,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }  // namespace gemv_mma
 
 // grid (ceil(N/64), KS = ceil(K/512), z), block 128: a CTA keeps its weight
-// tile and walks the blocks of 16 sequences z apart (64 sequences: one fetch
-// of the tile instead of four).  The KS partials of an output are added in
-// split order and converted to OT by one of three ways:
-//   CLUSTER  KS <= 8: the KS CTAs of a column block are a cluster, each adds a
+// tile and walks the blocks of 16 sequences z apart (gemv_side_by_side).
+// The KS partials of an output are added in split order and converted to OT by
+// one of three ways:
+//   CLUSTER  the KS <= 8 CTAs of a column block are a cluster, each adds a
 //            share of the block over distributed shared memory (KS = 1: writes
 //            its own) -- no partials in global memory, no ticket
-//   TICKET   more: partials part[ks][b][n], and the last CTA of each (column
-//            block, sequence block) to take a ticket adds them
+//   TICKET   partials part[ks][b][n], and the last CTA of each (column block,
+//            sequence block) to take a ticket adds them
 //   PARTIAL  the partials are the result (the caller adds them)
 // Activation row of sequence b for output column n:
 // x + b * xg.row + (n / xg.cols) * xg.step (xg.cols a multiple of 64); the
@@ -536,6 +536,28 @@ k_gemv_mma(const __grid_constant__ CUtensorMap tm_w, const XT* __restrict__ x, X
   }
 }
 
+// How many blocks of 16 sequences k_gemv_mma's grid has side by side (z), of
+// `ctas` CTAs each with room for `slots` at once.  A CTA that walks p blocks
+// fetches its weight tile once, which costs about a third of a block's products;
+// a walk's time counts once for every wave: one wave however full, from two on
+// the last one half; between one and two an SM's second CTA runs alone for long,
+// the more the emptier the second wave.
+// Us of the value up-projection and its merge / the query projection, 32 heads
+// of 128, r 1536 (192 CTAs a block of sequences): 64 sequences, z 1, 2, 4: 38.9,
+// 36.8, 34.6 / 23.3, 22.2, 19.8; 128, z 1, 3, 8: 74.8, 62.2, 64.4 / 44.6, 34.3,
+// 35.2; 256, z 1, 3, 16: 160, 137, 140 / 87, 68, 69.  32 heads, r 768 (128 CTAs):
+// 64 sequences, z 1, 2, 4: 34.3, 23.5, 24.3 / 18.3, 12.6, 13.2.
+inline int gemv_side_by_side(int ctas, int blocks, int slots) {
+  int best = 1;
+  double best_cost = 1e30;
+  for (int p = 1; p <= blocks && p <= 64; ++p) {
+    const int z = (blocks + p - 1) / p;
+    const double w = double(ctas) * z / slots, waves = w <= 1.0 ? 1.0 : w <= 2.0 ? 4.0 - w : w + 0.5;
+    if (waves * (3 * p + 1) < best_cost) { best = z; best_cost = waves * (3 * p + 1); }
+  }
+  return best;
+}
+
 // Launch the GEMV: tensor cores for 16-bit weights, CUDA cores for fp32.
 // Per-group activation rows (xg) and a non-float output need the tensor-core
 // variant (16-bit weights).  pf / pf_bytes: constant bytes the next kernel
@@ -563,7 +585,19 @@ cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-    const bool cluster = ticket != nullptr && KS <= gemv_mma::kMaxClusterK;
+    // Clusters of up to four CTAs but not three fill the SMs whatever the grid;
+    // others leave some empty where the CTAs would just fit or come in waves.  Us
+    // with clusters / with tickets, the up-projection and its merge of 48
+    // sequences: r 768 (KS 2) 21.2 / 20.3, r 1536 (KS 3) 30.9 / 26.8, r 2304 (KS 5)
+    // 54.8 / 52.2; a projection by W_O of 32: E 2048 (KS 4) 5.8 / 7.0, E 3584 (KS 7)
+    // 23.8 / 19.7, E 4096 (KS 8) 27.2 / 23.8.  The query projection runs beside the
+    // schedule only without tickets: r 768, 64 sequences, 12.6 / 17.5, r 1536, 32
+    // (192 CTAs, two blocks each) 11.9 / 13.7.
+    const int cols = (N + gemv_mma::CT - 1) / gemv_mma::CT, blocks = (B + 15) / 16;
+    const int sms = device_sms(), slots = 2 * (sms > 0 ? sms : 148);   // two CTAs fit an SM
+    const int z = gemv_side_by_side(cols * KS, blocks, slots);
+    const bool cluster = ticket != nullptr && KS <= gemv_mma::kMaxClusterK &&
+                         (KS <= 2 || KS == 4 || 4 * cols * KS * z <= 3 * slots);
     auto kern = cluster ? k_gemv_mma<XT, WT, OT, GEMV_CLUSTER, false>
                         : ticket ? k_gemv_mma<XT, WT, OT, GEMV_TICKET, false> : k_gemv_mma<XT, WT, OT, GEMV_PARTIAL, false>;
     if constexpr (std::is_same<WT, __nv_bfloat16>::value && std::is_same<XT, float>::value && std::is_same<OT, float>::value)
@@ -573,11 +607,6 @@ cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
-    // blocks of 16 sequences side by side while the CTAs still fit at once (two
-    // per SM); beyond that a CTA walks several with its weight tile in place
-    const int cols = (N + gemv_mma::CT - 1) / gemv_mma::CT, blocks = (B + 15) / 16;
-    int z = 296 / (cols * KS);
-    z = z < 1 ? 1 : z > blocks ? blocks : z;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(unsigned(cols), unsigned(KS), unsigned(z));

@@ -159,6 +159,7 @@ inline WsLayout ws_layout(const qsvd_dims& d, int G, bool keep_scores = false) {
 void note_launch();                 // counts kernels launched by this library
 qsvd_status set_error(qsvd_status st, const char* msg);   // records qsvd_last_error()
 cudaError_t check_launch();         // cudaGetLastError after a launch
+int device_sms();                   // of the current device; 0 if it cannot be asked
 
 // Programmatic dependent launch.  The decode-step kernels are launched with
 // programmatic stream serialisation, so each may start while the previous

@@ -518,7 +518,7 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
  *   prefix, prefix_scales  device, prefix_len rows (and group scales) as in
  *                  qsvd_append_latent's cache, 16-byte (2-byte) aligned; not
  *                  read when prefix_len is 0.
- *   prefix_len     >= 0, batch x prefix_len < 2^31.
+ *   prefix_len     0 .. 2^31 - 256, batch x prefix_len < 2^31.
  *   cache, scales, lengths, num_splits  the own rows, as in qsvd_decode_attn;
  *                  a sequence with len 0 attends the prefix alone, with
  *                  prefix_len 0 too its output row is zero.

@@ -615,12 +615,12 @@ qsvd_status qsvd_decode_attn_shared(const qsvd_dims* dims, const void* packed, c
   if (st != QSVD_OK) return st;
   const qsvd_dims& d = *dims;
   if (!workspace_bytes) return fail(QSVD_ERR_INVALID_ARG, "workspace_bytes is NULL");
-  // (rows of scores are padded to tiles of 256 tokens, in 32 bits)
-  if (prefix_len < 0 || prefix_len > 0x7FFFFFFF - (kPxTile - 1) || (long long)d.batch * prefix_len > 0x7FFFFFFFLL)
-    return fail(QSVD_ERR_INVALID_ARG,
-                "prefix_len (%d) must be >= 0 and at most 2^31 - 256, batch x prefix_len below 2^31", prefix_len);
+  if (prefix_len < 0 || (long long)d.batch * prefix_len > 0x7FFFFFFFLL)
+    return fail(QSVD_ERR_INVALID_ARG, "prefix_len (%d) must be >= 0 and batch x prefix_len below 2^31", prefix_len);
   if (d.rope && (long long)d.max_len + prefix_len > 0x7FFFFFFFLL)
     return fail(QSVD_ERR_INVALID_ARG, "max_len + prefix_len must be below 2^31");
+  if (prefix_len > 0x7FFFFFFF - (kPxTile - 1))   // rows of scores are padded to tiles of 256 tokens, in 32 bits
+    return fail(QSVD_ERR_INVALID_ARG, "prefix_len (%d) must be at most 2^31 - 256", prefix_len);
   if (workspace && prefix_len > 0) {
     if (!prefix || !aligned16(prefix)) return fail(QSVD_ERR_INVALID_ARG, "prefix must be given, 16-byte aligned");
     if (cache_is_int(d) && (!prefix_scales || !aligned2(prefix_scales)))

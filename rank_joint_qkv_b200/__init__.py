@@ -9,6 +9,7 @@ been built (``python rank_joint_qkv_b200/build.py``): there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -139,6 +140,29 @@ def qsvd_testing_set_score_wait_ns(ns: int) -> None:
     _check(_lib.qsvd_testing_set_score_wait_ns(int(ns)), "qsvd_testing_set_score_wait_ns")
 
 
+@functools.cache
+def _several_devices() -> bool:
+    return torch.cuda.device_count() > 1
+
+
+def _on_the_tensors_device(call):
+    """The call made with its stream's device current, or its first device
+    tensor's: the library launches on the current device, and kernels of one
+    GPU given another's memory fault."""
+    @functools.wraps(call)
+    def on_device(*args, **kwargs):
+        if not _several_devices():
+            return call(*args, **kwargs)
+        device = getattr(kwargs.get("stream"), "device", None)
+        if device is None:
+            device = next((t.device for t in (*args, *kwargs.values()) if getattr(t, "is_cuda", False)), None)
+        if device is None or device.index == torch.cuda.current_device():
+            return call(*args, **kwargs)
+        with torch.cuda.device(device):
+            return call(*args, **kwargs)
+    return on_device
+
+
 def _scratch(n: int, device, stream) -> torch.Tensor:
     """Device bytes for a call on ``stream`` (None: the current one).
 
@@ -160,6 +184,7 @@ def _scratch(n: int, device, stream) -> torch.Tensor:
     return t
 
 
+@_on_the_tensors_device
 def qsvd_prepare_weights(dims: qsvd_dims, wd, wuq, wuk, wuv, h2_q=None, packed=None,
                          stream=None) -> torch.Tensor:
     """Lay out W^d, W^u_q, W^u_k, W^u_v (device tensors) into a packed buffer.
@@ -180,6 +205,7 @@ def qsvd_prepare_weights(dims: qsvd_dims, wd, wuq, wuk, wuv, h2_q=None, packed=N
     return packed
 
 
+@_on_the_tensors_device
 def qsvd_prepare_out_proj(dims: qsvd_dims, wo, packed, stream=None):
     """Add W_O (E x E device tensor, y = o W_O) to a buffer filled by
     qsvd_prepare_weights with the same dims (dims.out_proj chain or fold)."""
@@ -188,6 +214,7 @@ def qsvd_prepare_out_proj(dims: qsvd_dims, wo, packed, stream=None):
            "qsvd_prepare_out_proj")
 
 
+@_on_the_tensors_device
 def qsvd_split_factors(dims: qsvd_dims, u, vt, a, b, wd, wuq, wuk, wuv, stream=None):
     """Fill wd (E x r) and wuq/wuk/wuv (r x E), weight-dtype device tensors,
     with U diag(a) and diag(b) V^T (u: E x r, vt: r x 3E, a, b: r; float32
@@ -205,6 +232,7 @@ def append_workspace_bytes(dims: qsvd_dims) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_append_latent(dims: qsvd_dims, packed, x, pos, cache, scales=None, c_out=None,
                        status=None, workspace=None, stream=None):
     if workspace is None:
@@ -217,6 +245,7 @@ def qsvd_append_latent(dims: qsvd_dims, packed, x, pos, cache, scales=None, c_ou
     return workspace
 
 
+@_on_the_tensors_device
 def qsvd_prefill_latent(dims: qsvd_dims, packed, x, dst_rows, cache, scales=None,
                         c_out=None, status=None, stream=None):
     """Latent rows of x.shape[0] tokens at once, row i stored at cache row
@@ -227,18 +256,21 @@ def qsvd_prefill_latent(dims: qsvd_dims, packed, x, dst_rows, cache, scales=None
            "qsvd_prefill_latent")
 
 
+@_on_the_tensors_device
 def qsvd_beta_exponents(sigma, beta: float, a, b, stream=None) -> None:
     """a = sigma^beta, b = sigma^(1 - beta) (float64 powers), device tensors."""
     _check(_lib.qsvd_beta_exponents(_ptr(sigma), int(sigma.numel()), float(beta), _ptr(a), _ptr(b),
                                     _stream(stream)), "qsvd_beta_exponents")
 
 
+@_on_the_tensors_device
 def qsvd_sq_diff_sum(y, yq, out, stream=None) -> None:
     """out[0] = sum (y - yq)^2 in float64 (device tensors; out float64)."""
     _check(_lib.qsvd_sq_diff_sum(_ptr(y), _ptr(yq), int(y.numel()), _ptr(out), _stream(stream)),
            "qsvd_sq_diff_sum")
 
 
+@_on_the_tensors_device
 def qsvd_prepare_per_head_fold(dims: qsvd_dims, bv, wo, f=None, stream=None) -> torch.Tensor:
     """F = [B_{Vh} W_{O,h}]_h (H r x E) in the weight type; returns F."""
     if f is None:
@@ -256,6 +288,7 @@ def prefill_attention_workspace_bytes(dims: qsvd_dims) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_prefill_attention(dims: qsvd_dims, packed, cache, lengths, out, status, workspace=None,
                            stream=None):
     """Causal attention over the prompts' latent rows (cache rows b * max_len
@@ -270,6 +303,7 @@ def qsvd_prefill_attention(dims: qsvd_dims, packed, cache, lengths, out, status,
     return workspace
 
 
+@_on_the_tensors_device
 def qsvd_append_latent_static(dims: qsvd_dims, packed, x, pos, cache, scales=None,
                               c_out=None, status=None, stream=None):
     """qsvd_append_latent for callers that cannot allocate: no workspace, the
@@ -288,6 +322,7 @@ def decode_workspace_bytes(dims: qsvd_dims, num_splits: int = 0) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_decode_attn(dims: qsvd_dims, packed, qin, qin_is_latent, cache, scales, lengths,
                      out, num_splits=0, workspace=None, phases=0, stream=None):
     if workspace is None:
@@ -309,6 +344,7 @@ def per_head_workspace_bytes(dims: qsvd_dims) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_decode_attn_per_head(dims: qsvd_dims, bk, bv, q, ck, cv, lengths, out, workspace=None,
                               layout=QSVD_PER_HEAD_HEAD_MAJOR, stream=None):
     """Decode over per-head key/value latents (ck, cv: B x H x max_len x r,
@@ -325,6 +361,7 @@ def qsvd_decode_attn_per_head(dims: qsvd_dims, bk, bv, q, ck, cv, lengths, out, 
     return workspace
 
 
+@_on_the_tensors_device
 def qsvd_combine_splits(dims: qsvd_dims, packed, workspace, num_splits, lengths, out,
                         stream=None):
     _check(_lib.qsvd_combine_splits(ctypes.byref(dims), _ptr(packed), _ptr(workspace),
@@ -340,6 +377,7 @@ def decode_weights_workspace_bytes(dims: qsvd_dims, num_splits: int = 0) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_decode_attn_weights(dims: qsvd_dims, packed, qin, qin_is_latent, cache, scales, lengths, out, weights,
                              accumulate=True, num_splits=0, workspace=None, stream=None):
     """qsvd_decode_attn that also gives each cache row's attention weight,
@@ -364,6 +402,7 @@ def decode_shared_workspace_bytes(dims: qsvd_dims, prefix_len: int, num_splits: 
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_decode_attn_shared(dims: qsvd_dims, packed, qin, qin_is_latent, prefix, prefix_scales, prefix_len, cache,
                             scales, lengths, out, weights=None, accumulate=True, num_splits=0, workspace=None,
                             stream=None):
@@ -391,6 +430,7 @@ def evict_workspace_bytes(dims: qsvd_dims, budget: int) -> int:
     return n.value
 
 
+@_on_the_tensors_device
 def qsvd_evict_rows(dims: qsvd_dims, weights, lengths, budget, cache, scales=None, *, sink=0, recent=0,
                     dst_max_len=None, dst_cache=None, dst_scales=None, dst_weights=None, dst_lengths=None, kept=None,
                     status=None, workspace=None, stream=None):
@@ -400,9 +440,11 @@ def qsvd_evict_rows(dims: qsvd_dims, weights, lengths, budget, cache, scales=Non
     cut is in place: cache, scales, weights and lengths are all updated.
     With it (B x dst_max_len rows; dst_scales beside int caches) the sources
     are left alone; dst_weights (B x dst_max_len) is optional, dst_lengths
-    is not.  ``kept``: optional B x budget int32, the kept rows' sources.
+    is not; dst_max_len and dst_scales go with it.  ``kept``: optional B x budget int32, the kept rows' sources.
     Returns the workspace."""
     if dst_cache is None:
+        if dst_scales is not None or dst_max_len not in (None, dims.max_len):
+            raise ValueError("qsvd_evict_rows: dst_scales and dst_max_len need dst_cache (without it the cut is in place)")
         dst_cache, dst_scales, dst_max_len = cache, scales, dims.max_len
         dst_weights = weights if dst_weights is None else dst_weights
         dst_lengths = lengths if dst_lengths is None else dst_lengths

@@ -41,7 +41,13 @@ def test_a_call_runs_on_its_tensors_device(device):
 
 def test_every_call_is_made_that_way():
     calls = [n for n in q._sigs if n != "qsvd_testing_set_score_wait_ns"]
-    assert all(hasattr(getattr(q, n), "__wrapped__") for n in calls)
+    assert all(getattr(q, n).on_the_tensors_device for n in calls)
+
+
+def test_one_gpu_needs_no_choice(monkeypatch):
+    monkeypatch.setattr(q, "_several_devices", lambda: False)
+    call = lambda: None  # noqa: E731
+    assert q._on_the_tensors_device(call) is call
 
 
 def test_an_error_leaves_the_current_device(device):

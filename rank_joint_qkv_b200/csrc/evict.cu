@@ -455,7 +455,8 @@ cudaError_t launch_evict(const qsvd_dims& d, const float* weights, const int32_t
   long long walkers;
   if (in_place) {
     // slices of 512 bytes, narrower ones where those are too few for the SMs, down to a sector of 32
-    for (ws = 5; ws > 1 && (long long)((a.vecs + (1 << ws) - 1) >> ws) * d.batch < 148; --ws) {}
+    const int sms = device_sms();
+    for (ws = 5; ws > 1 && (long long)((a.vecs + (1 << ws) - 1) >> ws) * d.batch < sms; --ws) {}
     walkers = (a.vecs + (1 << ws) - 1) >> ws;
   } else {
     walkers = ((long long)budget * a.vecs + kMvThreads * kMvUnroll - 1) / (kMvThreads * kMvUnroll);

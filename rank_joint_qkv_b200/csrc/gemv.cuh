@@ -563,6 +563,8 @@ inline int gemv_side_by_side(int ctas, int blocks, int slots) {
 // variant (16-bit weights).  pf / pf_bytes: constant bytes the next kernel
 // reads (its weights), requested into L2 while this one runs (tensor-core
 // variant; a hint only).  third: see k_gemv_mma (bf16 weights, fp32 output).
+// late: the kernel needs nothing of its predecessor in the stream and may run
+// beside it (see launch_pdl).
 template <typename XT, typename WT, typename OT = float>
 cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int N, int KS,
                         OT* out, int32_t* ticket, int32_t* status, cudaStream_t s,
@@ -622,8 +624,18 @@ cudaError_t launch_gemv(const XT* x, const WT* W, float* part, int B, int K, int
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster && KS > 1 ? 2 : 1;
+    // Beside its predecessor it hides the schedule, but its successor starts only
+    // when it ends.  That pays where the successor's own loads are short (few CTAs
+    // here) and where several blocks of sequences fill the GPU, which an early
+    // successor would share.  In between, the absorption's weights load beside the
+    // projection instead, and the split kernel behind a late one took up to 12%
+    // longer on most GPUs.  Us of a decode step, late / not: r 256, E 256 (4 CTAs)
+    // 25.8 / 27.4; E 4096, 16 sequences: r 768 (128 CTAs) 66.7 / 58.1, r 1536 (192;
+    // 8192 rows) 139.8 / 128.9; r 768, 64 sequences (256 CTAs) 96.3 / 99.3.
+    const int ctas = cols * KS * z;
+    const bool beside = late && cluster && (ctas < 32 || (blocks > 1 && 4 * ctas >= 3 * slots));
     e = cudaLaunchKernelEx(&cfg, kern, tm, x, xg, part, B, K, N, KS, out, ticket, status,
-                           static_cast<const uint8_t*>(pf), (unsigned long long)pf_bytes, int(late && cluster));
+                           static_cast<const uint8_t*>(pf), (unsigned long long)pf_bytes, int(beside));
     if (e != cudaSuccess) return e;
   } else {
     static_assert(std::is_same<OT, float>::value, "CUDA-core GEMV writes fp32");

@@ -176,6 +176,11 @@ int device_sms();                   // of the current device; 0 if it cannot be 
 // started once every CTA of the predecessor had passed its own wait, so what
 // came before the predecessor is complete and visible, and it runs beside the
 // predecessor; the wait at its end keeps the chain ordered for what follows.
+// That needs a predecessor that waits before it triggers.  k_rope_table triggers
+// first: behind it only what came two kernels before *it* is complete at a
+// kernel's start.  It stands behind k_prefix_schedule, which waits first, so that
+// is all but k_prefix_schedule, and the query GEMV behind it needs neither.
+// Nothing else may be put between those three.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {

@@ -485,7 +485,7 @@ k_schedule(const int32_t* __restrict__ lengths, int B, int max_len, int G,
 template <typename WT>
 cudaError_t q_partial_t(const qsvd_dims& d, const float* qin, const void* wuq, float* qpart,
                         int KS, float* q, int32_t* tickets, int32_t* status, bool third, cudaStream_t s) {
-  // beside the schedule before it, of which it needs nothing where it takes no tickets
+  // (late: it needs nothing of the schedule before it where it takes no tickets)
   return launch_gemv<float, WT>(qin, static_cast<const WT*>(wuq), qpart, d.batch, d.r, d.E, KS, q,
                                 tickets, status, s, XGroups{0, 0, 0}, nullptr, 0, true, third);
 }

@@ -390,3 +390,16 @@ def test_a_quantised_prefix_takes_a_query_of_any_size(cuda_ok, cache, kernel, si
     want = p * (values[0] @ wuv[:, 1])
     bar = (lim + 2.0 ** -11) * want.abs() + 2.0 ** -14 * (p * (values[0].abs() @ wuv[:, 1].abs()))
     assert bool(((out[:, 1].double().cpu() - want).abs() <= bar).all())
+
+
+@pytest.mark.parametrize("form", [dict(H=8, r=512, lens=(0, 257, 40)), dict(H=20, r=1024, lens=(130, 1)),
+                                  dict(H=32, d_h=128, r=2048, lens=(3, 300), kernel=q.QSVD_KERNEL_AUTO)],
+                         ids=["4-ctas", "4-ctas-20-heads", "auto"])
+def test_bf16_own_rows_on_clusters(cuda_ok, form):
+    """Own rows on the cluster kernel and the prefix's products, both from three parts of the query, and from two without weights."""
+    m = Layer(**dict(dict(cache="bf16", weight="bf16", prefix=700, kernel=q.QSVD_KERNEL_TCGEN05_CLUSTER), **form))
+    want, want_w, bound = m.exact()
+    w = torch.zeros(m.B, m.max_len, device=DEV)
+    close_out(m, run(m, weights=w), want)
+    close_weights(w, want_w, 3 * bound, m.lens)
+    close_out(m, run(m), want)

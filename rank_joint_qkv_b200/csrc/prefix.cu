@@ -914,10 +914,12 @@ PrefixLayout prefix_layout(const qsvd_dims& d, int plen, int sms, size_t base) {
     // token splits of the value product: the fewest that come within 3% of
     // the best fill of the GPU's waves (a split costs B H r float32 partials,
     // written and merged)
-    // pairs once the scores take more than a wave of single CTAs: at B 64, H 32,
-    // P 16384 (1024 tiles) the step took 395 us without and 377 us with; at
-    // B 16, P 8192 (128 tiles) 128 and 130 us
-    L.pair = L.MB > 1 && (long long)L.MB * L.tiles > sms;
+    // pairs once the scores take more than two waves of single CTAs (H 32, r 1536,
+    // fp16, step without / with pairs, us): B 16, P 12,000 (188 tiles) 101.5 /
+    // 110.8; B 32, P 8192 (256) 146 / 150; B 64, P 4096 (256) 196 / 198, P 6144
+    // (384) 220.5 / 217.7, P 8192 (512) 247 / 241, P 16,384 (1024) 407 / 391; int8,
+    // r 768, B 64: P 8192 197 / 191, P 16,384 287 / 267
+    L.pair = L.MB > 1 && (long long)L.MB * L.tiles > 2LL * sms;
     const int W = L.pair ? 2 : 1;   // CTAs per unit
     const long long units = (long long)((L.MB + W - 1) / W) * ((d.r + 255) / 256), walkers = sms / W > 0 ? sms / W : 1;
     double best = 1e30;

@@ -403,3 +403,26 @@ def test_bf16_own_rows_on_clusters(cuda_ok, form):
     close_out(m, run(m, weights=w), want)
     close_weights(w, want_w, 3 * bound, m.lens)
     close_out(m, run(m), want)
+
+
+PAIRS = {   # more than two waves of score tiles: blocks of query rows x tiles of 256 tokens > 296
+    "f16-5-blocks": dict(prefix=15800, lens=(3, 0, 130) * 6, H=32, r=128),   # the last pair's second CTA has no rows
+    "f16-2-blocks": dict(prefix=38000, lens=(5, 9), H=100, r=64),
+    "f16-heads-6": dict(prefix=26001, lens=(2,) * 50, H=6, r=192),
+    "bf16": dict(cache="bf16", weight="bf16", out="bf16", prefix=19001, lens=(1,) * 16, H=32, r=192),
+    "i8": dict(cache="i8", prefix=19999, lens=(20,) * 16, H=32, r=256),
+    "i4": dict(cache="i4", prefix=25600, lens=(0, 7, 20) * 3, H=32, r=128),
+    "rope": dict(prefix=15900, lens=(3, 0, 130) * 6, H=32, d_h=128, r=128, rope=True),
+}
+
+
+@pytest.mark.parametrize("name", list(PAIRS))
+def test_cta_pairs_against_the_definition(cuda_ok, name):
+    form = PAIRS[name]
+    m = Layer(**form)
+    tiles, blocks = -(-form["prefix"] // 256), -(-m.B // min(m.B, 128 // m.H))
+    assert blocks > 1 and tiles * blocks > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    want, want_w, bound = m.exact()
+    w = torch.zeros(m.B, m.max_len, device=DEV)
+    close_out(m, run(m, weights=w), want)
+    close_weights(w, want_w, 3 * bound, m.lens)

@@ -483,7 +483,7 @@ qsvd_status qsvd_prepare_per_head_fold(const qsvd_dims* dims, const void* bv, co
  * bf16 parts instead of two, and on the tensor cores the query is scaled up by
  * what their truncating accumulation takes off the scores of dense rows, about
  * g = 0.9 r / 16 x 2^-25 (2.6e-6 at r 1536; F16 and BF16 rows) and some 1e-7 for
- * the projections.  With it such scores are right on the mean to about g / 10;
+ * the projections.  With it such scores are right on the mean to 2e-7;
  * a score of few non-zero terms comes out up to g too large.
  * Serving decode; the pages have no counterpart.
  *   weights    device, B x max_len float32, 4-byte aligned.
@@ -531,8 +531,9 @@ qsvd_status qsvd_decode_attn_weights(const qsvd_dims* dims, const void* packed, 
  *   out            device, B x E, out_dtype (B x E projected with
  *                  dims->out_proj).
  * Scores carry the gain of qsvd_decode_attn_weights, with and without weights.
- * Made for many sequences: with one or two the decode over whole rows is faster
- * (B 1, 8192 + 512 rows, rotary: 156 us against 198).
+ * Made for several sequences: with one the decode over whole rows is faster
+ * (8192 + 512 rows: 77 us against 81, rotary 130 against 157; with two 94 against
+ * 83, rotary 215 against 160).
  * The prefix runs on the tensor cores for F16, BF16, I8 and I4 caches with
  * r % 64 == 0, H <= 128 and dims->kernel other than SIMT, and on the CUDA cores
  * otherwise; with dims->rope for cache and weights both F16 or both BF16 with

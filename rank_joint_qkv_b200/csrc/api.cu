@@ -157,34 +157,40 @@ static float score_scale_log2(const qsvd_dims& d) {
 }
 
 // The tensor cores add into their float32 accumulator by truncation: each of
-// a sum's `steps` accumulations loses half a unit in the last place on
-// average, 0.5 x 2^-23 of a mantissa that averages 1 / 0.72, while the partial
-// sum is on average 0.6 to 0.8 of the final one -- about 0.9 x 2^-25 of the sum a
-// step on tcgen05 and 0.7 x 2^-25 in the projections' chains of mma.sync.
-// Scores come out short by the sum of these, a slightly higher softmax
-// temperature that 16-bit outputs do not show but float32 attention weights do;
-// the serving calls scale the query up by it (decode over a shared prefix with
-// or without weights, so that both give the same output).  Measured as the
-// slope of the weights' log error over their log, one head, 2500 and 3000 rows:
-// without it -3.3e-6 at fp16, r 1536 (96 steps, and 16 of each projection);
-// with the scores' steps alone at 2^-25, -2e-7 to -7e-7 (int8 rows, whose sums
-// are exact: -7e-7, the projections' share).  Fitted over 13 forms (every split
-// kernel, r 1472 to 2560, own rows and prefixes): -5e-7 to -8.6e-6 without the
-// gain, each within 4% of these formulas, or 2e-7 of them; -2e-7 to 4e-7 with it.
-// It is a mean over dense rows, whose sums keep growing: a score of few terms is cut off fewer times and comes out
-// too large by up to the gain (2.6e-6 of itself at r 1536), one whose first terms
-// make most of it is cut off by up to 1 / 0.7 of the mean.
-static double score_gain(double steps) { return 1.0 + 0.9 * steps / 33554432.0; }
+// a sum's accumulations loses half a unit in the last place on average, 0.5 x
+// 2^-23 of a mantissa that averages 1 / 0.72, while the partial sum is on
+// average 0.6 to 0.8 of the final one -- about 0.9 x 2^-25 of the sum a step on
+// tcgen05 (0.85 of bf16's products, 0.825 with all the query's parts in one sum)
+// and 0.7 x 2^-25 in the projections' chains of mma.sync; a part that is
+// multiplied behind the others finds the sum at its full size, 0.86 to 1.04 x
+// 2^-25 a step.  Scores come out short by the sum of these, a slightly higher
+// softmax temperature that 16-bit outputs do not show but float32 attention
+// weights do; the serving calls scale the query up by it (decode over a shared
+// prefix with or without weights, so that both give the same output).
+// Fitted from the weights' errors over 40 forms (every split kernel, row and
+// weight type, r 256 to 2560, own rows and prefixes): without the gain -5e-7 to
+// -8.6e-6 of a score; with it, over five inputs each, within 1.6e-7.
+// It is a mean over dense rows, whose sums keep growing: a score of few terms is
+// cut off fewer times and comes out too large by up to the gain (2.6e-6 of itself
+// at r 1536), one whose first terms make most of it is cut off by up to 1 / 0.7 of
+// the mean.
+constexpr double kCut = 1.0 / 33554432.0;   // 2^-25
 static double split_score_gain(const qsvd_dims& d, int kernel) {
   if (kernel == QSVD_KERNEL_SIMT || cache_is_int(d)) return 1.0;   // quantised: integer sums, exact
-  return score_gain(kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) / 16.0 : d.r / 16.0);
+  const double steps = (kernel == QSVD_KERNEL_TCGEN05_CLUSTER ? split_cl_channels(d) : d.r) / 16.0;
+  return 1.0 + (d.cache_dtype == QSVD_BF16 ? 0.85 : 0.9) * steps * kCut;
 }
-static double projection_gain(const qsvd_dims& d, int qin_is_latent) {
+static double prefix_score_gain(const qsvd_dims& d, int qparts) {
+  const double steps = d.r / 16.0 * kCut;
+  if (d.cache_dtype == QSVD_BF16) return 1.0 + 0.825 * qparts * steps;
+  return 1.0 + 0.9 * 2 * steps + (cache_is_int(d) ? 1.04 * steps : 0.0);   // int: the rows' lo parts in a pass of their own
+}
+static double projection_gain(const qsvd_dims& d, int qin_is_latent, bool third) {
   if (d.weight_dtype == QSVD_F32) return 1.0;   // CUDA cores, rounded sums
-  double steps = 0.0;   // of 16, on two parts of the activation (a third one of bf16's adds next to nothing)
+  double steps = 0.0;   // of 16, for each part of the activation
   if (qin_is_latent) steps += (std::min(32, (d.r + 15) / 16) + 3) / 4;   // 512 rows over four warps
   if (!d.rope && d.d_h % 64 == 0 && d.d_h <= 256) steps += d.d_h / 16;
-  return 1.0 + 0.7 * 2 * steps / 33554432.0;
+  return 1.0 + (0.7 * 2 + (third && d.weight_dtype == QSVD_BF16 ? 0.86 : 0.0)) * steps * kCut;
 }
 
 }  // namespace qsvd
@@ -457,7 +463,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   const float* own_tab = rope_tab + (px && d.rope ? size_t(x.prefix_len) * d.d_h : 0);
   const double gain = x.on ? split_score_gain(d, kernel) : 1.0;
   const float sl2 = float(double(score_scale_log2(d)) * gain *
-                          (x.on ? projection_gain(d, qin_is_latent) : 1.0));
+                          (x.on ? projection_gain(d, qin_is_latent, x.weights != nullptr) : 1.0));
   float* scores = reinterpret_cast<float*>(Wb + W.scores);
   float* keep = x.weights ? scores : nullptr;
   const bool third = x.weights != nullptr;   // see launch_absorb
@@ -535,7 +541,7 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
       e = d.rope ? launch_prefix_rope(d, X, Wb, x.prefix, x.prefix_scales, P + L.wuk, P + L.wukT, qt32,
                                       float(1.0 / gain), sms, &hdr->status, s)
                  : launch_prefix(d, X, Wb, x.prefix, x.prefix_scales, px16, qparts, qt32,
-                                 float(score_gain(prefix_score_steps(d, qparts)) / gain), sms,
+                                 float(prefix_score_gain(d, qparts) / gain), sms,
                                  reinterpret_cast<int32_t*>(Wb + W.tickets) + W.NT, &hdr->status, s);
       if (e != cudaSuccess) return cuda_fail(e, "prefix");
     }

@@ -1010,8 +1010,6 @@ cudaError_t launch_prefix_expand(const qsvd_dims& d, const PrefixLayout& L, uint
   return check_launch();
 }
 
-int prefix_score_steps(const qsvd_dims& d, int qparts) { return d.r / 16 * (cache_is_int(d) ? 3 : qparts); }
-
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s) {
   cudaError_t e = launch_pdl(k_prefix_schedule, dim3(1), dim3(256), 0, s, reinterpret_cast<int32_t*>(ws + L.sched),
                              reinterpret_cast<int32_t*>(ws + L.csched), reinterpret_cast<WsHeader*>(ws + L.hdr), d.batch,

@@ -44,8 +44,6 @@ cudaError_t launch_prefix_rope(const qsvd_dims& d, const PrefixLayout& L, uint8_
                                const void* scales, const void* wuk, const void* wukT, const float* qrot,
                                float simt_gain, int sms, int32_t* status, cudaStream_t s);
 cudaError_t launch_prefix_schedule(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, cudaStream_t s);
-// Accumulations that a score of the tensor-core path takes.
-int prefix_score_steps(const qsvd_dims& d, int qparts);
 // Merge of the own splits' and the prefix's partials: zm [B][H][r], or (slots
 // != 0) one slot per sequence for launch_combine; ml {M, 1 / L} [B][H].
 cudaError_t launch_merge_shared(const qsvd_dims& d, const PrefixLayout& L, uint8_t* ws, const WsHeader* hdr, int G,

@@ -103,3 +103,30 @@ def test_a_score_of_few_terms_is_at_most_the_gain_too_large(cuda_ok):
     off = (got[:, 1:] / got[:, :1]).log() - scores[:, 1:]
     lim = ((0.9 * 96 + 1.4 * 4) * 2.0 ** -25 + 2.0 ** -22 + 3 * 2.0 ** -23) * scores[:, 1:] + 2.0 ** -20
     assert float((off.abs() / lim).max()) <= 1.0
+
+
+# bf16 weights take a third part of the activations, an int8 prefix a second pass over its rows, both behind the others
+LATER_PARTS = {"bf16": dict(cache="bf16", weight="bf16", r=512), "bf16-r256": dict(cache="bf16", weight="bf16", r=256),
+               "f16-rows": dict(weight="bf16", r=512), "i8": dict(cache="i8", weight="bf16", r=1536),
+               "i8-prefix": dict(cache="i8", r=1536, prefix=900), "bf16-prefix": dict(cache="bf16", weight="bf16", r=1536, prefix=900)}
+
+
+@pytest.mark.parametrize("name", list(LATER_PARTS))
+def test_parts_that_are_multiplied_behind_others(cuda_ok, name):
+    """Accumulations onto a sum of its full size lose more.  Left out they are 8 and 8 (the projections') x 0.86 x 2^-25 =
+    4.1e-7, or 96 x 0.14 x 2^-25 = 4e-7 of an int8 prefix; the mean of five inputs, each known to 1.4e-7 or better (the
+    spread of the fits), has to be within 2^-22 = 2.4e-7."""
+    off = []
+    for seed in range(5):
+        m = Layer(seed=seed, H=4, d_h=128, lens=(600, 400, 60), **LATER_PARTS[name])
+        P = m.prefix_values.shape[0]
+        w, out = torch.zeros(m.B, m.max_len, device=DEV), m.empty_out()
+        q.qsvd_decode_attn_shared(m.dims, m.packed, m.qin, True, m.prefix, m.prefix_scales, P, m.cache, m.scales, m.lengths,
+                                  out, weights=w, accumulate=False)
+        w_, cx, cy = shares(m).unbind(1)
+        got = torch.cat([w[b, :n].double() for b, n in enumerate(m.lens)])
+        cols = torch.stack([cx, cy] if P else [cx], 1) / w_[:, None]
+        off.append(torch.linalg.lstsq(cols.cpu(), ((got - w_) / w_)[:, None].cpu()).solution[:, 0])
+    off = torch.stack(off).mean(0)
+    print(name, off.tolist())
+    assert float(off.abs().max()) <= 2.0 ** -22

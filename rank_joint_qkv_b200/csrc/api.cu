@@ -471,8 +471,8 @@ static qsvd_status decode_impl(const qsvd_dims& d, const void* packed, const flo
   // are asked for (two carry 16 bits: weights off by 2e-6 to 6e-6 of
   // themselves, with three by 1e-6 or so).  What it costs, r 1536, 32 heads:
   // nothing on the own rows (B 16, 8192 of them: 178 and 179 us), on a prefix
-  // half of the scores' products again (B 16, 8192 + 512 rows: 116 -> 138 us;
-  // B 64, 16,384 + 512: 424 -> 484).
+  // half of the scores' products again (with the weights themselves, B 16, 8192 +
+  // 512 rows: 103 -> 133 us; B 64, 16,384 + 512: 386 -> 515).
   const int qparts = third && d.cache_dtype == QSVD_BF16 ? 3 : 2;
   void* px16 = cache_is_int(d) ? static_cast<void*>(Wb + X.qt16) : qt16;   // the prefix's 16-bit query parts
   cudaError_t e;

@@ -16,10 +16,16 @@
 //                   keys in registers across the steps and add up the
 //                   histograms over distributed shared memory (one CTA for
 //                   60,001 rows: 98 us; eight: 22 us).
-//   k_evict_move    the rows' bytes, scales and weights: bound by HBM, each
-//                   kept row read and written once (16 x 8192 rows of 3 KB to
-//                   half: 66 us, 6.1 TB/s, 0.93 of a copy's rate; in place, in
-//                   order, 4.6 TB/s)
+//   k_evict_move    the rows' bytes, scales and weights, each kept row read and
+//                   written once.  16-bit rows of a batch are bound by HBM (16
+//                   x 8192 rows of 3 KB to half: 66 us, 6.1 TB/s, 0.93 of a
+//                   copy's rate; in place, in order, 4.6 TB/s).  A quantised
+//                   cache's scales, like the weights, are moved by one CTA a
+//                   sequence in dependent rounds (move_small), which bounds
+//                   long sequences: whole calls, to half, into other memory /
+//                   in place, us: 16 x 8192 rows int8 r 768 60 / 50, int4 r 1536
+//                   81 / 83; one of 60,001 rows 155 / 204 and 252 / 343 (fp16 r
+//                   1536: 62 / 91)
 //
 // In place the move has an order to keep: row j of the result is row
 // src[j] >= j of the source, src increasing.  A CTA owns a column slice of a

@@ -217,3 +217,22 @@ def test_bf16_rows_see_more_of_the_query_on_every_kernel(cuda_ok, kernel, H, r, 
     two = bf(qt) + bf(qt - bf(qt))
     miss = ((two - qt) @ rows.t()) * 0.6931471805599453
     assert float((miss[:, 1:].abs() / lim[:, 1:]).max()) > 1.5
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("form", [dict(H=32, r=2048), dict(H=20, r=1792), dict(H=12, r=1024), dict(H=32, r=512)],
+                         ids=["8-ctas-one-buffer", "7-ctas-one-buffer", "4-ctas", "2-ctas-one-buffer"])
+def test_clusters_that_walk_many_tiles(cuda_ok, form, splits):
+    """The exchange buffers of the cluster kernel used over and over, one of them or two, from one cluster to all that fit."""
+    m = Layer(cache="bf16", weight="bf16", d_h=64, lens=(2500, 0, 1300, 128), kernel=C, seed=8, **form)
+    want, want_w, bound = m.exact()
+    w, out = torch.zeros(m.B, m.max_len, device=DEV), m.empty_out()
+    ws = q.qsvd_decode_attn_weights(m.dims, m.packed, m.qin, True, m.cache, None, m.lengths, out, w, accumulate=False,
+                                    num_splits=splits)
+    torch.cuda.synchronize()
+    assert q.status_word(ws) == 0
+    assert rel_err(out, want) <= 2e-3
+    close_weights(w, want_w, bound, m.lens)
+    plain = m.empty_out()
+    q.qsvd_decode_attn(m.dims, m.packed, m.qin, True, m.cache, None, m.lengths, plain, num_splits=splits)
+    assert rel_err(out, plain) <= 2e-3
